@@ -1,7 +1,8 @@
 """ctypes binding of ``libnvfp4_gemv.so`` (argument marshalling only).
 
-Each C entry point of ``include/nvfp4_gemv.h``, ``include/nvfp4_quantize.h``
-and ``include/nvfp4_mma.h`` has a Python function of the same name.  Pointer arguments accept a torch tensor (its ``data_ptr()``), a raw
+Each C entry point of ``include/nvfp4_gemv.h``, ``include/nvfp4_quantize.h``,
+``include/nvfp4_mma.h`` and ``include/nvfp4_ffn.h`` has a Python function of
+the same name.  Pointer arguments accept a torch tensor (its ``data_ptr()``), a raw
 integer device address, or None where the C side allows NULL; ``stream``
 accepts None (torch's current stream), a ``torch.cuda.Stream`` or a raw
 ``hipStream_t`` integer.  A negative status raises :class:`Nvfp4GemvError`.
@@ -32,6 +33,20 @@ NVFP4_ROUND_NEAREST_LOWER = 2
 
 NVFP4_OUT_F16 = 0
 NVFP4_OUT_BF16 = 1
+NVFP4_OUT_F32 = 2
+
+NVFP4_W_ROW_MAJOR = 0
+NVFP4_W_PACKED = 1
+
+NVFP4_ACT_NONE = 0
+NVFP4_ACT_RELU = 1
+NVFP4_ACT_GELU = 2
+NVFP4_ACT_GELU_TANH = 3
+NVFP4_ACT_SILU = 4
+NVFP4_ACT_GATED = 16
+
+NVFP4_SCORE_SOFTMAX = 0
+NVFP4_SCORE_SIGMOID = 1
 
 NVFP4_MMA_FORM_MATRIX_CORES = 0
 NVFP4_MMA_FORM_VALU_TILES = 1
@@ -74,6 +89,12 @@ EXPORTED = (
     "nvfp4_mma_pack_weight",
     "nvfp4_gemm_smalln_launch_packed",
     "nvfp4_grouped_gemv_launch_packed",
+    "nvfp4_linear_workspace_size",
+    "nvfp4_linear_launch_ws",
+    "nvfp4_linear_launch",
+    "nvfp4_moe_layer_workspace_size",
+    "nvfp4_moe_layer_launch_ws",
+    "nvfp4_moe_layer_launch",
 )
 
 
@@ -100,6 +121,18 @@ class MmaTuning(ctypes.Structure):
     def __repr__(self):
         return (f"MmaTuning(path={self.path}, variant={self.variant}, ksplit={self.ksplit}, "
                 f"rows_per_block={self.rows_per_block})")
+
+
+class MoeLayerStruct(ctypes.Structure):
+    """Mirror of ``nvfp4_moe_layer_t``."""
+    _fields_ = [("router", ctypes.c_void_p), ("route_bias", ctypes.c_void_p),
+                ("W13", ctypes.c_void_p), ("sf13", ctypes.c_void_p), ("alpha13", ctypes.c_void_p),
+                ("W2", ctypes.c_void_p), ("sf2", ctypes.c_void_p), ("alpha2", ctypes.c_void_p),
+                ("experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64),
+                ("topk", ctypes.c_int32), ("x_type", ctypes.c_int32), ("w_layout", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("scoring", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("routed_scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -182,6 +215,21 @@ def load():
     lib.nvfp4_gemm_smalln_launch_packed.argtypes = smalln_args + [ctypes.POINTER(MmaTuning), _P]
     lib.nvfp4_grouped_gemv_launch_packed.restype = ctypes.c_int
     lib.nvfp4_grouped_gemv_launch_packed.argtypes = grouped_args + [ctypes.POINTER(MmaTuning), _P]
+    I32 = ctypes.c_int32
+    linear_args = [_P, I32, _I64, _P, _P, I32, _P, _P, _P, _I64, _P, I32, _I64, _I64, _I64, _I64, I32]
+    lib.nvfp4_linear_workspace_size.restype = ctypes.c_size_t
+    lib.nvfp4_linear_workspace_size.argtypes = [_I64, _I64, _I64, I32]
+    lib.nvfp4_linear_launch_ws.restype = ctypes.c_int
+    lib.nvfp4_linear_launch_ws.argtypes = linear_args + [_P, ctypes.c_size_t, _P]
+    lib.nvfp4_linear_launch.restype = ctypes.c_int
+    lib.nvfp4_linear_launch.argtypes = linear_args + [_P]
+    moe_args = [ctypes.POINTER(MoeLayerStruct), _P, _I64, _P, _I64, _P, I32, _I64, _I64]
+    lib.nvfp4_moe_layer_workspace_size.restype = ctypes.c_size_t
+    lib.nvfp4_moe_layer_workspace_size.argtypes = [ctypes.POINTER(MoeLayerStruct), _I64]
+    lib.nvfp4_moe_layer_launch_ws.restype = ctypes.c_int
+    lib.nvfp4_moe_layer_launch_ws.argtypes = moe_args + [_P, ctypes.c_size_t, _P]
+    lib.nvfp4_moe_layer_launch.restype = ctypes.c_int
+    lib.nvfp4_moe_layer_launch.argtypes = moe_args + [_P]
     _lib = lib
     return lib
 
@@ -498,3 +546,205 @@ def pack_weight(W, sW, stream=None):
     scales = torch.empty(sb, dtype=torch.uint8, device=W.device)
     nvfp4_mma_pack_weight(W, sW, groups, rows, k, codes, scales, stream)
     return codes, scales
+
+
+# ---- feed-forward operators (include/nvfp4_ffn.h)
+
+def nvfp4_linear_workspace_size(n, m, k, activation=NVFP4_ACT_NONE) -> int:
+    return int(load().nvfp4_linear_workspace_size(n, m, k, int(activation)))
+
+
+def nvfp4_linear_launch_ws(X, x_type, ldx, W, sfW, w_layout, alpha, bias, residual, ldr, Y, y_type,
+                           ldy, n, m, k, activation, workspace, workspace_bytes, stream=None):
+    _check(load().nvfp4_linear_launch_ws(_ptr(X), x_type, ldx, _ptr(W), _ptr(sfW), w_layout,
+                                         _ptr(alpha), _ptr(bias), _ptr(residual), ldr, _ptr(Y), y_type,
+                                         ldy, n, m, k, activation, _ptr(workspace),
+                                         int(workspace_bytes), _stream(stream)),
+           "nvfp4_linear_launch_ws")
+
+
+def nvfp4_linear_launch(X, x_type, ldx, W, sfW, w_layout, alpha, bias, residual, ldr, Y, y_type, ldy,
+                        n, m, k, activation, stream=None):
+    _check(load().nvfp4_linear_launch(_ptr(X), x_type, ldx, _ptr(W), _ptr(sfW), w_layout, _ptr(alpha),
+                                      _ptr(bias), _ptr(residual), ldr, _ptr(Y), y_type, ldy, n, m, k,
+                                      activation, _stream(stream)), "nvfp4_linear_launch")
+
+
+def nvfp4_moe_layer_workspace_size(layer, tokens) -> int:
+    """``layer`` is a :class:`MoeLayerStruct` or a :class:`MoeLayer`."""
+    return int(load().nvfp4_moe_layer_workspace_size(_moe_struct(layer), tokens))
+
+
+def nvfp4_moe_layer_launch_ws(layer, X, ldx, residual, ldr, Y, y_type, ldy, tokens, workspace,
+                              workspace_bytes, stream=None):
+    _check(load().nvfp4_moe_layer_launch_ws(_moe_struct(layer), _ptr(X), ldx, _ptr(residual), ldr,
+                                            _ptr(Y), y_type, ldy, tokens, _ptr(workspace),
+                                            int(workspace_bytes), _stream(stream)),
+           "nvfp4_moe_layer_launch_ws")
+
+
+def nvfp4_moe_layer_launch(layer, X, ldx, residual, ldr, Y, y_type, ldy, tokens, stream=None):
+    _check(load().nvfp4_moe_layer_launch(_moe_struct(layer), _ptr(X), ldx, _ptr(residual), ldr, _ptr(Y),
+                                         y_type, ldy, tokens, _stream(stream)),
+           "nvfp4_moe_layer_launch")
+
+
+_ACTIVATIONS = {"none": NVFP4_ACT_NONE, "relu": NVFP4_ACT_RELU, "gelu": NVFP4_ACT_GELU,
+                "gelu_tanh": NVFP4_ACT_GELU_TANH, "silu": NVFP4_ACT_SILU}
+_SCORINGS = {"softmax": NVFP4_SCORE_SOFTMAX, "sigmoid": NVFP4_SCORE_SIGMOID}
+
+
+def _named(table, name, what):
+    if name not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)}")
+    return table[name]
+
+
+def _float_type(dtype, what, f32=False):
+    import torch
+
+    if dtype == torch.bfloat16:
+        return NVFP4_OUT_BF16
+    if dtype == torch.float16:
+        return NVFP4_OUT_F16
+    if f32 and dtype == torch.float32:
+        return NVFP4_OUT_F32
+    raise ValueError(f"{what} must be bfloat16{', float16 or float32' if f32 else ' or float16'}")
+
+
+def _rows(t, what, shape, dtype=None):
+    """Element stride of the rows of a 2-D device tensor whose columns are contiguous."""
+    if t.dim() != 2 or tuple(t.shape) != shape or not t.is_cuda or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be a device tensor of shape {shape}"
+                         f"{'' if dtype is None else f' and {dtype}'}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous columns")
+    # a single row's stride is free; torch reports anything there
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if ld < shape[1]:
+        raise ValueError(f"{what} must have rows that do not overlap")
+    return ld
+
+
+def _floats(t, count, what):
+    import torch
+
+    if t is not None and (t.dtype != torch.float32 or t.numel() != count or not t.is_contiguous()
+                          or not t.is_cuda):
+        raise ValueError(f"{what} must be a contiguous float32 device tensor of {count} values")
+
+
+def _weight(codes, scales, groups, rows, k, packed, what):
+    """Checks codes and scales of ``groups`` matrices of rows x k in either layout."""
+    import torch
+
+    if packed:
+        want = nvfp4_mma_packed_sizes(groups, rows, k)
+    else:
+        want = (groups * rows * (k // 2), groups * rows * (k // 16))
+    for t, count, name in ((codes, want[0], "codes"), (scales, want[1], "scales")):
+        if t.dtype != torch.uint8 or t.numel() != count or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{what} {name} must be a contiguous uint8 device tensor of {count} bytes")
+
+
+def _output(out, out_dtype, n, m, x, residual, stream):
+    """Output tensor (allocated on the stream that writes it if not given), its
+    type code and row strides of it and of the residual."""
+    import torch
+
+    if out is None:
+        dtype = x.dtype if out_dtype is None else out_dtype
+        _float_type(dtype, "out_dtype", f32=True)
+        if isinstance(stream, torch.cuda.Stream):
+            with torch.cuda.stream(stream):
+                out = torch.empty((n, m), dtype=dtype, device=x.device)
+        else:
+            out = torch.empty((n, m), dtype=dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out_dtype differs from out's type")
+    y_type = _float_type(out.dtype, "out", f32=True)
+    ldy = _rows(out, "out", (n, m))
+    ldr = 0 if residual is None else _rows(residual, "residual", (n, m), out.dtype)
+    return out, y_type, ldy, ldr
+
+
+def linear(x, codes, scales, m, alpha=None, bias=None, residual=None, activation="none", gated=False,
+           packed=False, out=None, out_dtype=None, stream=None):
+    """Tensor-level linear layer: ``residual + f(alpha x W^T + bias)`` or, gated,
+    ``residual + f(gate) * up``.
+
+    x (n, k) bfloat16 or float16 with any row stride; codes and scales uint8:
+    (m, k/2), (m, k/16), gated (2, m, k/2), (2, m, k/16), or with ``packed`` what
+    :func:`pack_weight` returns for them; alpha float32 of 1 (gated 2) values,
+    bias float32 of m (gated 2 m); residual (n, m) of the output's type, which
+    may be ``out`` itself.  Returns (n, m) of ``out_dtype`` (default x's type).
+    """
+    if x.dim() != 2:
+        raise ValueError("x must be (n, k)")
+    n, k = x.shape
+    x_type = _float_type(x.dtype, "x")
+    ldx = _rows(x, "x", (n, k))
+    groups = 2 if gated else 1
+    _weight(codes, scales, groups, m, k, packed, "weight")
+    _floats(alpha, groups, "alpha")
+    _floats(bias, groups * m, "bias")
+    act = _named(_ACTIVATIONS, activation, "activation") | (NVFP4_ACT_GATED if gated else 0)
+    out, y_type, ldy, ldr = _output(out, out_dtype, n, m, x, residual, stream)
+    if n > 0:
+        nvfp4_linear_launch(x, x_type, ldx, codes, scales, NVFP4_W_PACKED if packed else NVFP4_W_ROW_MAJOR,
+                            alpha, bias, residual, ldr, out, y_type, ldy, n, m, k, act, stream)
+    return out
+
+
+class MoeLayer:
+    """What stays the same from call to call of one mixture-of-experts layer
+    (``nvfp4_moe_layer_t``); keeps the tensors it names alive.
+
+    router (experts, hidden) bfloat16 or float16; codes13 / scales13 the gate
+    and up matrices, (2 experts, inter, .) with expert e's gate at 2 e; codes2 /
+    scales2 the down matrices, (experts, hidden, .); with ``packed`` what
+    :func:`pack_weight` returns for them.  alpha13 float32 (experts, 2),
+    alpha2 (experts,), route_bias (experts,), each optional.
+    """
+
+    def __init__(self, router, codes13, scales13, codes2, scales2, inter, topk, alpha13=None,
+                 alpha2=None, route_bias=None, activation="silu", scoring="softmax", renormalize=True,
+                 routed_scale=1.0, packed=False):
+        if router.dim() != 2 or not router.is_cuda or not router.is_contiguous():
+            raise ValueError("router must be a contiguous (experts, hidden) device tensor")
+        experts, hidden = router.shape
+        _weight(codes13, scales13, 2 * experts, inter, hidden, packed, "gate and up")
+        _weight(codes2, scales2, experts, hidden, inter, packed, "down")
+        _floats(alpha13, 2 * experts, "alpha13")
+        _floats(alpha2, experts, "alpha2")
+        _floats(route_bias, experts, "route_bias")
+        self.tensors = (router, codes13, scales13, codes2, scales2, alpha13, alpha2, route_bias)
+        self.dtype, self.hidden = router.dtype, hidden
+        self.struct = MoeLayerStruct(
+            router=_ptr(router), route_bias=_ptr(route_bias), W13=_ptr(codes13), sf13=_ptr(scales13),
+            alpha13=_ptr(alpha13), W2=_ptr(codes2), sf2=_ptr(scales2), alpha2=_ptr(alpha2),
+            experts=experts, hidden=hidden, inter=inter, topk=topk,
+            x_type=_float_type(router.dtype, "router"),
+            w_layout=NVFP4_W_PACKED if packed else NVFP4_W_ROW_MAJOR,
+            activation=_named(_ACTIVATIONS, activation, "activation"),
+            scoring=_named(_SCORINGS, scoring, "scoring"), renormalize=int(bool(renormalize)),
+            routed_scale=routed_scale, reserved=0)
+
+
+def _moe_struct(layer):
+    return ctypes.byref(layer.struct if isinstance(layer, MoeLayer) else layer)
+
+
+def moe_layer(x, layer, residual=None, out=None, out_dtype=None, stream=None):
+    """Tensor-level mixture-of-experts layer: x (tokens, hidden) of the
+    router's type with any row stride, ``layer`` a :class:`MoeLayer`, residual
+    (tokens, hidden) of the output's type, which may be ``out`` itself.  Returns
+    (tokens, hidden) of ``out_dtype`` (default x's type)."""
+    if x.dim() != 2 or x.shape[1] != layer.hidden:
+        raise ValueError(f"x must be (tokens, {layer.hidden})")
+    n = x.shape[0]
+    ldx = _rows(x, "x", (n, layer.hidden), layer.dtype)
+    out, y_type, ldy, ldr = _output(out, out_dtype, n, layer.hidden, x, residual, stream)
+    if n > 0:
+        nvfp4_moe_layer_launch(layer, x, ldx, residual, ldr, out, y_type, ldy, n, stream)
+    return out

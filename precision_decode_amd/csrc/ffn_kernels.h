@@ -1,0 +1,447 @@
+// Device code of the feed-forward operators (the linear layer and the
+// mixture-of-experts layer on NVFP4 weights); nvfp4_ffn.hip, the only
+// includer, describes the design and holds the host side.
+#ifndef NVFP4_FFN_KERNELS_H
+#define NVFP4_FFN_KERNELS_H
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "device_common.h"
+#include "ffn_plan.h"
+
+namespace {
+
+using namespace nvfp4dev;
+using namespace nvfp4ffnplan;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// What a kernel of products does with its accumulators and where its tokens
+// come from.
+enum Mode {
+    kLinear = 0,    // tokens in order; epilogue to Y
+    kMoeUp = 1,     // the tokens of an expert; f(gate) * up to h
+    kMoeDown = 2,   // the slots of an expert; alpha2 * sum to the slot's partial output
+};
+
+struct FfnArgs {
+    const uint8_t *X;           // 16-bit rows, ldx elements apart (kMoeDown: h)
+    int64_t ldx;
+    int64_t plane;              // kMoeDown: elements between the planes of h
+    const uint8_t *W, *sW;
+    const float *alpha;         // per matrix, or NULL
+    const float *bias;          // kLinear, or NULL
+    const void *residual;       // kLinear, or NULL
+    int64_t ldr;
+    void *Y;                    // kLinear: Y; kMoeUp: h; kMoeDown: partial outputs
+    int64_t ldy;
+    const int32_t *offsets;     // MoE: first slot of every expert
+    const int32_t *list;        // MoE: slots sorted by expert
+    int64_t n, m, k;            // tokens, rows of one matrix, K
+    int32_t topk;
+    int32_t act;
+    int32_t y_type;
+    int32_t y_planes;           // kMoeUp: planes of h to write
+};
+
+// ---------------------------------------------------------------- arithmetic
+// f of nvfp4_ffn.h in fp32.
+__device__ __forceinline__ float activate(int act, float z) {
+    switch (act) {
+    case NVFP4_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
+    case NVFP4_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
+    case NVFP4_ACT_GELU_TANH: {
+        // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+        const float u = 0.79788456f * (z + 0.044715f * z * z * z);
+        return z / (1.0f + expf(-2.0f * u));
+    }
+    case NVFP4_ACT_SILU: return z / (1.0f + expf(-z));
+    default: return z;
+    }
+}
+
+__device__ __forceinline__ float bf16_value(uint16_t b) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(b) << 16);
+}
+
+__device__ __forceinline__ float load_as_float(const void *p, int64_t i, int type) {
+    if (type == NVFP4_OUT_F32) return static_cast<const float *>(p)[i];
+    const uint16_t b = static_cast<const uint16_t *>(p)[i];
+    return type == NVFP4_OUT_BF16 ? bf16_value(b) : static_cast<float>(__builtin_bit_cast(_Float16, b));
+}
+
+__device__ __forceinline__ uint16_t round16(float v, bool bf16) {
+    return bf16 ? bf16_rne(v) : __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+}
+
+__device__ __forceinline__ void store_rounded(void *p, int64_t i, int type, float v) {
+    if (type == NVFP4_OUT_F32)
+        static_cast<float *>(p)[i] = v;
+    else
+        static_cast<uint16_t *>(p)[i] = round16(v, type == NVFP4_OUT_BF16);
+}
+
+// The i-th bf16 plane of v: the planes of a value are its rounding to bf16,
+// the rounding of what that leaves, and so on; two hold 16 significant bits,
+// three hold an fp32 value whole.  Infinities and NaN have no rest.
+__device__ __forceinline__ void split_planes(float v, int planes, uint16_t (&o)[kMaxPlanes]) {
+#pragma unroll
+    for (int i = 0; i < kMaxPlanes; ++i) {
+        o[i] = i < planes ? bf16_rne(v) : uint16_t(0);
+        const float hi = bf16_value(o[i]);
+        v = (o[i] & 0x7F80u) == 0x7F80u ? 0.0f : v - hi;
+    }
+}
+
+// ---------------------------------------------------------------- decode
+// 8 codes (4 bytes) times their block scale as a matrix-core operand, exact.
+// fp16: packed multiplies.  bf16: gfx950 has no packed bf16 multiply, so the
+// products are formed in fp32, where they are exact with the low 16 bits
+// zero, and their upper halves are taken.
+__device__ __forceinline__ f16x8 decode8(uint32_t q, f16x2 s) {
+    const f16x2 a = e2m1x2_f16<0>(q) * s, b = e2m1x2_f16<1>(q) * s, c = e2m1x2_f16<2>(q) * s,
+                d = e2m1x2_f16<3>(q) * s;
+    return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t decode2_bf16(uint32_t q, float s) {
+    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, SEL);
+    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, v.y * s),
+                                 __builtin_bit_cast(uint32_t, v.x * s), 0x07060302u);
+}
+__device__ __forceinline__ u32x4 decode8(uint32_t q, float s) {
+    return u32x4{decode2_bf16<0>(q, s), decode2_bf16<1>(q, s), decode2_bf16<2>(q, s),
+                 decode2_bf16<3>(q, s)};
+}
+
+// acc += w (rows) x (tokens) over 32 elements of K, 8 per lane.
+template <bool BF16>
+__device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 acc) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
+                                                       __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w),
+                                                      __builtin_bit_cast(f16x8, x), acc, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- tokens
+struct TokenRange {
+    int32_t first, end;   // positions in the token order (kLinear) or in the slot list
+};
+
+template <int MODE>
+__device__ __forceinline__ TokenRange expert_range(const FfnArgs &a, int expert) {
+    if (MODE == kLinear) return {0, static_cast<int32_t>(a.n)};
+    return {a.offsets[expert], a.offsets[expert + 1]};
+}
+
+// Output row (kLinear: token, else slot) and X row of position p.
+template <int MODE>
+__device__ __forceinline__ int32_t out_row(const FfnArgs &a, int32_t p) {
+    return MODE == kLinear ? p : a.list[p];
+}
+template <int MODE>
+__device__ __forceinline__ int32_t x_row(const FfnArgs &a, int32_t row) {
+    return MODE == kMoeUp ? row / a.topk : row;
+}
+
+// ---------------------------------------------------------------- epilogue
+// Rows r .. r+3 of the matrix (those below m) of one token or slot, from the
+// fp32 sums of the gate (or only) matrix and of the up matrix.
+template <int MODE, int G>
+__device__ __forceinline__ void finish4(const FfnArgs &a, int expert, int64_t row, int64_t r,
+                                        const f32x4 (&sum)[G]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (r + e >= a.m) return;
+        float z = (a.alpha ? a.alpha[MODE == kLinear ? 0 : G * expert] : 1.0f) * sum[0][e];
+        if (MODE == kMoeDown) {
+            static_cast<float *>(a.Y)[row * a.ldy + r + e] = z;
+            continue;
+        }
+        if (MODE == kLinear && a.bias) z += a.bias[r + e];
+        z = activate(a.act, z);
+        if constexpr (G == 2) {
+            float u = (a.alpha ? a.alpha[MODE == kLinear ? 1 : 2 * expert + 1] : 1.0f) * sum[1][e];
+            if (MODE == kLinear && a.bias) u += a.bias[a.m + r + e];
+            z *= u;
+        }
+        if (MODE == kMoeUp) {
+            uint16_t p[kMaxPlanes];
+            split_planes(z, a.y_planes, p);
+#pragma unroll
+            for (int i = 0; i < kMaxPlanes; ++i)
+                if (i < a.y_planes)
+                    static_cast<uint16_t *>(a.Y)[i * a.plane + row * a.ldy + r + e] = p[i];
+            continue;
+        }
+        if (a.residual) z += load_as_float(a.residual, row * a.ldr + r + e, a.y_type);
+        store_rounded(a.Y, row * a.ldy + r + e, a.y_type, z);
+    }
+}
+
+// ---------------------------------------------------------------- simple kernel
+constexpr int kSimpleWaves = 4;
+
+// Byte offsets of the codes and of the scale of elements e .. e+7 of a row
+// (e a multiple of 8) in either layout; `row` counts over all matrices before
+// it in row-major order, and the packed layout starts every matrix on a tile.
+template <bool PACKED>
+__device__ __forceinline__ void weight_at(int64_t matrix, int64_t row, int64_t m, int64_t k, int64_t e,
+                                          int64_t *code, int64_t *scale) {
+    if (PACKED) {
+        const int64_t wins = (k + kWinElems - 1) / kWinElems, tiles = (m + kTile - 1) / kTile;
+        const int64_t b = (matrix * tiles + row / kTile) * wins + e / kWinElems;
+        const int64_t lane = row % kTile + 16 * ((e % kWinElems) / 64);
+        *code = 2048 * b + 1024 * ((e % 64) / 32) + 16 * lane + (e % 32) / 2;
+        *scale = 256 * b + 4 * lane + (e % 64) / 16;
+    } else {
+        *code = (matrix * m + row) * (k / 2) + e / 2;
+        *scale = (matrix * m + row) * (k / 16) + e / 16;
+    }
+}
+
+// One workgroup owns 16 rows of a matrix (G = 2: of a gate and an up matrix)
+// and, in turn, every 16 tokens of its range (kLinear: 16 tokens alone).
+// Its waves take interleaved steps of 32 elements of K; their sums are added
+// in wave order through LDS.  Every load is made for its own 8 elements with
+// no assumption on alignment beyond the elements', so this kernel takes every
+// valid call.
+template <bool BF16, bool PACKED, int G, int P, int MODE>
+__global__ void __launch_bounds__(kSimpleWaves * kWave) ffn_simple(const FfnArgs a) {
+    __shared__ f32x4 red[(kSimpleWaves - 1) * G * kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int li = lane & 15, kq = lane >> 4;
+    const uint32_t tiles = static_cast<uint32_t>((a.m + kTile - 1) / kTile);
+    const uint32_t group = blockIdx.x / tiles;   // expert, or 16 tokens of the linear layer
+    const int64_t row0 = int64_t(blockIdx.x - group * tiles) * kTile;
+    const int expert = MODE == kLinear ? 0 : group;
+    TokenRange range = expert_range<MODE>(a, expert);
+    if (MODE == kLinear) {
+        range.first = group * kTile;
+        if (range.end > range.first + kTile) range.end = range.first + kTile;
+    }
+    const bool row_in = row0 + li < a.m;
+    for (int32_t p0 = range.first; p0 < range.end; p0 += kTile) {
+        const bool tok_in = p0 + li < range.end;
+        const int32_t orow = tok_in ? out_row<MODE>(a, p0 + li) : 0;
+        const uint8_t *x = a.X + 2 * (x_row<MODE>(a, orow) * a.ldx);
+        f32x4 acc[G] = {};
+        for (int64_t e0 = 32 * wave; e0 < a.k; e0 += 32 * kSimpleWaves) {
+            const int64_t e = e0 + 8 * kq;
+            u32x4 xv[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                xv[p] = u32x4{0, 0, 0, 0};
+                if (tok_in && e < a.k) __builtin_memcpy(&xv[p], x + 2 * (p * a.plane + e), 16);
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                uint32_t q = 0, s = 0;
+                if (row_in && e < a.k) {
+                    int64_t co, so;
+                    weight_at<PACKED>(G * int64_t(expert) + g, row0 + li, a.m, a.k, e, &co, &so);
+                    __builtin_memcpy(&q, a.W + co, 4);
+                    s = a.sW[so];
+                }
+                u32x4 w;
+                if constexpr (BF16) {
+                    w = decode8(q, e4m3x2_f32(s).x);
+                } else {
+                    const f16x2 sv = e4m3x2_f16(s);
+                    w = __builtin_bit_cast(u32x4, decode8(q, f16x2{sv.x, sv.x}));
+                }
+#pragma unroll
+                for (int p = 0; p < P; ++p) acc[g] = mfma<BF16>(w, xv[p], acc[g]);
+            }
+        }
+        if (wave > 0)
+#pragma unroll
+            for (int g = 0; g < G; ++g) red[((wave - 1) * G + g) * kWave + lane] = acc[g];
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                for (int w = 1; w < kSimpleWaves; ++w) acc[g] += red[((w - 1) * G + g) * kWave + lane];
+            if (tok_in) finish4<MODE, G>(a, expert, orow, row0 + 4 * kq, acc);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- routing
+struct RouteArgs {
+    const uint8_t *X;
+    int64_t ldx;
+    const uint8_t *router;
+    const float *route_bias;
+    double *logits;
+    int32_t *offsets, *choice, *list;
+    float *weights;
+    int64_t tokens, experts, hidden;
+    int32_t topk, bf16, scoring, renormalize;
+    float routed_scale;
+};
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+__device__ __forceinline__ double wave_max64(double v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
+    return v;
+}
+
+constexpr int kRouteThreads = 256;
+
+constexpr int kRouteTokens = 16;
+
+// Logits of one expert (blockIdx.x) and 16 tokens (blockIdx.y): products of 16-bit values are exact in
+// fp64, and the fp64 sum errs by about 2^-50, so the choice of experts is the
+// one of the exact scores unless these agree to some 14 digits.
+__global__ void __launch_bounds__(kRouteThreads) route_logits(const RouteArgs a) {
+    __shared__ double red[kRouteThreads / kWave];
+    const int64_t expert = blockIdx.x;
+    const uint16_t *w = reinterpret_cast<const uint16_t *>(a.router) + expert * a.hidden;
+    const int type = a.bf16 ? NVFP4_OUT_BF16 : NVFP4_OUT_F16;
+    const int64_t t0 = int64_t(blockIdx.y) * kRouteTokens;
+    for (int64_t t = t0; t < t0 + kRouteTokens && t < a.tokens; ++t) {
+        const uint16_t *x = reinterpret_cast<const uint16_t *>(a.X) + t * a.ldx;
+        double s = 0.0;
+        for (int64_t i = threadIdx.x; i < a.hidden; i += kRouteThreads)
+            s = __builtin_fma(double(load_as_float(x, i, type)), double(load_as_float(w, i, type)), s);
+        s = wave_sum64(s);
+        if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 1; i < kRouteThreads / kWave; ++i) s += red[i];
+            a.logits[t * a.experts + expert] = s;
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int kSelectWaves = 4;
+
+// One workgroup chooses the experts of every token, a wave per token at a
+// time: an expert's rank is the number of experts ahead of it (a larger key,
+// or an equal one at a lower index), so the ranks are a permutation whatever
+// the keys hold, and rank j < topk is slot token * topk + j.  Then the slots
+// are sorted by expert; the order inside an expert comes from an atomic and
+// may differ between runs, but nothing depends on it: every slot is a column
+// of its own in the products.
+__global__ void __launch_bounds__(kSelectWaves * kWave) route_select(const RouteArgs a) {
+    __shared__ double keys[kSelectWaves][kMaxExperts];
+    __shared__ int32_t count[kMaxExperts], cursor[kMaxExperts];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int experts = static_cast<int>(a.experts);
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) count[e] = 0;
+    __syncthreads();
+    const int64_t rounds = (a.tokens + kSelectWaves - 1) / kSelectWaves;
+    for (int64_t i = 0; i < rounds; ++i) {
+        const int64_t t = i * kSelectWaves + wave;
+        const bool in = t < a.tokens;
+        const double *z = a.logits + t * experts;
+        double top = -INFINITY, sum = 0.0;
+        if (in && a.scoring == NVFP4_SCORE_SOFTMAX) {
+            for (int e = lane; e < experts; e += kWave) top = fmax(top, z[e]);
+            top = wave_max64(top);
+            for (int e = lane; e < experts; e += kWave) sum += exp(z[e] - top);
+            sum = wave_sum64(sum);
+        }
+        auto score = [&](int e) {
+            return a.scoring == NVFP4_SCORE_SOFTMAX ? exp(z[e] - top) / sum : 1.0 / (1.0 + exp(-z[e]));
+        };
+        if (in)
+            for (int e = lane; e < experts; e += kWave) {
+                const double key = score(e) + (a.route_bias ? double(a.route_bias[e]) : 0.0);
+                keys[wave][e] = key == key ? key : -INFINITY;
+            }
+        __syncthreads();
+        double chosen = 0.0;
+        if (in) {
+            for (int e = lane; e < experts; e += kWave) {
+                const double key = keys[wave][e];
+                int rank = 0;
+                for (int o = 0; o < experts; ++o) {
+                    const double other = keys[wave][o];
+                    rank += other > key || (other == key && o < e);
+                }
+                if (rank < a.topk) {
+                    const double s = score(e);
+                    chosen += s;
+                    a.choice[t * a.topk + rank] = e;
+                    a.weights[t * a.topk + rank] = static_cast<float>(
+                        a.renormalize ? s : s * double(a.routed_scale));
+                    atomicAdd(&count[e], 1);
+                }
+            }
+            chosen = wave_sum64(chosen);
+        }
+        __syncthreads();
+        if (in && a.renormalize)
+            for (int j = lane; j < a.topk; j += kWave)
+                a.weights[t * a.topk + j] =
+                    static_cast<float>(a.weights[t * a.topk + j] / chosen * double(a.routed_scale));
+    }
+    __syncthreads();
+    // offsets: lane l of wave 0 sums its run of experts, the runs are scanned
+    if (wave == 0) {
+        const int per = (experts + kWave - 1) / kWave;
+        const int e0 = lane * per;
+        int own = 0;
+        for (int e = e0; e < e0 + per && e < experts; ++e) own += count[e];
+        int at = own;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int v = __shfl_up(at, o);
+            if (lane >= o) at += v;
+        }
+        at -= own;
+        for (int e = e0; e < e0 + per && e < experts; ++e) {
+            a.offsets[e] = cursor[e] = at;
+            at += count[e];
+        }
+        if (lane == kWave - 1) a.offsets[experts] = at;
+    }
+    __syncthreads();
+    const int64_t slots = a.tokens * a.topk;
+    for (int64_t s = threadIdx.x; s < slots; s += blockDim.x)
+        a.list[atomicAdd(&cursor[a.choice[s]], 1)] = static_cast<int32_t>(s);
+}
+
+// ---------------------------------------------------------------- combination
+struct CombineArgs {
+    const float *part, *weights;
+    const void *residual;
+    int64_t ldr;
+    void *Y;
+    int64_t ldy, tokens, hidden;
+    int32_t topk, y_type;
+};
+
+constexpr int kCombineThreads = 256;
+
+// Y of one token (blockIdx.y): its slots' partial outputs in the order of
+// their ranks.
+__global__ void __launch_bounds__(kCombineThreads) moe_combine(const CombineArgs a) {
+    const int64_t r = int64_t(blockIdx.x) * kCombineThreads + threadIdx.x, t = blockIdx.y;
+    if (r >= a.hidden) return;
+    float y = 0.0f;
+    for (int j = 0; j < a.topk; ++j) {
+        const int64_t s = t * a.topk + j;
+        y += a.weights[s] * a.part[s * a.hidden + r];
+    }
+    if (a.residual) y += load_as_float(a.residual, t * a.ldr + r, a.y_type);
+    store_rounded(a.Y, t * a.ldy + r, a.y_type, y);
+}
+
+}  // namespace
+
+#endif  // NVFP4_FFN_KERNELS_H

@@ -1,0 +1,126 @@
+// Host-side plan of the feed-forward operators on NVFP4 weights (the linear
+// layer with a fused epilogue and the mixture-of-experts layer): argument
+// checks, kernel choice, grids and workspace layout.
+//
+// Plain C++17 with no HIP types, so that the same code is compiled into the
+// library (nvfp4_ffn.hip) and into host-only checks built with g++ and the
+// address and undefined-behaviour sanitizers.  Not part of the C ABI.
+#ifndef NVFP4_FFN_PLAN_H
+#define NVFP4_FFN_PLAN_H
+
+#include <climits>
+#include <cstddef>
+#include <cstdint>
+
+#include "nvfp4_ffn.h"
+
+namespace nvfp4ffnplan {
+
+constexpr int kTile = 16;                          // MFMA tile: 16 weight rows x 16 tokens
+constexpr int kWinElems = 256;                     // K elements of one packed window
+constexpr int64_t kMaxK = int64_t(1) << 22;        // k and ldx: keeps row offsets within 31 bits
+constexpr int64_t kMaxLd = int64_t(1) << 31;       // ldy and ldr
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxTopk = 64;
+constexpr int64_t kMaxTokens = 65535;              // of a MoE call (a grid's second dimension)
+constexpr int64_t kMaxTiles = int64_t(1) << 24;    // workgroups of 256 threads: below 2^32 threads
+constexpr size_t kWsAlign = 256;
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool mul_fits(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / a; }
+inline size_t ws_round(size_t b) { return (b + kWsAlign - 1) & ~(kWsAlign - 1); }
+inline int type_bytes(int32_t t) { return t == NVFP4_OUT_F32 ? 4 : 2; }
+
+inline bool act_known(int32_t a) { return a >= NVFP4_ACT_NONE && a <= NVFP4_ACT_SILU; }
+inline bool in_type_known(int32_t t) { return t == NVFP4_OUT_F16 || t == NVFP4_OUT_BF16; }
+inline bool out_type_known(int32_t t) { return in_type_known(t) || t == NVFP4_OUT_F32; }
+inline bool layout_known(int32_t w) { return w == NVFP4_W_ROW_MAJOR || w == NVFP4_W_PACKED; }
+
+inline bool k_ok(int64_t k, int32_t w_layout) {
+    return k >= 16 && k <= kMaxK && k % (w_layout == NVFP4_W_PACKED ? 64 : 16) == 0;
+}
+
+// Bytes of the codes and scales of `groups` matrices of rows x k.
+inline bool weight_bytes(int64_t groups, int64_t rows, int64_t k, int32_t w_layout, int64_t *codes,
+                         int64_t *scales) {
+    const int64_t r = w_layout == NVFP4_W_PACKED ? ceil_div(rows, kTile) * kTile : rows;
+    const int64_t kk = w_layout == NVFP4_W_PACKED ? ceil_div(k, kWinElems) * kWinElems : k;
+    if (!mul_fits(groups, r) || !mul_fits(groups * r, kk)) return false;
+    *codes = groups * r * (kk / 2);
+    *scales = groups * r * (kk / 16);
+    return true;
+}
+
+// Bytes from the first to past the last element of `rows` rows of `cols`
+// elements, `ld` apart.
+inline bool span_bytes(int64_t rows, int64_t cols, int64_t ld, int bytes, int64_t *out) {
+    if (rows == 0) { *out = 0; return true; }
+    if (!mul_fits(rows - 1, ld)) return false;
+    const int64_t e = (rows - 1) * ld;
+    if (e > INT64_MAX / bytes - cols) return false;
+    *out = (e + cols) * bytes;
+    return true;
+}
+
+inline int check_linear_shape(int64_t n, int64_t m, int64_t k, int32_t w_layout) {
+    if (n < 0 || m < 1 || !k_ok(k, w_layout) || n >= (int64_t(1) << 31) || m >= (int64_t(1) << 31))
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    if (ceil_div(n, kTile) * ceil_div(m, kTile) >= kMaxTiles) return NVFP4_GEMV_ERR_BAD_SHAPE;
+    int64_t c, s;
+    if (!weight_bytes(2, m, k, w_layout, &c, &s)) return NVFP4_GEMV_ERR_BAD_SHAPE;
+    return NVFP4_GEMV_OK;
+}
+
+inline int check_moe_shape(const nvfp4_moe_layer_t &l, int64_t tokens) {
+    if (l.experts < 1 || l.experts > kMaxExperts || l.topk < 1 || l.topk > kMaxTopk ||
+        l.topk > l.experts || tokens < 0 || tokens > kMaxTokens ||
+        !k_ok(l.hidden, l.w_layout) || !k_ok(l.inter, l.w_layout) ||
+        l.experts * ceil_div(l.hidden, kTile) >= kMaxTiles || l.experts * ceil_div(l.inter, kTile) >= kMaxTiles)
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    int64_t c, s;
+    if (!weight_bytes(2 * l.experts, l.inter, l.hidden, l.w_layout, &c, &s) ||
+        !weight_bytes(l.experts, l.hidden, l.inter, l.w_layout, &c, &s))
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    return NVFP4_GEMV_OK;
+}
+
+// Workspace of one MoE call, in bytes from its start.  The sizes go by the
+// larger (fp32 output) number of planes of h, so they do not depend on it.
+struct MoeWorkspace {
+    size_t logits;    // double [tokens][experts]
+    size_t offsets;   // int32 [experts + 1]: first slot of every expert
+    size_t choice;    // int32 [slots]: expert of every slot (slot = token * topk + j)
+    size_t list;      // int32 [slots]: slots sorted by expert
+    size_t weights;   // float [slots]
+    size_t h;         // bf16 [planes][slots][inter]
+    size_t part;      // float [slots][hidden]
+    size_t x;         // 16-bit [tokens][hidden]: aligned copy of X
+    size_t total;
+};
+
+constexpr int kMaxPlanes = 3;
+
+inline MoeWorkspace moe_workspace(const nvfp4_moe_layer_t &l, int64_t tokens) {
+    const size_t slots = static_cast<size_t>(tokens) * l.topk;
+    MoeWorkspace w;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += ws_round(bytes);
+        return here;
+    };
+    w.logits = take(static_cast<size_t>(tokens) * l.experts * 8);
+    w.offsets = take(static_cast<size_t>(l.experts + 1) * 4);
+    w.choice = take(slots * 4);
+    w.list = take(slots * 4);
+    w.weights = take(slots * 4);
+    w.h = take(kMaxPlanes * slots * l.inter * 2);
+    w.part = take(slots * l.hidden * 4);
+    w.x = take(static_cast<size_t>(tokens) * l.hidden * 2);
+    w.total = at;
+    return w;
+}
+
+}  // namespace nvfp4ffnplan
+
+#endif  // NVFP4_FFN_PLAN_H

@@ -1,0 +1,372 @@
+// Feed-forward operators on NVFP4 weights for MI355X (gfx950): the linear
+// layer with bias, activation and residual in its epilogue, and a whole
+// mixture-of-experts layer for a few tokens.
+//
+// A weight element times its block scale, e2m1 * e4m3, has at most 5
+// significant bits and lies in 2^-10 .. 2688, so it is exact as bf16 and as
+// fp16.  The 16-bit activations therefore meet the 4-bit weights on the
+// 16x16x32 matrix-core instructions of their own type without being
+// quantised: the VALU decodes weight tiles into operands, the products are
+// exact in fp32 and summed there.  The weight tile is the A operand and the
+// tokens are the B operand, so a lane ends with four consecutive rows of one
+// token, which the epilogue finishes and stores together.
+//
+// The MoE layer runs as route_logits, route_select, the gate/up product, the
+// down product and moe_combine.  Each slot (a token and one of its experts)
+// is a column of the expert's products; h = f(gate) up goes through the
+// workspace as bf16 planes (the value, the rest of its rounding, ...) that
+// the down product multiplies one after another into the same sums.
+//
+// This file holds the host side (validation, launches, the C-ABI entry
+// points); the device code is ffn_kernels.h and the argument checks, kernel
+// choice and workspace layout are ffn_plan.h.
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "device_common.h"
+#include "ffn_kernels.h"
+#include "ffn_plan.h"
+#include "nvfp4_ffn.h"
+
+namespace {
+
+bool misaligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+struct Span {
+    const void *p;
+    int64_t n;
+};
+
+bool overlaps(Span a, Span b) {
+    if (!a.p || !b.p || a.n <= 0 || b.n <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + static_cast<uintptr_t>(b.n) && y < x + static_cast<uintptr_t>(a.n);
+}
+
+int run(const void *fn, dim3 grid, int threads, void **args, hipStream_t stream) {
+    return hipLaunchKernel(fn, grid, dim3(threads), args, 0, stream) == hipSuccess ? NVFP4_GEMV_OK
+                                                                                  : NVFP4_GEMV_ERR_LAUNCH;
+}
+
+template <typename A>
+int run(void (*fn)(A), dim3 grid, int threads, A a, hipStream_t stream) {
+    void *args[] = {&a};
+    return run(reinterpret_cast<const void *>(fn), grid, threads, args, stream);
+}
+
+template <bool BF16, int G, int P, int MODE>
+int launch_simple(const FfnArgs &a, bool packed, dim3 grid, hipStream_t stream) {
+    return run(packed ? ffn_simple<BF16, true, G, P, MODE> : ffn_simple<BF16, false, G, P, MODE>, grid,
+               kSimpleWaves * kWave, a, stream);
+}
+
+// ---------------------------------------------------------------- linear
+struct LinearCall {
+    const void *X;
+    int32_t x_type;
+    int64_t ldx;
+    const uint8_t *W, *sfW;
+    int32_t w_layout;
+    const float *alpha, *bias;
+    const void *residual;
+    int64_t ldr;
+    void *Y;
+    int32_t y_type;
+    int64_t ldy, n, m, k;
+    int32_t activation;
+    bool gated() const { return (activation & NVFP4_ACT_GATED) != 0; }
+};
+
+// The weight, its layout and its scales: pointers' alignment.
+int check_weight_alignment(const void *W, const void *sf, int32_t w_layout) {
+    if (w_layout == NVFP4_W_PACKED && (misaligned(W, 16) || misaligned(sf, 4)))
+        return NVFP4_GEMV_ERR_ALIGNMENT;
+    return NVFP4_GEMV_OK;
+}
+
+int check_linear(const LinearCall &c) {
+    if (!c.X || !c.W || !c.sfW || !c.Y) return NVFP4_GEMV_ERR_NULL_POINTER;
+    if (!in_type_known(c.x_type) || !out_type_known(c.y_type) || !layout_known(c.w_layout) ||
+        !act_known(c.activation & ~NVFP4_ACT_GATED))
+        return NVFP4_GEMV_ERR_BAD_ARGUMENT;
+    int s = check_linear_shape(c.n, c.m, c.k, c.w_layout);
+    if (s != NVFP4_GEMV_OK) return s;
+    if (c.ldx < c.k || c.ldx > kMaxK || c.ldy < c.m || c.ldy > kMaxLd ||
+        (c.residual && (c.ldr < c.m || c.ldr > kMaxLd)))
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    const int yb = type_bytes(c.y_type);
+    if (misaligned(c.X, 2) || misaligned(c.Y, yb) || misaligned(c.residual, yb) ||
+        misaligned(c.alpha, 4) || misaligned(c.bias, 4))
+        return NVFP4_GEMV_ERR_ALIGNMENT;
+    s = check_weight_alignment(c.W, c.sfW, c.w_layout);
+    if (s != NVFP4_GEMV_OK) return s;
+    const int64_t mats = c.gated() ? 2 : 1;
+    int64_t wb, sb, xs, ys, rs = 0;
+    if (!weight_bytes(mats, c.m, c.k, c.w_layout, &wb, &sb) || !span_bytes(c.n, c.k, c.ldx, 2, &xs) ||
+        !span_bytes(c.n, c.m, c.ldy, yb, &ys) ||
+        (c.residual && !span_bytes(c.n, c.m, c.ldr, yb, &rs)))
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    const Span y{c.Y, ys};
+    const bool in_place = c.residual == c.Y && c.ldr == c.ldy;
+    if (overlaps(y, {c.X, xs}) || overlaps(y, {c.W, wb}) || overlaps(y, {c.sfW, sb}) ||
+        overlaps(y, {c.alpha, mats * 4}) || overlaps(y, {c.bias, mats * c.m * 4}) ||
+        (!in_place && overlaps(y, {c.residual, rs})))
+        return NVFP4_GEMV_ERR_ALIAS;
+    return NVFP4_GEMV_OK;
+}
+
+template <bool BF16>
+int launch_linear(const FfnArgs &a, bool packed, bool gated, hipStream_t stream) {
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile)));
+    return gated ? launch_simple<BF16, 2, 1, kLinear>(a, packed, grid, stream)
+                 : launch_simple<BF16, 1, 1, kLinear>(a, packed, grid, stream);
+}
+
+int linear(const LinearCall &c, hipStream_t stream) {
+    if (c.n == 0) return NVFP4_GEMV_OK;
+    FfnArgs a = {};
+    a.X = static_cast<const uint8_t *>(c.X);
+    a.ldx = c.ldx;
+    a.W = c.W;
+    a.sW = c.sfW;
+    a.alpha = c.alpha;
+    a.bias = c.bias;
+    a.residual = c.residual;
+    a.ldr = c.ldr;
+    a.Y = c.Y;
+    a.ldy = c.ldy;
+    a.n = c.n;
+    a.m = c.m;
+    a.k = c.k;
+    a.topk = 1;
+    a.act = c.activation & ~NVFP4_ACT_GATED;
+    a.y_type = c.y_type;
+    const bool packed = c.w_layout == NVFP4_W_PACKED;
+    return c.x_type == NVFP4_OUT_BF16 ? launch_linear<true>(a, packed, c.gated(), stream)
+                                      : launch_linear<false>(a, packed, c.gated(), stream);
+}
+
+// ---------------------------------------------------------------- MoE
+struct MoeCall {
+    const nvfp4_moe_layer_t *layer;
+    const void *X;
+    int64_t ldx;
+    const void *residual;
+    int64_t ldr;
+    void *Y;
+    int32_t y_type;
+    int64_t ldy, tokens;
+};
+
+int check_moe(const MoeCall &c) {
+    if (!c.layer || !c.X || !c.Y) return NVFP4_GEMV_ERR_NULL_POINTER;
+    const nvfp4_moe_layer_t &l = *c.layer;
+    if (!l.router || !l.W13 || !l.sf13 || !l.W2 || !l.sf2) return NVFP4_GEMV_ERR_NULL_POINTER;
+    if (!in_type_known(l.x_type) || !out_type_known(c.y_type) || !layout_known(l.w_layout) ||
+        !act_known(l.activation) || l.scoring < NVFP4_SCORE_SOFTMAX || l.scoring > NVFP4_SCORE_SIGMOID ||
+        l.renormalize < 0 || l.renormalize > 1 || l.reserved != 0)
+        return NVFP4_GEMV_ERR_BAD_ARGUMENT;
+    int s = check_moe_shape(l, c.tokens);
+    if (s != NVFP4_GEMV_OK) return s;
+    if (c.ldx < l.hidden || c.ldx > kMaxK || c.ldy < l.hidden || c.ldy > kMaxLd ||
+        (c.residual && (c.ldr < l.hidden || c.ldr > kMaxLd)))
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    const int yb = type_bytes(c.y_type);
+    if (misaligned(c.X, 2) || misaligned(l.router, 2) || misaligned(c.Y, yb) ||
+        misaligned(c.residual, yb) || misaligned(l.route_bias, 4) || misaligned(l.alpha13, 4) ||
+        misaligned(l.alpha2, 4))
+        return NVFP4_GEMV_ERR_ALIGNMENT;
+    s = check_weight_alignment(l.W13, l.sf13, l.w_layout);
+    if (s == NVFP4_GEMV_OK) s = check_weight_alignment(l.W2, l.sf2, l.w_layout);
+    if (s != NVFP4_GEMV_OK) return s;
+    int64_t w13, s13, w2, s2, xs, ys, rs = 0;
+    if (!weight_bytes(2 * l.experts, l.inter, l.hidden, l.w_layout, &w13, &s13) ||
+        !weight_bytes(l.experts, l.hidden, l.inter, l.w_layout, &w2, &s2) ||
+        !span_bytes(c.tokens, l.hidden, c.ldx, 2, &xs) || !span_bytes(c.tokens, l.hidden, c.ldy, yb, &ys) ||
+        (c.residual && !span_bytes(c.tokens, l.hidden, c.ldr, yb, &rs)))
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    const Span y{c.Y, ys};
+    const bool in_place = c.residual == c.Y && c.ldr == c.ldy;
+    if (overlaps(y, {c.X, xs}) || overlaps(y, {l.router, l.experts * l.hidden * 2}) ||
+        overlaps(y, {l.route_bias, l.experts * 4}) || overlaps(y, {l.W13, w13}) ||
+        overlaps(y, {l.sf13, s13}) || overlaps(y, {l.W2, w2}) || overlaps(y, {l.sf2, s2}) ||
+        overlaps(y, {l.alpha13, l.experts * 8}) || overlaps(y, {l.alpha2, l.experts * 4}) ||
+        (!in_place && overlaps(y, {c.residual, rs})))
+        return NVFP4_GEMV_ERR_ALIAS;
+    return NVFP4_GEMV_OK;
+}
+
+template <bool BF16>
+int launch_up(const FfnArgs &a, bool packed, int64_t experts, hipStream_t stream) {
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * experts));
+    return launch_simple<BF16, 2, 1, kMoeUp>(a, packed, grid, stream);
+}
+
+int launch_down(const FfnArgs &a, bool packed, int planes, int64_t experts, hipStream_t stream) {
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * experts));
+    return planes == 2 ? launch_simple<true, 1, 2, kMoeDown>(a, packed, grid, stream)
+                       : launch_simple<true, 1, 3, kMoeDown>(a, packed, grid, stream);
+}
+
+int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
+    if (c.tokens == 0) return NVFP4_GEMV_OK;
+    const nvfp4_moe_layer_t &l = *c.layer;
+    const MoeWorkspace w = moe_workspace(l, c.tokens);
+    const bool packed = l.w_layout == NVFP4_W_PACKED, bf16 = l.x_type == NVFP4_OUT_BF16;
+    const int64_t slots = c.tokens * l.topk;
+
+    RouteArgs r = {};
+    r.X = static_cast<const uint8_t *>(c.X);
+    r.ldx = c.ldx;
+    r.router = static_cast<const uint8_t *>(l.router);
+    r.route_bias = l.route_bias;
+    r.logits = reinterpret_cast<double *>(ws + w.logits);
+    r.offsets = reinterpret_cast<int32_t *>(ws + w.offsets);
+    r.choice = reinterpret_cast<int32_t *>(ws + w.choice);
+    r.list = reinterpret_cast<int32_t *>(ws + w.list);
+    r.weights = reinterpret_cast<float *>(ws + w.weights);
+    r.tokens = c.tokens;
+    r.experts = l.experts;
+    r.hidden = l.hidden;
+    r.topk = l.topk;
+    r.bf16 = bf16;
+    r.scoring = l.scoring;
+    r.renormalize = l.renormalize;
+    r.routed_scale = l.routed_scale;
+    int s = run(route_logits, dim3(static_cast<uint32_t>(l.experts), static_cast<uint32_t>(ceil_div(c.tokens, kRouteTokens))),
+                kRouteThreads, r, stream);
+    if (s == NVFP4_GEMV_OK) s = run(route_select, dim3(1), kSelectWaves * kWave, r, stream);
+    if (s != NVFP4_GEMV_OK) return s;
+
+    const int planes = c.y_type == NVFP4_OUT_F32 ? 3 : 2;
+    FfnArgs a = {};
+    a.X = r.X;
+    a.ldx = c.ldx;
+    a.plane = slots * l.inter;
+    a.W = l.W13;
+    a.sW = l.sf13;
+    a.alpha = l.alpha13;
+    a.Y = ws + w.h;
+    a.ldy = l.inter;
+    a.offsets = r.offsets;
+    a.list = r.list;
+    a.n = c.tokens;
+    a.m = l.inter;
+    a.k = l.hidden;
+    a.topk = l.topk;
+    a.act = l.activation;
+    a.y_planes = planes;
+    s = bf16 ? launch_up<true>(a, packed, l.experts, stream) : launch_up<false>(a, packed, l.experts, stream);
+    if (s != NVFP4_GEMV_OK) return s;
+
+    a.X = ws + w.h;
+    a.ldx = l.inter;
+    a.W = l.W2;
+    a.sW = l.sf2;
+    a.alpha = l.alpha2;
+    a.Y = ws + w.part;
+    a.ldy = l.hidden;
+    a.m = l.hidden;
+    a.k = l.inter;
+    s = launch_down(a, packed, planes, l.experts, stream);
+    if (s != NVFP4_GEMV_OK) return s;
+
+    CombineArgs y = {};
+    y.part = reinterpret_cast<const float *>(ws + w.part);
+    y.weights = r.weights;
+    y.residual = c.residual;
+    y.ldr = c.ldr;
+    y.Y = c.Y;
+    y.ldy = c.ldy;
+    y.tokens = c.tokens;
+    y.hidden = l.hidden;
+    y.topk = l.topk;
+    y.y_type = c.y_type;
+    return run(moe_combine,
+               dim3(static_cast<uint32_t>(ceil_div(l.hidden, kCombineThreads)), static_cast<uint32_t>(c.tokens)),
+               kCombineThreads, y, stream);
+}
+
+// The library-owned workspace of the stream: nullptr and a status if it
+// cannot be had.
+int owned_workspace(size_t need, void *stream, void **ws) {
+    *ws = nullptr;
+    if (need == 0) return NVFP4_GEMV_OK;
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return NVFP4_GEMV_ERR_DEVICE;
+    }
+    *ws = nvfp4_stream_workspace(dev, stream, need);
+    return *ws ? NVFP4_GEMV_OK : NVFP4_GEMV_ERR_WORKSPACE;
+}
+
+int check_workspace(const void *ws, size_t bytes, size_t need) {
+    if (need == 0) return NVFP4_GEMV_OK;
+    if (!ws || bytes < need) return NVFP4_GEMV_ERR_WORKSPACE;
+    return misaligned(ws, kWsAlign) ? NVFP4_GEMV_ERR_ALIGNMENT : NVFP4_GEMV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nvfp4_linear_workspace_size(int64_t n, int64_t m, int64_t k, int32_t activation) {
+    (void)activation;
+    if (check_linear_shape(n, m, k, NVFP4_W_ROW_MAJOR) != NVFP4_GEMV_OK) return 0;
+    return 0;
+}
+
+int nvfp4_linear_launch_ws(const void *X, int32_t x_type, int64_t ldx, const uint8_t *W,
+                           const uint8_t *sfW, int32_t w_layout, const float *alpha, const float *bias,
+                           const void *residual, int64_t ldr, void *Y, int32_t y_type, int64_t ldy,
+                           int64_t n, int64_t m, int64_t k, int32_t activation, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    const LinearCall c = {X, x_type, ldx, W, sfW, w_layout, alpha, bias, residual, ldr,
+                          Y, y_type, ldy, n, m, k, activation};
+    const int s = check_linear(c);
+    if (s != NVFP4_GEMV_OK) return s;
+    (void)workspace;
+    (void)workspace_bytes;
+    return linear(c, static_cast<hipStream_t>(stream));
+}
+
+int nvfp4_linear_launch(const void *X, int32_t x_type, int64_t ldx, const uint8_t *W,
+                        const uint8_t *sfW, int32_t w_layout, const float *alpha, const float *bias,
+                        const void *residual, int64_t ldr, void *Y, int32_t y_type, int64_t ldy,
+                        int64_t n, int64_t m, int64_t k, int32_t activation, void *stream) {
+    return nvfp4_linear_launch_ws(X, x_type, ldx, W, sfW, w_layout, alpha, bias, residual, ldr, Y, y_type,
+                                  ldy, n, m, k, activation, nullptr, 0, stream);
+}
+
+size_t nvfp4_moe_layer_workspace_size(const nvfp4_moe_layer_t *layer, int64_t tokens) {
+    if (!layer || !layout_known(layer->w_layout) || check_moe_shape(*layer, tokens) != NVFP4_GEMV_OK) return 0;
+    return tokens == 0 ? 0 : moe_workspace(*layer, tokens).total;
+}
+
+int nvfp4_moe_layer_launch_ws(const nvfp4_moe_layer_t *layer, const void *X, int64_t ldx,
+                              const void *residual, int64_t ldr, void *Y, int32_t y_type, int64_t ldy,
+                              int64_t tokens, void *workspace, size_t workspace_bytes, void *stream) {
+    const MoeCall c = {layer, X, ldx, residual, ldr, Y, y_type, ldy, tokens};
+    int s = check_moe(c);
+    if (s != NVFP4_GEMV_OK) return s;
+    s = check_workspace(workspace, workspace_bytes, nvfp4_moe_layer_workspace_size(layer, tokens));
+    if (s != NVFP4_GEMV_OK) return s;
+    return moe(c, static_cast<uint8_t *>(workspace), static_cast<hipStream_t>(stream));
+}
+
+int nvfp4_moe_layer_launch(const nvfp4_moe_layer_t *layer, const void *X, int64_t ldx,
+                           const void *residual, int64_t ldr, void *Y, int32_t y_type, int64_t ldy,
+                           int64_t tokens, void *stream) {
+    const MoeCall c = {layer, X, ldx, residual, ldr, Y, y_type, ldy, tokens};
+    int s = check_moe(c);
+    if (s != NVFP4_GEMV_OK) return s;
+    void *ws;
+    s = owned_workspace(nvfp4_moe_layer_workspace_size(layer, tokens), stream, &ws);
+    if (s != NVFP4_GEMV_OK) return s;
+    return moe(c, static_cast<uint8_t *>(ws), static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
