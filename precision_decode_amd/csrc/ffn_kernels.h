@@ -8,6 +8,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 #include "device_common.h"
 #include "ffn_plan.h"
@@ -45,6 +46,8 @@ struct FfnArgs {
     int32_t act;
     int32_t y_type;
     int32_t y_planes;           // kMoeUp: planes of h to write
+    float *part;                // kLinear with K split: [split][n][matrices][m] sums, or NULL
+    int32_t splits;             // workgroups along K
 };
 
 // ---------------------------------------------------------------- arithmetic
@@ -153,8 +156,16 @@ __device__ __forceinline__ int32_t x_row(const FfnArgs &a, int32_t row) {
 // Rows r .. r+3 of the matrix (those below m) of one token or slot, from the
 // fp32 sums of the gate (or only) matrix and of the up matrix.
 template <int MODE, int G>
-__device__ __forceinline__ void finish4(const FfnArgs &a, int expert, int64_t row, int64_t r,
+__device__ __forceinline__ void finish4(const FfnArgs &a, int expert, int split, int64_t row, int64_t r,
                                         const f32x4 (&sum)[G]) {
+    if (MODE == kLinear && a.part) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r + e < a.m) a.part[((split * a.n + row) * G + g) * a.m + r + e] = sum[g][e];
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (r + e >= a.m) return;
@@ -267,10 +278,301 @@ __global__ void __launch_bounds__(kSimpleWaves * kWave) ffn_simple(const FfnArgs
 #pragma unroll
             for (int g = 0; g < G; ++g)
                 for (int w = 1; w < kSimpleWaves; ++w) acc[g] += red[((w - 1) * G + g) * kWave + lane];
-            if (tok_in) finish4<MODE, G>(a, expert, orow, row0 + 4 * kq, acc);
+            if (tok_in) finish4<MODE, G>(a, expert, 0, orow, row0 + 4 * kq, acc);
         }
         __syncthreads();
     }
+}
+
+// ---------------------------------------------------------------- stream kernel
+// 32 codes (16 bytes) and the two scale bytes 2 H, 2 H + 1 of s -> the four
+// operands of elements 0-7, 8-15 (first scale) and 16-23, 24-31 (second).
+template <bool BF16, int H>
+__device__ __forceinline__ void decode32(u32x4 q, uint32_t s, u32x4 (&o)[4]) {
+    if constexpr (BF16) {
+        const f32x2 v = e4m3x2_f32(s >> (16 * H));
+        o[0] = decode8(q.x, v.x);
+        o[1] = decode8(q.y, v.x);
+        o[2] = decode8(q.z, v.y);
+        o[3] = decode8(q.w, v.y);
+    } else {
+        const f16x2 v = e4m3x2_f16(s >> (16 * H));
+        const f16x2 a = {v.x, v.x}, b = {v.y, v.y};
+        o[0] = __builtin_bit_cast(u32x4, decode8(q.x, a));
+        o[1] = __builtin_bit_cast(u32x4, decode8(q.y, a));
+        o[2] = __builtin_bit_cast(u32x4, decode8(q.z, b));
+        o[3] = __builtin_bit_cast(u32x4, decode8(q.w, b));
+    }
+}
+
+constexpr int kWinCodeBytes = 2048, kWinScaleBytes = 256;   // of a packed window of a tile
+constexpr int kAnyRange = 0x7FFFFFF0;   // descriptor range where every used offset is known to be valid
+
+// The weights of one matrix as a workgroup reads them: R tiles of 16 rows from
+// row0, window by window (256 elements of K).  Lane i + 16 q holds, of row i of
+// each tile, the 64 elements from 64 q on: two 16-byte loads and their four
+// scales.  Rows past m and elements past k read zeros without touching memory.
+template <bool PACKED, int R>
+struct WeightTiles {
+    __amdgpu_buffer_rsrc_t wdesc, sdesc;
+    uint32_t code[R], scale[R];   // the lane's offsets at window 0 (or out of range)
+
+    __device__ __forceinline__ WeightTiles(const FfnArgs &a, int64_t matrix, int64_t row0, int li, int kq) {
+        if (PACKED) {
+            const int64_t wins = (a.k + kWinElems - 1) / kWinElems, tiles = (a.m + kTile - 1) / kTile;
+            const int64_t t0 = matrix * tiles + row0 / kTile;
+            wdesc = buffer_of(a.W + t0 * wins * kWinCodeBytes, kAnyRange);
+            sdesc = buffer_of(a.sW + t0 * wins * kWinScaleBytes, kAnyRange);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool in = row0 + r * kTile < a.m;
+                const uint32_t w = static_cast<uint32_t>(r * wins), lane = li + 16 * kq;
+                code[r] = in ? w * kWinCodeBytes + 16 * lane : kOutOfRange;
+                scale[r] = in ? w * kWinScaleBytes + 4 * lane : kOutOfRange;
+            }
+        } else {
+            wdesc = buffer_of(a.W + (matrix * a.m + row0) * (a.k / 2), kAnyRange);
+            sdesc = buffer_of(a.sW + (matrix * a.m + row0) * (a.k / 16), kAnyRange);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool in = row0 + r * kTile + li < a.m;
+                const uint32_t row = r * kTile + li;
+                code[r] = in ? row * static_cast<uint32_t>(a.k / 2) + 32 * kq : kOutOfRange;
+                scale[r] = in ? row * static_cast<uint32_t>(a.k / 16) + 4 * kq : kOutOfRange;
+            }
+        }
+    }
+    // `past`: kOutOfRange when the lane's elements lie past k, else 0
+    __device__ __forceinline__ void load(int r, uint32_t window, uint32_t past, u32x4 (&q)[2], uint32_t &s) const {
+        const uint32_t co = (code[r] + window * (PACKED ? kWinCodeBytes : 128)) | past;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            q[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 wdesc, co + h * (PACKED ? 1024 : 16), 0, kNonTemporal));
+        s = __builtin_amdgcn_raw_buffer_load_b32(sdesc, (scale[r] + window * (PACKED ? kWinScaleBytes : 16)) | past,
+                                                 0, PACKED ? kNonTemporal : 0);
+    }
+};
+
+// Orders a wave's own LDS writes before its later reads (and the reverse)
+// for the compiler; the hardware runs one wave's LDS operations in order.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// One workgroup owns R tiles of 16 rows of each of G matrices and up to 16
+// tokens at a time; its W waves take interleaved windows of 256 elements of K
+// of its part of K, U windows in flight each, and their sums are added in wave
+// order through LDS.  This is the shape for few tokens, where the weights'
+// bytes are the bound: every weight byte is read once, in 1 KiB instructions
+// (packed), and decoded once for all tokens.
+//
+// The tokens' elements of a window (512 bytes each) are read row by row, two
+// tokens per instruction, as far ahead as the weights, and go through a slot
+// of LDS that belongs to the wave, from where every lane reads its eight
+// 16-byte operand pieces: read straight from memory in operand order, each
+// instruction would touch a different line in every lane.  The 16-byte pieces
+// are swizzled by the token, so the 16 lanes that read the same piece of 16
+// tokens hit distinct banks.  NX = instructions = half the tokens staged.
+template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int W, int NX>
+__device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
+                                            int32_t end, u32x4 *lds) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int li = lane & 15, kq = lane >> 4;
+    const uint32_t k = static_cast<uint32_t>(a.k);
+    const int wins = static_cast<int>((k + kWinElems - 1) / kWinElems);
+    const int win0 = static_cast<int>(int64_t(split) * wins / a.splits);
+    const int nwin = static_cast<int>(int64_t(split + 1) * wins / a.splits) - win0;
+    const int niter = nwin > wave ? (nwin - wave + W - 1) / W : 0;
+
+    const WeightTiles<PACKED, R> w0(a, G * int64_t(expert), row0, li, kq);
+    const WeightTiles<PACKED, R> w1(a, G * int64_t(expert) + (G - 1), row0, li, kq);
+
+    // X: kLinear from token p0 on, else from row 0 (the host keeps rows * ldx in 31 bits)
+    const uint8_t *xbase = a.X + (MODE == kLinear ? 2 * (int64_t(p0) * a.ldx) : 0);
+    __amdgpu_buffer_rsrc_t xdesc[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) xdesc[p] = buffer_of(xbase + 2 * p * a.plane, kAnyRange);
+    uint32_t xo[NX];
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+        const int32_t t = p0 + 2 * j + (lane >> 5);
+        xo[j] = kOutOfRange;
+        if (t < end) {
+            const int32_t row = MODE == kLinear ? t - p0 : x_row<MODE>(a, out_row<MODE>(a, t));
+            xo[j] = 2 * static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldx) + 16 * (lane & 31);
+        }
+    }
+    u32x4 *slot = lds + wave * (P * 2 * NX * 32);
+    const int tok = li & (2 * NX - 1);   // columns past the staged tokens repeat them and are dropped
+
+    u32x4 wq[U][G][R][2], xq[U][P][NX];
+    uint32_t ws[U][G][R];
+    auto issue = [&](int i, int u) {
+        const uint32_t win = static_cast<uint32_t>(win0 + wave + W * i);
+        const bool run = i < niter;
+        const uint32_t xpast = run && win * kWinElems + 8 * (lane & 31) < k ? 0u : kOutOfRange;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int j = 0; j < NX; ++j)
+                xq[u][p][j] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(xdesc[p], (xo[j] + win * 512) | xpast, 0, 0));
+        const uint32_t past = run && win * kWinElems + 64 * kq < k ? 0u : kOutOfRange;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            w0.load(r, win, past, wq[u][0][r], ws[u][0][r]);
+            if constexpr (G == 2) w1.load(r, win, past, wq[u][1][r], ws[u][1][r]);
+        }
+    };
+    f32x4 acc[G][R] = {};
+    auto consume = [&](int u) {
+        wave_lds_fence();
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int j = 0; j < NX; ++j) {
+                const int t = 2 * j + (lane >> 5);
+                slot[(p * 2 * NX + t) * 32 + ((lane & 31) ^ (t & 15))] = xq[u][p][j];
+            }
+        wave_lds_fence();
+        auto half = [&](auto hc) {
+            constexpr int h = decltype(hc)::value;
+            u32x4 xv[P][4];
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) xv[p][c] = slot[(p * 2 * NX + tok) * 32 + ((8 * kq + 4 * h + c) ^ tok)];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    u32x4 wo[4];
+                    decode32<BF16, h>(wq[u][g][r][h], ws[u][g][r], wo);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[g][r] = mfma<BF16>(wo[c], xv[p][c], acc[g][r]);
+                }
+        };
+        half(std::integral_constant<int, 0>{});
+        half(std::integral_constant<int, 1>{});
+    };
+
+    phase_fence();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        issue(u, u);
+        phase_fence();
+    }
+    for (int i = 0; i < niter; i += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u < niter) consume(u);   // wave-uniform
+            issue(i + u + U, u);             // past the wave's windows: zeros, no traffic
+            phase_fence();
+        }
+    }
+
+    // sums of the waves, in wave order; wave r % W finishes row tile r
+    f32x4 *red = reinterpret_cast<f32x4 *>(lds);
+    if (W > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int r = 0; r < R; ++r) red[((wave * G + g) * R + r) * kWave + lane] = acc[g][r];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (W > 1 && r % W != wave) continue;
+        f32x4 sum[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            sum[g] = acc[g][r];
+            if (W > 1) {
+                sum[g] = red[(g * R + r) * kWave + lane];
+                for (int w = 1; w < W; ++w) sum[g] += red[((w * G + g) * R + r) * kWave + lane];
+            }
+        }
+        if (p0 + li < end && li < 2 * NX)
+            finish4<MODE, G>(a, expert, split, out_row<MODE>(a, p0 + li), row0 + r * kTile + 4 * kq, sum);
+    }
+    if (MODE != kLinear && W > 1) __syncthreads();   // before the next pass writes LDS
+}
+
+// LDS of a stream workgroup: the waves' slots, later their sums.
+template <int G, int P, int R, int W, int NX>
+constexpr int stream_lds() {
+    return W * kWave * (P * NX > G * R ? P * NX : G * R);
+}
+
+template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int W, int NXMAX>
+__global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
+    __shared__ u32x4 lds[stream_lds<G, P, R, W, NXMAX>()];
+    const uint32_t strips = static_cast<uint32_t>((a.m + R * kTile - 1) / (R * kTile));
+    const uint32_t q = blockIdx.x / strips;   // split, or expert
+    const int64_t row0 = int64_t(blockIdx.x - q * strips) * (R * kTile);
+    if constexpr (MODE == kLinear) {
+        stream_pass<BF16, PACKED, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q, 0, static_cast<int32_t>(a.n), lds);
+    } else {
+        const TokenRange range = expert_range<MODE>(a, q);
+        for (int32_t p = range.first; p < range.end; p += 2 * NXMAX) {
+            const int32_t end = range.end - p > 2 * NXMAX ? p + 2 * NXMAX : range.end;
+            const int n = end - p;   // workgroup-uniform
+            if (n <= 2)
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 1>(a, q, row0, 0, p, end, lds);
+            else if (n <= 4)
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 2>(a, q, row0, 0, p, end, lds);
+            else if (NXMAX == 4 || n <= 8)
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 4>(a, q, row0, 0, p, end, lds);
+            else
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, NXMAX>(a, q, row0, 0, p, end, lds);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- split sums
+constexpr int kFinishThreads = 256;
+
+// The epilogue of a linear layer whose K was split across workgroups: the
+// splits' sums in split order.  One thread per four rows of one token.
+template <int G>
+__global__ void __launch_bounds__(kFinishThreads) linear_finish(FfnArgs a) {
+    const int64_t quads = (a.m + 3) / 4;
+    const int64_t i = int64_t(blockIdx.x) * kFinishThreads + threadIdx.x;
+    if (i >= a.n * quads) return;
+    const int64_t row = i / quads, r = 4 * (i - row * quads);
+    const float *part = a.part;
+    a.part = nullptr;
+    f32x4 sum[G] = {};
+    for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r + e < a.m) sum[g][e] += part[((s * a.n + row) * G + g) * a.m + r + e];
+    finish4<kLinear, G>(a, 0, 0, row, r, sum);
+}
+
+// ---------------------------------------------------------------- alignment of X
+constexpr int kAlignThreads = 256;
+
+// Copies 16-bit rows with any stride and alignment to rows of k elements (a
+// multiple of 16) on 16-byte boundaries: one thread per 8 elements.
+__global__ void __launch_bounds__(kAlignThreads) align_rows(const uint16_t *x, int64_t ldx, uint16_t *y,
+                                                            int64_t rows, int64_t k) {
+    const int64_t pieces = k / 8;
+    const int64_t i = int64_t(blockIdx.x) * kAlignThreads + threadIdx.x;
+    if (i >= rows * pieces) return;
+    const int64_t row = i / pieces, e = 8 * (i - row * pieces);
+    uint16_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = x[row * ldx + e + j];
+    __builtin_memcpy(y + row * k + e, v, 16);
 }
 
 // ---------------------------------------------------------------- routing

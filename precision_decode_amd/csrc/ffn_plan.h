@@ -84,6 +84,41 @@ inline int check_moe_shape(const nvfp4_moe_layer_t &l, int64_t tokens) {
     return NVFP4_GEMV_OK;
 }
 
+// ---------------------------------------------------------------- linear
+constexpr int64_t kStreamTokens = 16;   // most tokens the stream kernel takes
+constexpr int64_t kComputeUnits = 256;  // CUs of an MI355X (8 XCDs x 32)
+constexpr int kStreamWaves = 8;
+
+// Row tiles per matrix of a stream workgroup of the linear layer.
+constexpr int stream_tiles(bool gated) { return gated ? 1 : 1; }
+
+struct LinearPlan {
+    bool stream;        // stream kernel, else the simple one
+    int64_t strips;     // workgroups along the rows
+    int64_t splits;     // workgroups along K
+    size_t part_bytes;  // split sums
+    size_t x_bytes;     // aligned copy of X
+    size_t ws_bytes() const { return ws_round(part_bytes) + ws_round(x_bytes); }
+};
+
+// `fast`: the weight's alignment and k allow the fast kernels; `x_aligned`: so
+// do X's rows.  K is split while the workgroups leave compute units idle and
+// every wave keeps a window of its own.
+inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool fast, bool x_aligned) {
+    LinearPlan p = {};
+    p.splits = 1;
+    p.stream = fast && n <= kStreamTokens;
+    if (!p.stream) return p;
+    p.strips = ceil_div(m, kTile * stream_tiles(gated));
+    const int64_t wins = ceil_div(k, kWinElems);
+    while (p.strips * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
+    if (p.splits > 1)
+        p.part_bytes = static_cast<size_t>(p.splits) * n * m * (gated ? 2 : 1) * sizeof(float);
+    if (!x_aligned) p.x_bytes = static_cast<size_t>(n) * k * 2;
+    return p;
+}
+
+// ---------------------------------------------------------------- MoE
 // Workspace of one MoE call, in bytes from its start.  The sizes go by the
 // larger (fp32 output) number of planes of h, so they do not depend on it.
 struct MoeWorkspace {
@@ -99,6 +134,7 @@ struct MoeWorkspace {
 };
 
 constexpr int kMaxPlanes = 3;
+constexpr int64_t kMaxStreamBytes = 0x7FFFFFF0;   // row offsets the stream kernel can form
 
 inline MoeWorkspace moe_workspace(const nvfp4_moe_layer_t &l, int64_t tokens) {
     const size_t slots = static_cast<size_t>(tokens) * l.topk;

@@ -117,18 +117,60 @@ int check_linear(const LinearCall &c) {
     return NVFP4_GEMV_OK;
 }
 
-template <bool BF16>
-int launch_linear(const FfnArgs &a, bool packed, bool gated, hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile)));
-    return gated ? launch_simple<BF16, 2, 1, kLinear>(a, packed, grid, stream)
-                 : launch_simple<BF16, 1, 1, kLinear>(a, packed, grid, stream);
+template <bool BF16, bool PACKED, int G, int NX>
+int launch_linear_stream(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
+    constexpr int R = stream_tiles(G == 2);
+    return run(ffn_stream<BF16, PACKED, G, 1, kLinear, R, 2, kStreamWaves, NX>,
+               dim3(static_cast<uint32_t>(p.strips * p.splits)), kStreamWaves * kWave, a, stream);
 }
 
-int linear(const LinearCall &c, hipStream_t stream) {
+template <bool BF16, bool PACKED, int G>
+int launch_linear(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
+    if (!p.stream)
+        return launch_simple<BF16, G, 1, kLinear>(
+            a, PACKED, dim3(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile))), stream);
+    return a.n <= 2   ? launch_linear_stream<BF16, PACKED, G, 1>(a, p, stream)
+           : a.n <= 4 ? launch_linear_stream<BF16, PACKED, G, 2>(a, p, stream)
+           : a.n <= 8 ? launch_linear_stream<BF16, PACKED, G, 4>(a, p, stream)
+                      : launch_linear_stream<BF16, PACKED, G, 8>(a, p, stream);
+}
+
+template <bool BF16>
+int launch_linear(const FfnArgs &a, const LinearPlan &p, bool packed, bool gated, hipStream_t stream) {
+    return packed ? gated ? launch_linear<BF16, true, 2>(a, p, stream) : launch_linear<BF16, true, 1>(a, p, stream)
+                  : gated ? launch_linear<BF16, false, 2>(a, p, stream) : launch_linear<BF16, false, 1>(a, p, stream);
+}
+
+// Whether the weight's pointers and K suit the fast kernels.
+bool fast_weight(const void *W, const void *sf, int64_t k) {
+    return k % 64 == 0 && !misaligned(W, 16) && !misaligned(sf, 4);
+}
+bool aligned_rows(const void *X, int64_t ldx) { return !misaligned(X, 16) && ldx % 8 == 0; }
+
+int copy_aligned(const void *X, int64_t ldx, void *to, int64_t rows, int64_t k, hipStream_t stream) {
+    const uint16_t *x = static_cast<const uint16_t *>(X);
+    uint16_t *y = static_cast<uint16_t *>(to);
+    void *args[] = {&x, &ldx, &y, &rows, &k};
+    return run(reinterpret_cast<const void *>(align_rows),
+               dim3(static_cast<uint32_t>(ceil_div(rows * (k / 8), kAlignThreads))), kAlignThreads, args, stream);
+}
+
+LinearPlan plan_of(const LinearCall &c) {
+    return plan_linear(c.n, c.m, c.k, c.gated(), fast_weight(c.W, c.sfW, c.k), aligned_rows(c.X, c.ldx));
+}
+
+int linear(const LinearCall &c, const LinearPlan &p, uint8_t *ws, hipStream_t stream) {
     if (c.n == 0) return NVFP4_GEMV_OK;
     FfnArgs a = {};
     a.X = static_cast<const uint8_t *>(c.X);
     a.ldx = c.ldx;
+    if (p.x_bytes > 0) {
+        uint8_t *x = ws + ws_round(p.part_bytes);
+        const int s = copy_aligned(c.X, c.ldx, x, c.n, c.k, stream);
+        if (s != NVFP4_GEMV_OK) return s;
+        a.X = x;
+        a.ldx = c.k;
+    }
     a.W = c.W;
     a.sW = c.sfW;
     a.alpha = c.alpha;
@@ -143,9 +185,15 @@ int linear(const LinearCall &c, hipStream_t stream) {
     a.topk = 1;
     a.act = c.activation & ~NVFP4_ACT_GATED;
     a.y_type = c.y_type;
+    a.splits = static_cast<int32_t>(p.splits);
+    a.part = p.part_bytes > 0 ? reinterpret_cast<float *>(ws) : nullptr;
     const bool packed = c.w_layout == NVFP4_W_PACKED;
-    return c.x_type == NVFP4_OUT_BF16 ? launch_linear<true>(a, packed, c.gated(), stream)
-                                      : launch_linear<false>(a, packed, c.gated(), stream);
+    const int s = c.x_type == NVFP4_OUT_BF16 ? launch_linear<true>(a, p, packed, c.gated(), stream)
+                                             : launch_linear<false>(a, p, packed, c.gated(), stream);
+    if (s != NVFP4_GEMV_OK || !a.part) return s;
+    const dim3 grid(static_cast<uint32_t>(ceil_div(c.n * ceil_div(c.m, 4), kFinishThreads)));
+    return c.gated() ? run(linear_finish<2>, grid, kFinishThreads, a, stream)
+                     : run(linear_finish<1>, grid, kFinishThreads, a, stream);
 }
 
 // ---------------------------------------------------------------- MoE
@@ -198,13 +246,33 @@ int check_moe(const MoeCall &c) {
     return NVFP4_GEMV_OK;
 }
 
+constexpr int kUpTiles = 2, kUpWaves = 4;       // per workgroup: row tiles of gate and of up, waves
+constexpr int kDownTiles = 4, kDownWaves = 2;
+
+template <bool BF16, bool PACKED>
+int stream_up(const FfnArgs &a, int64_t experts, hipStream_t stream) {
+    return run(ffn_stream<BF16, PACKED, 2, 1, kMoeUp, kUpTiles, 2, kUpWaves, 8>,
+               dim3(static_cast<uint32_t>(ceil_div(a.m, kUpTiles * kTile) * experts)), kUpWaves * kWave, a, stream);
+}
+
+template <bool PACKED, int P>
+int stream_down(const FfnArgs &a, int64_t experts, hipStream_t stream) {
+    return run(ffn_stream<true, PACKED, 1, P, kMoeDown, kDownTiles, 2, kDownWaves, 4>,
+               dim3(static_cast<uint32_t>(ceil_div(a.m, kDownTiles * kTile) * experts)), kDownWaves * kWave, a,
+               stream);
+}
+
 template <bool BF16>
-int launch_up(const FfnArgs &a, bool packed, int64_t experts, hipStream_t stream) {
+int launch_up(const FfnArgs &a, bool packed, bool fast, int64_t experts, hipStream_t stream) {
+    if (fast) return packed ? stream_up<BF16, true>(a, experts, stream) : stream_up<BF16, false>(a, experts, stream);
     const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * experts));
     return launch_simple<BF16, 2, 1, kMoeUp>(a, packed, grid, stream);
 }
 
-int launch_down(const FfnArgs &a, bool packed, int planes, int64_t experts, hipStream_t stream) {
+int launch_down(const FfnArgs &a, bool packed, bool fast, int planes, int64_t experts, hipStream_t stream) {
+    if (fast && planes == 2)
+        return packed ? stream_down<true, 2>(a, experts, stream) : stream_down<false, 2>(a, experts, stream);
+    if (fast) return packed ? stream_down<true, 3>(a, experts, stream) : stream_down<false, 3>(a, experts, stream);
     const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * experts));
     return planes == 2 ? launch_simple<true, 1, 2, kMoeDown>(a, packed, grid, stream)
                        : launch_simple<true, 1, 3, kMoeDown>(a, packed, grid, stream);
@@ -242,8 +310,17 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
 
     const int planes = c.y_type == NVFP4_OUT_F32 ? 3 : 2;
     FfnArgs a = {};
+    a.splits = 1;
     a.X = r.X;
     a.ldx = c.ldx;
+    bool fast = fast_weight(l.W13, l.sf13, l.hidden);
+    if (fast && !aligned_rows(c.X, c.ldx)) {
+        s = copy_aligned(c.X, c.ldx, ws + w.x, c.tokens, l.hidden, stream);
+        if (s != NVFP4_GEMV_OK) return s;
+        a.X = ws + w.x;
+        a.ldx = l.hidden;
+    }
+    fast = fast && c.tokens * a.ldx * 2 < kMaxStreamBytes;
     a.plane = slots * l.inter;
     a.W = l.W13;
     a.sW = l.sf13;
@@ -258,7 +335,8 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     a.topk = l.topk;
     a.act = l.activation;
     a.y_planes = planes;
-    s = bf16 ? launch_up<true>(a, packed, l.experts, stream) : launch_up<false>(a, packed, l.experts, stream);
+    s = bf16 ? launch_up<true>(a, packed, fast, l.experts, stream)
+             : launch_up<false>(a, packed, fast, l.experts, stream);
     if (s != NVFP4_GEMV_OK) return s;
 
     a.X = ws + w.h;
@@ -270,7 +348,8 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     a.ldy = l.hidden;
     a.m = l.hidden;
     a.k = l.inter;
-    s = launch_down(a, packed, planes, l.experts, stream);
+    fast = fast_weight(l.W2, l.sf2, l.inter) && slots * l.inter * 2 < kMaxStreamBytes;
+    s = launch_down(a, packed, fast, planes, l.experts, stream);
     if (s != NVFP4_GEMV_OK) return s;
 
     CombineArgs y = {};
@@ -314,9 +393,8 @@ int check_workspace(const void *ws, size_t bytes, size_t need) {
 extern "C" {
 
 size_t nvfp4_linear_workspace_size(int64_t n, int64_t m, int64_t k, int32_t activation) {
-    (void)activation;
     if (check_linear_shape(n, m, k, NVFP4_W_ROW_MAJOR) != NVFP4_GEMV_OK) return 0;
-    return 0;
+    return plan_linear(n, m, k, (activation & NVFP4_ACT_GATED) != 0, k % 64 == 0, false).ws_bytes();
 }
 
 int nvfp4_linear_launch_ws(const void *X, int32_t x_type, int64_t ldx, const uint8_t *W,
@@ -326,19 +404,27 @@ int nvfp4_linear_launch_ws(const void *X, int32_t x_type, int64_t ldx, const uin
                            size_t workspace_bytes, void *stream) {
     const LinearCall c = {X, x_type, ldx, W, sfW, w_layout, alpha, bias, residual, ldr,
                           Y, y_type, ldy, n, m, k, activation};
-    const int s = check_linear(c);
+    int s = check_linear(c);
     if (s != NVFP4_GEMV_OK) return s;
-    (void)workspace;
-    (void)workspace_bytes;
-    return linear(c, static_cast<hipStream_t>(stream));
+    const LinearPlan p = plan_of(c);
+    s = check_workspace(workspace, workspace_bytes, p.ws_bytes());
+    if (s != NVFP4_GEMV_OK) return s;
+    return linear(c, p, static_cast<uint8_t *>(workspace), static_cast<hipStream_t>(stream));
 }
 
 int nvfp4_linear_launch(const void *X, int32_t x_type, int64_t ldx, const uint8_t *W,
                         const uint8_t *sfW, int32_t w_layout, const float *alpha, const float *bias,
                         const void *residual, int64_t ldr, void *Y, int32_t y_type, int64_t ldy,
                         int64_t n, int64_t m, int64_t k, int32_t activation, void *stream) {
-    return nvfp4_linear_launch_ws(X, x_type, ldx, W, sfW, w_layout, alpha, bias, residual, ldr, Y, y_type,
-                                  ldy, n, m, k, activation, nullptr, 0, stream);
+    const LinearCall c = {X, x_type, ldx, W, sfW, w_layout, alpha, bias, residual, ldr,
+                          Y, y_type, ldy, n, m, k, activation};
+    int s = check_linear(c);
+    if (s != NVFP4_GEMV_OK) return s;
+    const LinearPlan p = plan_of(c);
+    void *ws;
+    s = owned_workspace(p.ws_bytes(), stream, &ws);
+    if (s != NVFP4_GEMV_OK) return s;
+    return linear(c, p, static_cast<uint8_t *>(ws), static_cast<hipStream_t>(stream));
 }
 
 size_t nvfp4_moe_layer_workspace_size(const nvfp4_moe_layer_t *layer, int64_t tokens) {
