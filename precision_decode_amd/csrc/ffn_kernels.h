@@ -9,6 +9,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "device_common.h"
 #include "ffn_plan.h"
@@ -48,21 +49,58 @@ struct FfnArgs {
     int32_t y_planes;           // kMoeUp: planes of h to write
     float *part;                // kLinear with K split: [split][n][matrices][m] sums, or NULL
     int32_t splits;             // workgroups along K
+    int32_t vec;                // kLinear: rows of Y and of the residual start on 16-byte boundaries
 };
 
 // ---------------------------------------------------------------- arithmetic
+// exp(x) and 1 / x by the hardware's instructions (one unit in the last place
+// each; exp errs by |x| 2^-24 more, which every use below multiplies by a result
+// that falls with |x|).
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(1.44269504f * x); }
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// The normal distribution function: with a = |z| / sqrt 2 its smaller side is
+// erfc(a) / 2 = exp(-z^2 / 2) (exp(a^2) erfc(a)) / 2, and exp(a^2) erfc(a) is, to
+// 2e-8 of itself up to a = 4 and as far as exp(-a^2) lets it matter beyond, a
+// polynomial of degree 9 in t = 1 / (1 + 0.4 a) without a constant term: a
+// weighted least-squares fit, reweighted until the error is level.
+__device__ __forceinline__ float normal_cdf(float z) {
+    const float t = fast_rcp(__builtin_fmaf(0.4f * 0.70710678f, __builtin_fabsf(z), 1.0f));
+    constexpr float c[9] = {0.22539076f, 0.23008046f, 0.17877823f, 0.27498057f, -0.09545095f,
+                            0.32257387f, -0.10755151f, -0.05302797f, 0.02422655f};
+    float p = c[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i) p = __builtin_fmaf(p, t, c[i]);
+    const float tail = 0.5f * p * t * fast_exp(-0.5f * z * z);
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
 // f of nvfp4_ffn.h in fp32.
 __device__ __forceinline__ float activate(int act, float z) {
     switch (act) {
     case NVFP4_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
-    case NVFP4_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
+    case NVFP4_ACT_GELU: return z * normal_cdf(z);
     case NVFP4_ACT_GELU_TANH: {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
         const float u = 0.79788456f * (z + 0.044715f * z * z * z);
-        return z / (1.0f + expf(-2.0f * u));
+        return z * fast_rcp(1.0f + fast_exp(-2.0f * u));
     }
-    case NVFP4_ACT_SILU: return z / (1.0f + expf(-z));
+    case NVFP4_ACT_SILU: return z * fast_rcp(1.0f + fast_exp(-z));
     default: return z;
+    }
+}
+
+__device__ __forceinline__ void activate8(int act, float (&z)[8]) {
+    auto all = [&](auto kind) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = activate(decltype(kind)::value, z[e]);
+    };
+    switch (act) {
+    case NVFP4_ACT_RELU: return all(std::integral_constant<int, NVFP4_ACT_RELU>{});
+    case NVFP4_ACT_GELU: return all(std::integral_constant<int, NVFP4_ACT_GELU>{});
+    case NVFP4_ACT_GELU_TANH: return all(std::integral_constant<int, NVFP4_ACT_GELU_TANH>{});
+    case NVFP4_ACT_SILU: return all(std::integral_constant<int, NVFP4_ACT_SILU>{});
+    default: return;
     }
 }
 
@@ -342,15 +380,23 @@ struct WeightTiles {
             }
         }
     }
-    // `past`: kOutOfRange when the lane's elements lie past k, else 0
+    // `past`: kOutOfRange when the lane's elements lie past k, else 0.  POLICY:
+    // kNonTemporal for weights that are read once.
+    template <int POLICY>
+    __device__ __forceinline__ void load_half(int r, uint32_t window, uint32_t past, int h, u32x4 &q) const {
+        q = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                          wdesc, (code[r] | past) + h * (PACKED ? 1024 : 16),
+                                          window * (PACKED ? kWinCodeBytes : 128), POLICY));
+    }
+    template <int POLICY>
+    __device__ __forceinline__ void load_scale(int r, uint32_t window, uint32_t past, uint32_t &s) const {
+        s = __builtin_amdgcn_raw_buffer_load_b32(sdesc, scale[r] | past, window * (PACKED ? kWinScaleBytes : 16),
+                                                 POLICY);
+    }
     __device__ __forceinline__ void load(int r, uint32_t window, uint32_t past, u32x4 (&q)[2], uint32_t &s) const {
-        const uint32_t co = (code[r] + window * (PACKED ? kWinCodeBytes : 128)) | past;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            q[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 wdesc, co + h * (PACKED ? 1024 : 16), 0, kNonTemporal));
-        s = __builtin_amdgcn_raw_buffer_load_b32(sdesc, (scale[r] + window * (PACKED ? kWinScaleBytes : 16)) | past,
-                                                 0, PACKED ? kNonTemporal : 0);
+        load_half<kNonTemporal>(r, window, past, 0, q[0]);
+        load_half<kNonTemporal>(r, window, past, 1, q[1]);
+        load_scale<PACKED ? kNonTemporal : 0>(r, window, past, s);
     }
 };
 
@@ -535,6 +581,393 @@ __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
     }
 }
 
+// ---------------------------------------------------------------- tile kernel
+// 8 consecutive values of a row of Y's type; `whole`: all 8 exist and the row
+// starts on a 16-byte boundary.
+struct Row8 {
+    u32x4 v[2];
+};
+__device__ __forceinline__ Row8 load_row8(const void *p, int64_t i, int type) {
+    Row8 o;
+    if (type == NVFP4_OUT_F32) {
+        const u32x4 *from = reinterpret_cast<const u32x4 *>(static_cast<const float *>(p) + i);
+        o.v[0] = from[0];
+        o.v[1] = from[1];
+    } else {
+        o.v[0] = o.v[1] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + i);
+    }
+    return o;
+}
+__device__ __forceinline__ void add_row8(const Row8 &o, int type, float (&z)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t w = o.v[0][e / 2];
+        const uint16_t b = static_cast<uint16_t>(w >> (16 * (e & 1)));
+        z[e] += type == NVFP4_OUT_F32 ? __builtin_bit_cast(float, uint32_t(o.v[e / 4][e % 4]))
+                : type == NVFP4_OUT_BF16 ? bf16_value(b)
+                                         : static_cast<float>(__builtin_bit_cast(_Float16, b));
+    }
+}
+__device__ __forceinline__ uint32_t round16x2(float lo, float hi, bool bf16) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    if (bf16) return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
+    return bits(f16x2{static_cast<_Float16>(lo), static_cast<_Float16>(hi)});
+}
+__device__ __forceinline__ void store_row8(void *p, int64_t i, int type, const float (&z)[8]) {
+    if (type == NVFP4_OUT_F32) {
+        f32x4 *to = reinterpret_cast<f32x4 *>(static_cast<float *>(p) + i);
+        to[0] = f32x4{z[0], z[1], z[2], z[3]};
+        to[1] = f32x4{z[4], z[5], z[6], z[7]};
+        return;
+    }
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = round16x2(z[2 * e], z[2 * e + 1], type == NVFP4_OUT_BF16);
+    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = o;
+}
+
+// Orders the workgroup's LDS accesses around the barrier and leaves global
+// loads in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Word c (elements 8 c .. 8 c + 7) of a lane's 32 codes; v: the two block scales
+// of the 32 elements.
+template <bool BF16>
+__device__ __forceinline__ u32x4 decode_word(u32x4 q, int c, f32x2 v) {
+    if constexpr (BF16) return decode8(q[c], c < 2 ? v.x : v.y);
+    else {
+        const _Float16 s = static_cast<_Float16>(c < 2 ? v.x : v.y);
+        return __builtin_bit_cast(u32x4, decode8(q[c], f16x2{s, s}));
+    }
+}
+
+constexpr int kStageElems = 128;    // K elements of one stage: half of every lane's part of a window
+constexpr int kXcds = 8;            // dies, each with its own L2; workgroup i runs on die i % 8
+
+template <typename F, int... I>
+__device__ __forceinline__ void each_tile(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+typedef __attribute__((address_space(3))) char lds_void_t;
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+template <int G, int Q, int NT, int WM, int WN, int WK>
+struct TileShape {
+    static constexpr int waves = WM * WN * WK;
+    static constexpr int rows = kTile * Q * WM;       // of each matrix
+    static constexpr int tokens = kTile * NT * WN;
+    static constexpr int stage = tokens * kStageElems / 8;             // 16-byte pieces
+    static constexpr int stride = kTile * Q * G * 4 + 16;              // bytes of a token in the epilogue
+    static constexpr int out_tiles = Q == 1 ? 2 : 1;                   // token tiles a wave's epilogue takes at a time
+    static constexpr int wave_out = out_tiles * kTile * stride;        // bytes of them
+    static constexpr int out_waves = WM * WN * (WK < NT / out_tiles ? WK : NT / out_tiles);   // waves that have any
+};
+
+// More than 16 tokens.  A workgroup owns 16 Q WM rows of each of G matrices and
+// 16 NT WN tokens; WK groups of WM x WN waves take the windows of K in turn and
+// add their sums through LDS at the end.  A wave holds the sums of G Q row tiles
+// by NT token tiles.
+//
+// Weights go from memory straight into the registers of the wave that owns their
+// rows, in 1 KiB instructions (packed), and are decoded there, once for all NT
+// token tiles, between the matrix instructions: 16 (bf16) or 8 (fp16) VALU
+// operations per operand, against NT matrix instructions of 16 cycles.  The
+// tokens go through LDS, in stages of half a window (128 elements), copied there
+// directly while the other of two buffers is multiplied: a token's 16 pieces of
+// 16 bytes lie in positions xored with its number, so that the 16 lanes that read
+// the same piece of 16 tokens hit distinct banks.  Two buffers are two variables:
+// in one, every read would wait for the copies into the other half.
+//
+// 4096 tokens x (4096 x 7168), bf16, in 256 x 128 tiles: 227 us, 1.06 PFLOP/s
+// (fp16 211 us), where a library's bf16 product reaches 1.54.  Without the loads
+// and the decode, so with matrix instructions and LDS reads alone, the same loop
+// takes 180 us, without the LDS reads 167: the matrix cores do not sustain their
+// nominal rate on such operands, and what the kernel adds is 20 us for the
+// tokens' copies, 15 for the weights' loads and 12-25 for the decode.  Tiles of
+// 256 x 256, whose 128 sums per lane leave too few registers to decode ahead,
+// took 236-263 us.
+template <bool BF16, bool PACKED, int G, int Q, int NT, int WM, int WN, int WK>
+__device__ __forceinline__ void tile_product(const FfnArgs &a) {
+    using S = TileShape<G, Q, NT, WM, WN, WK>;
+    constexpr int RT = G * Q;
+    static_assert(S::out_waves * S::wave_out <= 2 * 16 * S::stage * WK && S::out_waves % 2 == 0, "the epilogue fits");
+    static_assert(WK == 1 || (S::waves * NT * kWave <= S::stage * WK && RT <= 2), "the groups' sums fit");
+    __shared__ u32x4 lds0[WK * S::stage], lds1[WK * S::stage];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int li = lane & 15, kq = lane >> 4;
+    const int wm = wave % WM, wn = wave / WM % WN, kg = wave / (WM * WN);
+    const int gwave = wave % (WM * WN);   // wave of its group
+    const uint32_t k = static_cast<uint32_t>(a.k);
+
+    // Workgroup -> (split, strip of rows, block of tokens): every die takes a
+    // run of consecutive tiles, ordered in bands of four token blocks, so that
+    // its L2 serves few different rows and tokens.
+    const uint32_t strips = static_cast<uint32_t>((a.m + S::rows - 1) / S::rows);
+    const uint32_t blocks = static_cast<uint32_t>((a.n + S::tokens - 1) / S::tokens);
+    const uint32_t total = gridDim.x, die = blockIdx.x % kXcds;
+    uint32_t id = die * (total / kXcds) + (die < total % kXcds ? die : total % kXcds) + blockIdx.x / kXcds;
+    const int split = static_cast<int>(id / (strips * blocks));
+    id -= split * strips * blocks;
+    const uint32_t band = id / (4 * strips), width = blocks - 4 * band < 4 ? blocks - 4 * band : 4;
+    id -= 4 * band * strips;
+    const int64_t row0 = int64_t(id / width) * S::rows + kTile * Q * wm;
+    const int64_t tok0 = int64_t(4 * band + id % width) * S::tokens;
+
+    const int wins = static_cast<int>((k + kWinElems - 1) / kWinElems);
+    const int win0 = static_cast<int>(int64_t(split) * wins / a.splits);
+    const int win1 = static_cast<int>(int64_t(split + 1) * wins / a.splits);
+
+    const WeightTiles<PACKED, Q> w0(a, 0, row0, li, kq);
+    const WeightTiles<PACKED, Q> w1(a, G - 1, row0, li, kq);
+
+    // staging: copy i of 4 tokens: lane l fills position l % 16 of token t = 4 i + l / 16
+    // with piece (l % 16) ^ (t & 15); piece 4 q + c holds elements 64 q + 32 h + 8 c
+    // of the window
+    constexpr int kCopies = S::tokens / 4 / (WM * WN);
+    static_assert(S::tokens % (4 * WM * WN) == 0, "whole copies per wave");
+    const __amdgpu_buffer_rsrc_t xdesc = buffer_of(a.X + 2 * (tok0 * a.ldx), kAnyRange);
+    const int tlast = a.n - tok0 < S::tokens ? static_cast<int>(a.n - tok0) - 1 : S::tokens - 1;
+    const int piece = li ^ ((4 * kCopies * gwave + kq) & 15);
+    uint32_t xo[kCopies];   // rows past the last repeat it and are not stored
+#pragma unroll
+    for (int j = 0; j < kCopies; ++j) {
+        const int t = 4 * (kCopies * gwave + j) + kq;
+        xo[j] = 2 * ((t < tlast ? t : tlast) * static_cast<uint32_t>(a.ldx) +
+                     64 * ((piece >> 2) ^ (j & 3)) + 8 * (piece & 3));
+    }
+    u32x4 wq[2][RT];
+    uint32_t ws[2][RT];
+    auto load = [&](auto hc, int win, int slot) {
+        constexpr int h = decltype(hc)::value;
+        const int left = win < win1 ? static_cast<int>(k - win * kWinElems) : 0;   // elements from this window on
+        lds_void_t *to = h == 0 ? (lds_void_t *)lds0 : (lds_void_t *)lds1;
+        const uint32_t past = 64 * kq < left ? 0u : kOutOfRange;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const WeightTiles<PACKED, Q> &w = r < Q ? w0 : w1;
+            w.template load_half<0>(r % Q, win, past, h, wq[h][r]);
+            if (h == 0) w.template load_scale<0>(r % Q, win, past, ws[slot][r]);
+        }
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                xdesc, to + 16 * S::stage * kg + 1024 * (kCopies * gwave + j), 16,
+                xo[j] | (64 * ((piece >> 2) ^ (j & 3)) < left ? 0u : kOutOfRange),
+                2 * (win * kWinElems + 32 * h), 0, 0);
+    };
+    f32x4 acc[RT][NT] = {};
+    // Operands of this step of 32 elements and, where the registers allow it, of
+    // the next.
+    constexpr bool kAhead = RT * NT <= 16;
+    u32x4 wo[kAhead ? 2 : 1][RT];
+    auto decode = [&](u32x4 q, int c, int h, uint32_t s, u32x4 &o) {
+        const uint32_t b = s >> (16 * h + 8 * (c / 2));
+        if constexpr (BF16) {
+            o = decode8(q[c], e4m3x2_f32(b).x);
+        } else {
+            const f16x2 v = e4m3x2_f16(b);
+            o = __builtin_bit_cast(u32x4, decode8(q[c], f16x2{v.x, v.x}));
+        }
+        __asm__ volatile("" : "+v"(o));
+    };
+    // One stage: 4 steps of 32 elements, each in groups of two token tiles.  A
+    // group reads the next group's tokens and, kAhead, decodes part of the next
+    // step's weights (of the next stage's first one at the end) between its
+    // products.
+    auto compute = [&](auto hc) {
+        constexpr int h = decltype(hc)::value;
+        constexpr int kPairs = NT / 2;
+        u32x4 xv[2][2];
+        auto read = [&](int c, int t, u32x4 &to) {
+            to = (h == 0 ? lds0 : lds1)[S::stage * kg + 16 * (16 * (wn * NT + t) + li) + ((4 * kq + c) ^ li)];
+        };
+        read(0, 0, xv[0][0]);
+        read(0, 1, xv[0][1]);
+        phase_fence();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (!kAhead)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) decode(wq[h][r], c, h, ws[0][r], wo[0][r]);
+#pragma unroll
+            for (int t = 0; t < kPairs; ++t) {
+                const int g = (c * kPairs + t) & 1;
+                if (t + 1 < kPairs || c + 1 < 4) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        read(t + 1 < kPairs ? c : c + 1, t + 1 < kPairs ? 2 * (t + 1) + i : i, xv[g ^ 1][i]);
+                }
+                if (kAhead)
+#pragma unroll
+                    for (int r = RT * t / kPairs; r < RT * (t + 1) / kPairs; ++r) {
+                        if (c < 3) decode(wq[h][r], c + 1, h, ws[0][r], wo[(c + 1) & 1][r]);
+                        else decode(wq[1 - h][r], 0, 1 - h, ws[h][r], wo[0][r]);
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        acc[r][2 * t + i] = mfma<BF16>(wo[kAhead ? c & 1 : 0][r], xv[g][i], acc[r][2 * t + i]);
+                if (kAhead) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+                    for (int i = 0; i < 2 * RT; ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, BF16 ? 4 : 2, 0);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) __asm__ volatile("" : "+v"(acc[r][2 * t + i]));
+                phase_fence();
+            }
+        }
+    };
+    constexpr auto h0 = std::integral_constant<int, 0>{};
+    constexpr auto h1 = std::integral_constant<int, 1>{};
+    // the groups of waves take the windows in turn; all make the same number of
+    // rounds, past the last window on zeros
+    load(h0, win0 + kg, 0);
+    wait_vmcnt<0>();
+#pragma unroll
+    for (int r = 0; r < (kAhead ? RT : 0); ++r) decode(wq[0][r], 0, 0, ws[0][r], wo[0][r]);
+    lds_barrier();
+    for (int win = win0 + kg; win < win1 + kg; win += WK) {
+        load(h1, win, 0);
+        phase_fence();
+        compute(h0);
+        wait_vmcnt<0>();
+        lds_barrier();
+        load(h0, win + WK, 1);
+        phase_fence();
+        compute(h1);
+        wait_vmcnt<0>();
+#pragma unroll
+        for (int r = 0; r < RT; ++r) ws[0][r] = ws[1][r];
+        lds_barrier();
+    }
+    if (WK > 1) {
+        // each group's sums to LDS; then every group adds those of its token tiles
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                reinterpret_cast<f32x4 *>(r == 0 ? lds0 : lds1)[(wave * NT + t) * kWave + lane] = acc[r][t];
+        lds_barrier();
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t / S::out_tiles % WK != kg) continue;
+                const f32x4 *from = reinterpret_cast<const f32x4 *>(r == 0 ? lds0 : lds1) + (gwave * NT + t) * kWave + lane;
+                f32x4 sum = from[0];
+#pragma unroll
+                for (int i = 1; i < WK; ++i) sum += from[i * WM * WN * NT * kWave];
+                acc[r][t] = sum;
+            }
+        lds_barrier();
+    }
+
+    // Epilogue.  The sums go through LDS, which turns them into rows of 8
+    // consecutive outputs of one token: each wave has its own part and takes
+    // out_tiles token tiles at a time, with the residual of the next already on
+    // its way.
+    uint8_t *out = reinterpret_cast<uint8_t *>(2 * wave < S::out_waves ? lds0 : lds1) + wave % (S::out_waves / 2) * S::wave_out;
+    constexpr int kGroups = 2 * Q;                       // groups of 8 rows of a matrix
+    constexpr int kStep = kWave / kGroups;               // tokens per iteration
+    constexpr int kIters = S::out_tiles * kTile / kStep;
+    const int64_t r = row0 + 8 * (lane % kGroups);
+    const int64_t first = tok0 + kTile * NT * wn + lane / kGroups;   // the lane's first token
+    const int rows = a.m - r < 8 ? static_cast<int>(a.m - r) : 8;    // of the lane's 8, those that exist
+    const bool vec = a.vec != 0 && rows == 8;
+    const float al = a.alpha ? a.alpha[0] : 1.0f, au = G == 2 && a.alpha ? a.alpha[1] : 1.0f;
+    float b[G][8];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[g][e] = a.bias && e < rows ? a.bias[g * a.m + r + e] : 0.0f;
+    Row8 res[2][kIters];
+    auto fetch = [&](int t, Row8 (&to)[kIters]) {
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const int64_t row = first + kTile * t + kStep * i;
+            if (a.residual && vec && t < NT && row < a.n) to[i] = load_row8(a.residual, row * a.ldr + r, a.y_type);
+        }
+    };
+    if (!a.part) fetch(S::out_tiles * kg, res[0]);
+#pragma unroll 1
+    for (int t = S::out_tiles * kg; t < NT; t += S::out_tiles * WK) {
+        wave_lds_fence();
+        // the sums are picked by constant indices: any other would put them in memory
+        each_tile([&](auto tc) {
+            constexpr int T = decltype(tc)::value;
+            if (t != T - T % S::out_tiles) return;
+#pragma unroll
+            for (int q = 0; q < RT; ++q)
+                *reinterpret_cast<f32x4 *>(out + (T % S::out_tiles * kTile + li) * S::stride +
+                                           4 * (kTile * q + 4 * kq)) = acc[q][T];
+        }, std::make_integer_sequence<int, NT>{});
+        wave_lds_fence();
+        if (!a.part) fetch(t + S::out_tiles * WK, res[1]);
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const int64_t row = first + kTile * t + kStep * i;
+            if (row >= a.n || rows <= 0) continue;
+            float z[8], u[8];
+            const uint8_t *from = out + (lane / kGroups + kStep * i) * S::stride + 32 * (lane % kGroups);
+            __builtin_memcpy(z, from, 32);
+            if (G == 2) __builtin_memcpy(u, from + 4 * kTile * Q, 32);
+            if (a.part) {
+                float *to = a.part + ((split * a.n + row) * G) * a.m + r;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float(&v)[8] = g == 0 ? z : u;
+                    if (a.m % 4 == 0 && rows == 8) {
+                        store_row8(to, g * a.m, NVFP4_OUT_F32, v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < rows) to[g * a.m + e] = v[e];
+                    }
+                }
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = z[e] * al + b[0][e];
+            activate8(a.act, z);
+            if constexpr (G == 2)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] *= u[e] * au + b[1][e];
+            if (vec) {
+                if (a.residual) add_row8(res[0][i], a.y_type, z);
+                store_row8(a.Y, row * a.ldy + r, a.y_type, z);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < rows) {
+                    if (a.residual) z[e] += load_as_float(a.residual, row * a.ldr + r + e, a.y_type);
+                    store_rounded(a.Y, row * a.ldy + r + e, a.y_type, z[e]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) res[0][i] = res[1][i];
+    }
+}
+
+template <bool BF16, bool PACKED, int G, int Q, int NT, int WM, int WN, int WK>
+__global__ void __launch_bounds__(WM *WN *WK *kWave, 2) ffn_tile(const FfnArgs a) {
+    tile_product<BF16, PACKED, G, Q, NT, WM, WN, WK>(a);
+}
+
 // ---------------------------------------------------------------- split sums
 constexpr int kFinishThreads = 256;
 
@@ -546,15 +979,22 @@ __global__ void __launch_bounds__(kFinishThreads) linear_finish(FfnArgs a) {
     const int64_t i = int64_t(blockIdx.x) * kFinishThreads + threadIdx.x;
     if (i >= a.n * quads) return;
     const int64_t row = i / quads, r = 4 * (i - row * quads);
-    const float *part = a.part;
+    const float *part = a.part + row * G * a.m + r;
     a.part = nullptr;
     f32x4 sum[G] = {};
-    for (int s = 0; s < a.splits; ++s)
+    if (a.m % 4 == 0) {
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s)
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+            for (int g = 0; g < G; ++g) sum[g] += *reinterpret_cast<const f32x4 *>(part + (s * a.n * G + g) * a.m);
+    } else {
+        for (int s = 0; s < a.splits; ++s)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (r + e < a.m) sum[g][e] += part[((s * a.n + row) * G + g) * a.m + r + e];
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (r + e < a.m) sum[g][e] += part[(s * a.n * G + g) * a.m + e];
+    }
     finish4<kLinear, G>(a, 0, 0, row, r, sum);
 }
 

@@ -92,9 +92,27 @@ constexpr int kStreamWaves = 8;
 // Row tiles per matrix of a stream workgroup of the linear layer.
 constexpr int stream_tiles(bool gated) { return gated ? 1 : 1; }
 
+// Shapes of the tile kernel, largest first.  A workgroup owns rows() rows of each
+// matrix and tokens() tokens; its wk groups of wm waves take the windows of K in
+// turn.  A wave holds q row tiles of each matrix times nt token tiles.
+struct TileKind {
+    int q, nt, wm, wk;
+    constexpr int rows() const { return kTile * q * wm; }
+    constexpr int tokens() const { return kTile * nt; }
+    constexpr int waves() const { return wm * wk; }
+};
+constexpr TileKind kTileKinds[] = {{2, 8, 8, 1}, {2, 8, 4, 2}, {2, 4, 4, 2}, {1, 4, 4, 2}, {1, 2, 4, 2}};
+// two matrices: half the rows of each, so that a wave holds as many sums
+constexpr TileKind kGatedTileKinds[] = {{1, 8, 8, 1}, {1, 8, 4, 2}, {1, 4, 4, 2}, {1, 2, 4, 2}};
+constexpr int kNumTileKinds = 5, kNumGatedTileKinds = 4;
+constexpr int64_t kEnoughTiles = 192;   // three quarters of the compute units busy
+constexpr int64_t kTileSplitWins = 14;  // fewest windows of a workgroup for which a split of K pays
+
 struct LinearPlan {
-    bool stream;        // stream kernel, else the simple one
+    bool stream;        // stream kernel
+    int tile;           // shape of the tile kernel, or -1; neither: the simple kernel
     int64_t strips;     // workgroups along the rows
+    int64_t blocks;     // workgroups along the tokens
     int64_t splits;     // workgroups along K
     size_t part_bytes;  // split sums
     size_t x_bytes;     // aligned copy of X
@@ -102,16 +120,38 @@ struct LinearPlan {
 };
 
 // `fast`: the weight's alignment and k allow the fast kernels; `x_aligned`: so
-// do X's rows.  K is split while the workgroups leave compute units idle and
-// every wave keeps a window of its own.
+// do X's rows.  Up to 16 tokens: the stream kernel, K split while the workgroups
+// leave compute units idle and every wave keeps a window of its own.  More: the
+// tile kernel in the largest shape that keeps three quarters of the compute
+// units busy (a larger tile reads and decodes less per product; 7168 x 4096
+// weights in us with tiles of 256 x 128, 128 x 128, 128 x 64, 64 x 64:
+// 256 tokens 96, 60, 37, 32; 512 tokens 96, 61, 41, 50; 1024 tokens 98, 70, 72,
+// 93; 4096 tokens 225, 264, -, -), else in the smallest with K split while
+// every workgroup keeps 14 windows (64 tokens, 28 windows: 20.7 us whole, 17.8
+// in two; 32 tokens, 7168 rows, 8 windows: 9.4 us whole, 12.4 in two, since the
+// sums go through memory and a second kernel).
 inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool fast, bool x_aligned) {
     LinearPlan p = {};
     p.splits = 1;
-    p.stream = fast && n <= kStreamTokens;
-    if (!p.stream) return p;
-    p.strips = ceil_div(m, kTile * stream_tiles(gated));
+    p.tile = -1;
+    if (!fast || n == 0) return p;
     const int64_t wins = ceil_div(k, kWinElems);
-    while (p.strips * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
+    p.stream = n <= kStreamTokens;
+    if (p.stream) {
+        p.strips = ceil_div(m, kTile * stream_tiles(gated));
+        p.blocks = 1;
+        while (p.strips * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
+    } else {
+        const int kinds = gated ? kNumGatedTileKinds : kNumTileKinds;
+        for (p.tile = 0;; ++p.tile) {
+            const TileKind &t = gated ? kGatedTileKinds[p.tile] : kTileKinds[p.tile];
+            p.strips = ceil_div(m, t.rows());
+            p.blocks = ceil_div(n, t.tokens());
+            if (p.tile == kinds - 1 || p.strips * p.blocks >= kEnoughTiles) break;
+        }
+        while (p.strips * p.blocks * p.splits < kEnoughTiles && wins >= 2 * p.splits * kTileSplitWins)
+            p.splits *= 2;
+    }
     if (p.splits > 1)
         p.part_bytes = static_cast<size_t>(p.splits) * n * m * (gated ? 2 : 1) * sizeof(float);
     if (!x_aligned) p.x_bytes = static_cast<size_t>(n) * k * 2;

@@ -124,15 +124,30 @@ int launch_linear_stream(const FfnArgs &a, const LinearPlan &p, hipStream_t stre
                dim3(static_cast<uint32_t>(p.strips * p.splits)), kStreamWaves * kWave, a, stream);
 }
 
+template <bool BF16, bool PACKED, int G, int KIND>
+int launch_tile(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
+    constexpr TileKind t = G == 2 ? kGatedTileKinds[KIND % kNumGatedTileKinds] : kTileKinds[KIND];
+    return run(ffn_tile<BF16, PACKED, G, t.q, t.nt, t.wm, 1, t.wk>,
+               dim3(static_cast<uint32_t>(p.strips * p.blocks * p.splits)), t.waves() * kWave, a, stream);
+}
+
 template <bool BF16, bool PACKED, int G>
 int launch_linear(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
-    if (!p.stream)
-        return launch_simple<BF16, G, 1, kLinear>(
-            a, PACKED, dim3(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile))), stream);
-    return a.n <= 2   ? launch_linear_stream<BF16, PACKED, G, 1>(a, p, stream)
-           : a.n <= 4 ? launch_linear_stream<BF16, PACKED, G, 2>(a, p, stream)
-           : a.n <= 8 ? launch_linear_stream<BF16, PACKED, G, 4>(a, p, stream)
-                      : launch_linear_stream<BF16, PACKED, G, 8>(a, p, stream);
+    if (p.stream)
+        return a.n <= 2   ? launch_linear_stream<BF16, PACKED, G, 1>(a, p, stream)
+               : a.n <= 4 ? launch_linear_stream<BF16, PACKED, G, 2>(a, p, stream)
+               : a.n <= 8 ? launch_linear_stream<BF16, PACKED, G, 4>(a, p, stream)
+                          : launch_linear_stream<BF16, PACKED, G, 8>(a, p, stream);
+    switch (p.tile) {
+    case 0: return launch_tile<BF16, PACKED, G, 0>(a, p, stream);
+    case 1: return launch_tile<BF16, PACKED, G, 1>(a, p, stream);
+    case 2: return launch_tile<BF16, PACKED, G, 2>(a, p, stream);
+    case 3: return launch_tile<BF16, PACKED, G, 3>(a, p, stream);
+    case 4:
+        if constexpr (G == 1) return launch_tile<BF16, PACKED, 1, 4>(a, p, stream);
+    }
+    return launch_simple<BF16, G, 1, kLinear>(
+        a, PACKED, dim3(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile))), stream);
 }
 
 template <bool BF16>
@@ -145,7 +160,9 @@ int launch_linear(const FfnArgs &a, const LinearPlan &p, bool packed, bool gated
 bool fast_weight(const void *W, const void *sf, int64_t k) {
     return k % 64 == 0 && !misaligned(W, 16) && !misaligned(sf, 4);
 }
-bool aligned_rows(const void *X, int64_t ldx) { return !misaligned(X, 16) && ldx % 8 == 0; }
+// Whether rows start on 16-byte boundaries, `piece` elements being 16 bytes.
+bool aligned_rows16(const void *p, int64_t ld, int64_t piece) { return !misaligned(p, 16) && ld % piece == 0; }
+bool aligned_rows(const void *X, int64_t ldx) { return aligned_rows16(X, ldx, 8); }
 
 int copy_aligned(const void *X, int64_t ldx, void *to, int64_t rows, int64_t k, hipStream_t stream) {
     const uint16_t *x = static_cast<const uint16_t *>(X);
@@ -187,6 +204,8 @@ int linear(const LinearCall &c, const LinearPlan &p, uint8_t *ws, hipStream_t st
     a.y_type = c.y_type;
     a.splits = static_cast<int32_t>(p.splits);
     a.part = p.part_bytes > 0 ? reinterpret_cast<float *>(ws) : nullptr;
+    const int64_t piece = 16 / type_bytes(c.y_type);
+    a.vec = aligned_rows16(c.Y, c.ldy, piece) && (!c.residual || aligned_rows16(c.residual, c.ldr, piece));
     const bool packed = c.w_layout == NVFP4_W_PACKED;
     const int s = c.x_type == NVFP4_OUT_BF16 ? launch_linear<true>(a, p, packed, c.gated(), stream)
                                              : launch_linear<false>(a, p, packed, c.gated(), stream);

@@ -88,6 +88,18 @@ def test_linear_sizes(n, m, k, layout):
         linear_case(rng, n, m, k, x=x, gated=gated, layout=layout)
 
 
+@pytest.mark.parametrize("n,m,k", [(2817, 2050, 320), (1409, 2050, 832), (769, 2050, 1088), (385, 2050, 576),
+                                   (97, 2050, 1024), (40, 520, 8192)])
+def test_linear_every_tile_shape(n, m, k):
+    """Weights that take each shape of the tile kernel, largest tiles first, then K split."""
+    print(f"linear tiles {n} {m} {k}", flush=True)
+    rng = np.random.default_rng(n)
+    linear_case(rng, n, m, k, x="bf16", bias=True, residual="in place", act="silu", layout="packed", ldy=2056)
+    linear_case(rng, n, m, k, x="f16", y="f32", act="gelu", bias=True, residual="in place", ldx=k + 8, ldy=2052)
+    linear_case(rng, n, (m + 1) // 2, k, x="f16", gated=True, bias=True, act="gelu_tanh", layout="packed", ldy=2059)
+    linear_case(rng, n, (m + 1) // 2, k, x="bf16", y="f32", gated=True, residual="apart", act="relu", ldx=k + 1)
+
+
 @pytest.mark.parametrize("k", [16, 32, 48, 80, 112, 144, 240, 272, 1040, 2064])
 def test_linear_row_major_k_of_whole_blocks(k):
     rng = np.random.default_rng(k)
