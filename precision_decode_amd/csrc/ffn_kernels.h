@@ -1021,11 +1021,12 @@ struct RouteArgs {
     int64_t ldx;
     const uint8_t *router;
     const float *route_bias;
-    double *logits;
+    double *logits;             // [splits][tokens][experts]: sums over parts of hidden
     int32_t *offsets, *choice, *list;
     float *weights;
     int64_t tokens, experts, hidden;
-    int32_t topk, bf16, scoring, renormalize;
+    int32_t splits;
+    int32_t topk, scoring, renormalize;
     float routed_scale;
 };
 
@@ -1040,36 +1041,103 @@ __device__ __forceinline__ double wave_max64(double v) {
     return v;
 }
 
-constexpr int kRouteThreads = 256;
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kRouteTokens = 16;
+constexpr int kRouteWaves = 4;
+constexpr int kRouteDepth = 4;   // steps of 32 elements a wave loads at a time
 
-// Logits of one expert (blockIdx.x) and 16 tokens (blockIdx.y): products of 16-bit values are exact in
-// fp64, and the fp64 sum errs by about 2^-50, so the choice of experts is the
-// one of the exact scores unless these agree to some 14 digits.
-__global__ void __launch_bounds__(kRouteThreads) route_logits(const RouteArgs a) {
-    __shared__ double red[kRouteThreads / kWave];
-    const int64_t expert = blockIdx.x;
-    const uint16_t *w = reinterpret_cast<const uint16_t *>(a.router) + expert * a.hidden;
-    const int type = a.bf16 ? NVFP4_OUT_BF16 : NVFP4_OUT_F16;
-    const int64_t t0 = int64_t(blockIdx.y) * kRouteTokens;
-    for (int64_t t = t0; t < t0 + kRouteTokens && t < a.tokens; ++t) {
-        const uint16_t *x = reinterpret_cast<const uint16_t *>(a.X) + t * a.ldx;
-        double s = 0.0;
-        for (int64_t i = threadIdx.x; i < a.hidden; i += kRouteThreads)
-            s = __builtin_fma(double(load_as_float(x, i, type)), double(load_as_float(w, i, type)), s);
-        s = wave_sum64(s);
-        if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = s;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int i = 1; i < kRouteThreads / kWave; ++i) s += red[i];
-            a.logits[t * a.experts + expert] = s;
+// Partial logits of 16 experts and 16 tokens over one of `splits` parts of
+// hidden.  Products of 16-bit values are exact in fp64 and the fp64 sums err by
+// about 2^-50, so the choice of experts is the one of the exact scores unless
+// these agree to some 14 digits.  The fp64 matrix instruction takes 4 elements of
+// K, one per lane quarter; a lane loads 8 consecutive ones at a time, so
+// instruction j of a step of 32 multiplies elements 8 q + j of all quarters q.
+// 64 experts x 7168: 1 token - us, 16 tokens - us, 64 tokens - us (summed by the
+// VALU, an expert per workgroup, they took 5, 58 and 53 us).
+template <bool BF16>
+__global__ void __launch_bounds__(kRouteWaves * kWave) route_logits(const RouteArgs a) {
+    __shared__ double red[kRouteWaves - 1][4][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int li = lane & 15, kq = lane >> 4;
+    const int64_t split = blockIdx.x % a.splits, e0 = int64_t(blockIdx.x / a.splits) * kTile;
+    const int64_t t0 = int64_t(blockIdx.y) * kTile;
+    const int64_t steps = (a.hidden + 31) / 32;
+    const int64_t first = split * steps / a.splits + wave, last = (split + 1) * steps / a.splits;
+    // rows past the last repeat it; their sums are not stored
+    const int64_t er = e0 + li < a.experts ? e0 + li : a.experts - 1;
+    const int64_t tr = t0 + li < a.tokens ? t0 + li : a.tokens - 1;
+    const uint8_t *w = a.router + 2 * er * a.hidden, *x = a.X + 2 * tr * a.ldx;
+    f64x4 acc = {};
+    for (int64_t s0 = first; s0 < last; s0 += kRouteWaves * kRouteDepth) {
+        u32x4 wv[kRouteDepth], xv[kRouteDepth];
+#pragma unroll
+        for (int d = 0; d < kRouteDepth; ++d) {
+            const int64_t s = s0 + kRouteWaves * d, e = 32 * s + 8 * kq;
+            wv[d] = xv[d] = u32x4{0, 0, 0, 0};
+            if (s < last && e < a.hidden) {
+                __builtin_memcpy(&wv[d], w + 2 * e, 16);
+                __builtin_memcpy(&xv[d], x + 2 * e, 16);
+            }
         }
-        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < kRouteDepth; ++d)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint16_t wb = static_cast<uint16_t>(wv[d][j / 2] >> (16 * (j & 1)));
+                const uint16_t xb = static_cast<uint16_t>(xv[d][j / 2] >> (16 * (j & 1)));
+                const float wf = BF16 ? bf16_value(wb) : static_cast<float>(__builtin_bit_cast(_Float16, wb));
+                const float xf = BF16 ? bf16_value(xb) : static_cast<float>(__builtin_bit_cast(_Float16, xb));
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64(double(wf), double(xf), acc, 0, 0, 0);
+            }
+    }
+    if (wave > 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[wave - 1][i][lane] = acc[i];
+    __syncthreads();
+    if (wave > 0 || t0 + li >= a.tokens) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        double v = acc[i];
+        for (int u = 0; u < kRouteWaves - 1; ++u) v += red[u][i][lane];
+        const int64_t e = e0 + 4 * i + kq;   // the fp64 instruction's row of register i
+        if (e < a.experts) a.logits[(split * a.tokens + t0 + li) * a.experts + e] = v;
     }
 }
 
-constexpr int kSelectWaves = 4;
+// A token's score of an expert with logit z, once the softmax's maximum and sum
+// are known.
+struct Scores {
+    double top, sum;
+    int scoring;
+    __device__ __forceinline__ double score(double z) const {
+        return scoring == NVFP4_SCORE_SOFTMAX ? exp(z - top) / sum : 1.0 / (1.0 + exp(-z));
+    }
+};
+__device__ __forceinline__ double logit(const RouteArgs &a, int64_t t, int e) {
+    const double *z = a.logits + t * a.experts + e;
+    double v = z[0];
+#pragma unroll 4
+    for (int s = 1; s < a.splits; ++s) v += z[s * a.tokens * a.experts];
+    return v;
+}
+// The key experts are chosen by; a NaN counts as the least.
+__device__ __forceinline__ double choice_key(const RouteArgs &a, int e, double score) {
+    const double key = score + (a.route_bias ? double(a.route_bias[e]) : 0.0);
+    return key == key ? key : -INFINITY;
+}
+__device__ __forceinline__ float routed_weight(const RouteArgs &a, double score, double chosen) {
+    return static_cast<float>((a.renormalize ? score / chosen : score) * double(a.routed_scale));
+}
+
+constexpr int kSelectWaves = 16;
+constexpr int kSelectLds = 32768;   // bytes of scores and keys
+
+// Tokens that one workgroup of route_select chooses for at a time.
+inline __host__ __device__ int select_tokens(int64_t experts) {
+    const int64_t n = kSelectLds / 16 / experts;
+    return static_cast<int>(n < 1 ? 1 : n < kSelectWaves ? n : kSelectWaves);
+}
 
 // One workgroup chooses the experts of every token, a wave per token at a
 // time: an expert's rank is the number of experts ahead of it (a larger key,
@@ -1079,58 +1147,50 @@ constexpr int kSelectWaves = 4;
 // may differ between runs, but nothing depends on it: every slot is a column
 // of its own in the products.
 __global__ void __launch_bounds__(kSelectWaves * kWave) route_select(const RouteArgs a) {
-    __shared__ double keys[kSelectWaves][kMaxExperts];
-    __shared__ int32_t count[kMaxExperts], cursor[kMaxExperts];
+    __shared__ double lds[kSelectLds / 8];
+    __shared__ int32_t count[kMaxExperts], cursor[kMaxExperts], order[kSelectWaves][kMaxTopk];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int experts = static_cast<int>(a.experts);
+    const int experts = static_cast<int>(a.experts), each = select_tokens(a.experts);
+    double *score = lds + wave * 2 * experts, *keys = score + experts;
     for (int e = threadIdx.x; e < experts; e += blockDim.x) count[e] = 0;
     __syncthreads();
-    const int64_t rounds = (a.tokens + kSelectWaves - 1) / kSelectWaves;
-    for (int64_t i = 0; i < rounds; ++i) {
-        const int64_t t = i * kSelectWaves + wave;
-        const bool in = t < a.tokens;
-        const double *z = a.logits + t * experts;
-        double top = -INFINITY, sum = 0.0;
-        if (in && a.scoring == NVFP4_SCORE_SOFTMAX) {
-            for (int e = lane; e < experts; e += kWave) top = fmax(top, z[e]);
-            top = wave_max64(top);
-            for (int e = lane; e < experts; e += kWave) sum += exp(z[e] - top);
-            sum = wave_sum64(sum);
+    for (int64_t t = wave; t < a.tokens && wave < each; t += each) {
+        Scores sc = {-INFINITY, 0.0, a.scoring};
+        for (int e = lane; e < experts; e += kWave) {
+            score[e] = logit(a, t, e);
+            sc.top = fmax(sc.top, score[e]);
         }
-        auto score = [&](int e) {
-            return a.scoring == NVFP4_SCORE_SOFTMAX ? exp(z[e] - top) / sum : 1.0 / (1.0 + exp(-z[e]));
-        };
-        if (in)
-            for (int e = lane; e < experts; e += kWave) {
-                const double key = score(e) + (a.route_bias ? double(a.route_bias[e]) : 0.0);
-                keys[wave][e] = key == key ? key : -INFINITY;
-            }
-        __syncthreads();
+        if (a.scoring == NVFP4_SCORE_SOFTMAX) {
+            sc.top = wave_max64(sc.top);
+            for (int e = lane; e < experts; e += kWave) sc.sum += exp(score[e] - sc.top);
+            sc.sum = wave_sum64(sc.sum);
+        }
+        for (int e = lane; e < experts; e += kWave) {
+            score[e] = sc.score(score[e]);
+            keys[e] = choice_key(a, e, score[e]);
+        }
+        wave_lds_fence();
         double chosen = 0.0;
-        if (in) {
-            for (int e = lane; e < experts; e += kWave) {
-                const double key = keys[wave][e];
-                int rank = 0;
-                for (int o = 0; o < experts; ++o) {
-                    const double other = keys[wave][o];
-                    rank += other > key || (other == key && o < e);
-                }
-                if (rank < a.topk) {
-                    const double s = score(e);
-                    chosen += s;
-                    a.choice[t * a.topk + rank] = e;
-                    a.weights[t * a.topk + rank] = static_cast<float>(
-                        a.renormalize ? s : s * double(a.routed_scale));
-                    atomicAdd(&count[e], 1);
-                }
+        for (int e = lane; e < experts; e += kWave) {
+            const double key = keys[e];
+            int rank = 0;
+#pragma unroll 8
+            for (int o = 0; o < experts; ++o) {
+                const double other = keys[o];
+                rank += other > key || (other == key && o < e);
             }
-            chosen = wave_sum64(chosen);
+            if (rank < a.topk) {
+                chosen += score[e];
+                order[wave][rank] = e;
+                a.choice[t * a.topk + rank] = e;
+                atomicAdd(&count[e], 1);
+            }
         }
-        __syncthreads();
-        if (in && a.renormalize)
-            for (int j = lane; j < a.topk; j += kWave)
-                a.weights[t * a.topk + j] =
-                    static_cast<float>(a.weights[t * a.topk + j] / chosen * double(a.routed_scale));
+        chosen = wave_sum64(chosen);
+        wave_lds_fence();
+        for (int j = lane; j < a.topk; j += kWave)
+            a.weights[t * a.topk + j] = routed_weight(a, score[order[wave][j]], chosen);
+        wave_lds_fence();
     }
     __syncthreads();
     // offsets: lane l of wave 0 sums its run of experts, the runs are scanned
@@ -1171,17 +1231,19 @@ struct CombineArgs {
 constexpr int kCombineThreads = 256;
 
 // Y of one token (blockIdx.y): its slots' partial outputs in the order of
-// their ranks.
+// their ranks.  A thread makes four outputs (hidden is a multiple of 16).
 __global__ void __launch_bounds__(kCombineThreads) moe_combine(const CombineArgs a) {
-    const int64_t r = int64_t(blockIdx.x) * kCombineThreads + threadIdx.x, t = blockIdx.y;
+    const int64_t r = 4 * (int64_t(blockIdx.x) * kCombineThreads + threadIdx.x), t = blockIdx.y;
     if (r >= a.hidden) return;
-    float y = 0.0f;
-    for (int j = 0; j < a.topk; ++j) {
-        const int64_t s = t * a.topk + j;
-        y += a.weights[s] * a.part[s * a.hidden + r];
+    const float *part = a.part + t * a.topk * a.hidden + r, *w = a.weights + t * a.topk;
+    f32x4 y = {};
+#pragma unroll 8
+    for (int j = 0; j < a.topk; ++j) y += w[j] * *reinterpret_cast<const f32x4 *>(part + j * a.hidden);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (a.residual) y[e] += load_as_float(a.residual, t * a.ldr + r + e, a.y_type);
+        store_rounded(a.Y, t * a.ldy + r + e, a.y_type, y[e]);
     }
-    if (a.residual) y += load_as_float(a.residual, t * a.ldr + r, a.y_type);
-    store_rounded(a.Y, t * a.ldy + r, a.y_type, y);
 }
 
 }  // namespace

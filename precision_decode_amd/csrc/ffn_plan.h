@@ -162,7 +162,7 @@ inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool 
 // Workspace of one MoE call, in bytes from its start.  The sizes go by the
 // larger (fp32 output) number of planes of h, so they do not depend on it.
 struct MoeWorkspace {
-    size_t logits;    // double [tokens][experts]
+    size_t logits;    // double [route_splits][tokens][experts]
     size_t offsets;   // int32 [experts + 1]: first slot of every expert
     size_t choice;    // int32 [slots]: expert of every slot (slot = token * topk + j)
     size_t list;      // int32 [slots]: slots sorted by expert
@@ -176,6 +176,14 @@ struct MoeWorkspace {
 constexpr int kMaxPlanes = 3;
 constexpr int64_t kMaxStreamBytes = 0x7FFFFFF0;   // row offsets the stream kernel can form
 
+// Parts of hidden that the logits are summed in: 512 elements each, while that
+// makes no more workgroups than there are compute units.
+inline int64_t route_splits(const nvfp4_moe_layer_t &l, int64_t tokens) {
+    const int64_t tiles = ceil_div(l.experts, kTile) * ceil_div(tokens, kTile);
+    const int64_t most = kComputeUnits / tiles, want = ceil_div(l.hidden, 512);
+    return most < 1 ? 1 : want < most ? want : most;
+}
+
 inline MoeWorkspace moe_workspace(const nvfp4_moe_layer_t &l, int64_t tokens) {
     const size_t slots = static_cast<size_t>(tokens) * l.topk;
     MoeWorkspace w;
@@ -185,7 +193,7 @@ inline MoeWorkspace moe_workspace(const nvfp4_moe_layer_t &l, int64_t tokens) {
         at += ws_round(bytes);
         return here;
     };
-    w.logits = take(static_cast<size_t>(tokens) * l.experts * 8);
+    w.logits = take(static_cast<size_t>(route_splits(l, tokens)) * tokens * l.experts * 8);
     w.offsets = take(static_cast<size_t>(l.experts + 1) * 4);
     w.choice = take(slots * 4);
     w.list = take(slots * 4);

@@ -318,12 +318,13 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     r.experts = l.experts;
     r.hidden = l.hidden;
     r.topk = l.topk;
-    r.bf16 = bf16;
+    r.splits = static_cast<int32_t>(route_splits(l, c.tokens));
     r.scoring = l.scoring;
     r.renormalize = l.renormalize;
     r.routed_scale = l.routed_scale;
-    int s = run(route_logits, dim3(static_cast<uint32_t>(l.experts), static_cast<uint32_t>(ceil_div(c.tokens, kRouteTokens))),
-                kRouteThreads, r, stream);
+    const dim3 route_grid(static_cast<uint32_t>(ceil_div(l.experts, kTile) * r.splits),
+                          static_cast<uint32_t>(ceil_div(c.tokens, kTile)));
+    int s = run(bf16 ? route_logits<true> : route_logits<false>, route_grid, kRouteWaves * kWave, r, stream);
     if (s == NVFP4_GEMV_OK) s = run(route_select, dim3(1), kSelectWaves * kWave, r, stream);
     if (s != NVFP4_GEMV_OK) return s;
 
@@ -383,7 +384,7 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     y.topk = l.topk;
     y.y_type = c.y_type;
     return run(moe_combine,
-               dim3(static_cast<uint32_t>(ceil_div(l.hidden, kCombineThreads)), static_cast<uint32_t>(c.tokens)),
+               dim3(static_cast<uint32_t>(ceil_div(l.hidden, 4 * kCombineThreads)), static_cast<uint32_t>(c.tokens)),
                kCombineThreads, y, stream);
 }
 
