@@ -42,6 +42,7 @@ struct FfnArgs {
     int64_t ldy;
     const int32_t *offsets;     // MoE: first slot of every expert
     const int32_t *list;        // MoE: slots sorted by expert
+    const int32_t *active;      // MoE: experts that have slots, then -1
     int64_t n, m, k;            // tokens, rows of one matrix, K
     int32_t topk;
     int32_t act;
@@ -192,11 +193,33 @@ __device__ __forceinline__ int32_t x_row(const FfnArgs &a, int32_t row) {
 
 // ---------------------------------------------------------------- epilogue
 // Rows r .. r+3 of the matrix (those below m) of one token or slot, from the
-// fp32 sums of the gate (or only) matrix and of the up matrix.
+// fp32 sums of the gate (or only) matrix and of the up matrix.  The matrices of
+// the MoE layer have a multiple of 16 rows.
 template <int MODE, int G>
 __device__ __forceinline__ void finish4(const FfnArgs &a, int expert, int split, int64_t row, int64_t r,
                                         const f32x4 (&sum)[G]) {
-    if (MODE == kLinear && a.part) {
+    if (MODE == kMoeDown) {
+        if (r < a.m)
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.Y) + row * a.ldy + r) =
+                (a.alpha ? a.alpha[expert] : 1.0f) * sum[0];
+        return;
+    }
+    if (MODE == kMoeUp) {
+        if (r >= a.m) return;
+        const float al = a.alpha ? a.alpha[2 * expert] : 1.0f, au = a.alpha ? a.alpha[2 * expert + 1] : 1.0f;
+        uint16_t p[4][kMaxPlanes];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            split_planes(activate(a.act, al * sum[0][e]) * (au * sum[G - 1][e]), a.y_planes, p[e]);
+#pragma unroll
+        for (int i = 0; i < kMaxPlanes; ++i)
+            if (i < a.y_planes) {
+                const uint64_t v = p[0][i] | uint64_t(p[1][i]) << 16 | uint64_t(p[2][i]) << 32 | uint64_t(p[3][i]) << 48;
+                *reinterpret_cast<uint64_t *>(static_cast<uint16_t *>(a.Y) + i * a.plane + row * a.ldy + r) = v;
+            }
+        return;
+    }
+    if (a.part) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -207,26 +230,13 @@ __device__ __forceinline__ void finish4(const FfnArgs &a, int expert, int split,
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (r + e >= a.m) return;
-        float z = (a.alpha ? a.alpha[MODE == kLinear ? 0 : G * expert] : 1.0f) * sum[0][e];
-        if (MODE == kMoeDown) {
-            static_cast<float *>(a.Y)[row * a.ldy + r + e] = z;
-            continue;
-        }
-        if (MODE == kLinear && a.bias) z += a.bias[r + e];
+        float z = (a.alpha ? a.alpha[0] : 1.0f) * sum[0][e];
+        if (a.bias) z += a.bias[r + e];
         z = activate(a.act, z);
         if constexpr (G == 2) {
-            float u = (a.alpha ? a.alpha[MODE == kLinear ? 1 : 2 * expert + 1] : 1.0f) * sum[1][e];
-            if (MODE == kLinear && a.bias) u += a.bias[a.m + r + e];
+            float u = (a.alpha ? a.alpha[1] : 1.0f) * sum[1][e];
+            if (a.bias) u += a.bias[a.m + r + e];
             z *= u;
-        }
-        if (MODE == kMoeUp) {
-            uint16_t p[kMaxPlanes];
-            split_planes(z, a.y_planes, p);
-#pragma unroll
-            for (int i = 0; i < kMaxPlanes; ++i)
-                if (i < a.y_planes)
-                    static_cast<uint16_t *>(a.Y)[i * a.plane + row * a.ldy + r + e] = p[i];
-            continue;
         }
         if (a.residual) z += load_as_float(a.residual, row * a.ldr + r + e, a.y_type);
         store_rounded(a.Y, row * a.ldy + r + e, a.y_type, z);
@@ -266,9 +276,10 @@ __global__ void __launch_bounds__(kSimpleWaves * kWave) ffn_simple(const FfnArgs
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int li = lane & 15, kq = lane >> 4;
     const uint32_t tiles = static_cast<uint32_t>((a.m + kTile - 1) / kTile);
-    const uint32_t group = blockIdx.x / tiles;   // expert, or 16 tokens of the linear layer
+    const uint32_t group = blockIdx.x / tiles;   // place in the list of experts, or 16 tokens of the linear layer
     const int64_t row0 = int64_t(blockIdx.x - group * tiles) * kTile;
-    const int expert = MODE == kLinear ? 0 : group;
+    const int expert = MODE == kLinear ? 0 : a.active[group];
+    if (expert < 0) return;   // workgroup-uniform
     TokenRange range = expert_range<MODE>(a, expert);
     if (MODE == kLinear) {
         range.first = group * kTile;
@@ -560,23 +571,25 @@ template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int W, i
 __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
     __shared__ u32x4 lds[stream_lds<G, P, R, W, NXMAX>()];
     const uint32_t strips = static_cast<uint32_t>((a.m + R * kTile - 1) / (R * kTile));
-    const uint32_t q = blockIdx.x / strips;   // split, or expert
+    const uint32_t q = blockIdx.x / strips;   // split, or place in the list of experts
     const int64_t row0 = int64_t(blockIdx.x - q * strips) * (R * kTile);
     if constexpr (MODE == kLinear) {
         stream_pass<BF16, PACKED, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q, 0, static_cast<int32_t>(a.n), lds);
     } else {
-        const TokenRange range = expert_range<MODE>(a, q);
+        const int expert = a.active[q];
+        if (expert < 0) return;   // workgroup-uniform
+        const TokenRange range = expert_range<MODE>(a, expert);
         for (int32_t p = range.first; p < range.end; p += 2 * NXMAX) {
             const int32_t end = range.end - p > 2 * NXMAX ? p + 2 * NXMAX : range.end;
             const int n = end - p;   // workgroup-uniform
             if (n <= 2)
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 1>(a, q, row0, 0, p, end, lds);
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 1>(a, expert, row0, 0, p, end, lds);
             else if (n <= 4)
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 2>(a, q, row0, 0, p, end, lds);
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 2>(a, expert, row0, 0, p, end, lds);
             else if (NXMAX == 4 || n <= 8)
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 4>(a, q, row0, 0, p, end, lds);
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 4>(a, expert, row0, 0, p, end, lds);
             else
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, NXMAX>(a, q, row0, 0, p, end, lds);
+                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, NXMAX>(a, expert, row0, 0, p, end, lds);
         }
     }
 }
@@ -1022,10 +1035,10 @@ struct RouteArgs {
     const uint8_t *router;
     const float *route_bias;
     double *logits;             // [splits][tokens][experts]: sums over parts of hidden
-    int32_t *offsets, *choice, *list;
+    int32_t *offsets, *choice, *list, *active;
     float *weights;
     int64_t tokens, experts, hidden;
-    int32_t splits;
+    int32_t splits, groups;     // groups: entries of active
     int32_t topk, scoring, renormalize;
     float routed_scale;
 };
@@ -1193,24 +1206,30 @@ __global__ void __launch_bounds__(kSelectWaves * kWave) route_select(const Route
         wave_lds_fence();
     }
     __syncthreads();
-    // offsets: lane l of wave 0 sums its run of experts, the runs are scanned
+    // offsets and the list of experts with slots: lane l of wave 0 sums its run of
+    // experts, the runs are scanned (slots in the low half, experts in the high)
     if (wave == 0) {
         const int per = (experts + kWave - 1) / kWave;
         const int e0 = lane * per;
-        int own = 0;
-        for (int e = e0; e < e0 + per && e < experts; ++e) own += count[e];
-        int at = own;
+        uint64_t own = 0;
+        for (int e = e0; e < e0 + per && e < experts; ++e) own += count[e] > 0 ? (uint64_t(1) << 32) + count[e] : 0;
+        uint64_t at = own;
 #pragma unroll
         for (int o = 1; o < kWave; o <<= 1) {
-            const int v = __shfl_up(at, o);
+            const uint64_t v = __shfl_up(static_cast<unsigned long long>(at), o);
             if (lane >= o) at += v;
         }
+        const int total = static_cast<int>(__shfl(static_cast<unsigned long long>(at), kWave - 1) >> 32);
         at -= own;
         for (int e = e0; e < e0 + per && e < experts; ++e) {
-            a.offsets[e] = cursor[e] = at;
-            at += count[e];
+            a.offsets[e] = cursor[e] = static_cast<int32_t>(at);
+            if (count[e] > 0) {
+                a.active[at >> 32] = e;
+                at += (uint64_t(1) << 32) + count[e];
+            }
         }
-        if (lane == kWave - 1) a.offsets[experts] = at;
+        if (lane == kWave - 1) a.offsets[experts] = static_cast<int32_t>(at);
+        for (int i = total + lane; i < a.groups; i += kWave) a.active[i] = -1;
     }
     __syncthreads();
     const int64_t slots = a.tokens * a.topk;

@@ -166,6 +166,7 @@ struct MoeWorkspace {
     size_t offsets;   // int32 [experts + 1]: first slot of every expert
     size_t choice;    // int32 [slots]: expert of every slot (slot = token * topk + j)
     size_t list;      // int32 [slots]: slots sorted by expert
+    size_t active;    // int32 [moe_groups]: experts that have slots, then -1
     size_t weights;   // float [slots]
     size_t h;         // bf16 [planes][slots][inter]
     size_t part;      // float [slots][hidden]
@@ -175,6 +176,11 @@ struct MoeWorkspace {
 
 constexpr int kMaxPlanes = 3;
 constexpr int64_t kMaxStreamBytes = 0x7FFFFFF0;   // row offsets the stream kernel can form
+
+// Most experts that can have slots.
+inline int64_t moe_groups(const nvfp4_moe_layer_t &l, int64_t tokens) {
+    return tokens * l.topk < l.experts ? tokens * l.topk : l.experts;
+}
 
 // Parts of hidden that the logits are summed in: 512 elements each, while that
 // makes no more workgroups than there are compute units.
@@ -197,6 +203,7 @@ inline MoeWorkspace moe_workspace(const nvfp4_moe_layer_t &l, int64_t tokens) {
     w.offsets = take(static_cast<size_t>(l.experts + 1) * 4);
     w.choice = take(slots * 4);
     w.list = take(slots * 4);
+    w.active = take(static_cast<size_t>(moe_groups(l, tokens)) * 4);
     w.weights = take(slots * 4);
     w.h = take(kMaxPlanes * slots * l.inter * 2);
     w.part = take(slots * l.hidden * 4);

@@ -269,30 +269,30 @@ constexpr int kUpTiles = 2, kUpWaves = 4;       // per workgroup: row tiles of g
 constexpr int kDownTiles = 4, kDownWaves = 2;
 
 template <bool BF16, bool PACKED>
-int stream_up(const FfnArgs &a, int64_t experts, hipStream_t stream) {
+int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
     return run(ffn_stream<BF16, PACKED, 2, 1, kMoeUp, kUpTiles, 2, kUpWaves, 8>,
-               dim3(static_cast<uint32_t>(ceil_div(a.m, kUpTiles * kTile) * experts)), kUpWaves * kWave, a, stream);
+               dim3(static_cast<uint32_t>(ceil_div(a.m, kUpTiles * kTile) * groups)), kUpWaves * kWave, a, stream);
 }
 
 template <bool PACKED, int P>
-int stream_down(const FfnArgs &a, int64_t experts, hipStream_t stream) {
+int stream_down(const FfnArgs &a, int64_t groups, hipStream_t stream) {
     return run(ffn_stream<true, PACKED, 1, P, kMoeDown, kDownTiles, 2, kDownWaves, 4>,
-               dim3(static_cast<uint32_t>(ceil_div(a.m, kDownTiles * kTile) * experts)), kDownWaves * kWave, a,
+               dim3(static_cast<uint32_t>(ceil_div(a.m, kDownTiles * kTile) * groups)), kDownWaves * kWave, a,
                stream);
 }
 
 template <bool BF16>
-int launch_up(const FfnArgs &a, bool packed, bool fast, int64_t experts, hipStream_t stream) {
-    if (fast) return packed ? stream_up<BF16, true>(a, experts, stream) : stream_up<BF16, false>(a, experts, stream);
-    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * experts));
+int launch_up(const FfnArgs &a, bool packed, bool fast, int64_t groups, hipStream_t stream) {
+    if (fast) return packed ? stream_up<BF16, true>(a, groups, stream) : stream_up<BF16, false>(a, groups, stream);
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * groups));
     return launch_simple<BF16, 2, 1, kMoeUp>(a, packed, grid, stream);
 }
 
-int launch_down(const FfnArgs &a, bool packed, bool fast, int planes, int64_t experts, hipStream_t stream) {
+int launch_down(const FfnArgs &a, bool packed, bool fast, int planes, int64_t groups, hipStream_t stream) {
     if (fast && planes == 2)
-        return packed ? stream_down<true, 2>(a, experts, stream) : stream_down<false, 2>(a, experts, stream);
-    if (fast) return packed ? stream_down<true, 3>(a, experts, stream) : stream_down<false, 3>(a, experts, stream);
-    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * experts));
+        return packed ? stream_down<true, 2>(a, groups, stream) : stream_down<false, 2>(a, groups, stream);
+    if (fast) return packed ? stream_down<true, 3>(a, groups, stream) : stream_down<false, 3>(a, groups, stream);
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * groups));
     return planes == 2 ? launch_simple<true, 1, 2, kMoeDown>(a, packed, grid, stream)
                        : launch_simple<true, 1, 3, kMoeDown>(a, packed, grid, stream);
 }
@@ -313,6 +313,8 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     r.offsets = reinterpret_cast<int32_t *>(ws + w.offsets);
     r.choice = reinterpret_cast<int32_t *>(ws + w.choice);
     r.list = reinterpret_cast<int32_t *>(ws + w.list);
+    r.active = reinterpret_cast<int32_t *>(ws + w.active);
+    r.groups = static_cast<int32_t>(moe_groups(l, c.tokens));
     r.weights = reinterpret_cast<float *>(ws + w.weights);
     r.tokens = c.tokens;
     r.experts = l.experts;
@@ -349,14 +351,15 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     a.ldy = l.inter;
     a.offsets = r.offsets;
     a.list = r.list;
+    a.active = r.active;
     a.n = c.tokens;
     a.m = l.inter;
     a.k = l.hidden;
     a.topk = l.topk;
     a.act = l.activation;
     a.y_planes = planes;
-    s = bf16 ? launch_up<true>(a, packed, fast, l.experts, stream)
-             : launch_up<false>(a, packed, fast, l.experts, stream);
+    s = bf16 ? launch_up<true>(a, packed, fast, r.groups, stream)
+             : launch_up<false>(a, packed, fast, r.groups, stream);
     if (s != NVFP4_GEMV_OK) return s;
 
     a.X = ws + w.h;
@@ -369,7 +372,7 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     a.m = l.hidden;
     a.k = l.inter;
     fast = fast_weight(l.W2, l.sf2, l.inter) && slots * l.inter * 2 < kMaxStreamBytes;
-    s = launch_down(a, packed, fast, planes, l.experts, stream);
+    s = launch_down(a, packed, fast, planes, r.groups, stream);
     if (s != NVFP4_GEMV_OK) return s;
 
     CombineArgs y = {};
