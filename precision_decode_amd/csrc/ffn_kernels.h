@@ -27,6 +27,8 @@ enum Mode {
     kLinear = 0,    // tokens in order; epilogue to Y
     kMoeUp = 1,     // the tokens of an expert; f(gate) * up to h
     kMoeDown = 2,   // the slots of an expert; alpha2 * sum to the slot's partial output
+    kSlotUp = 3,    // one slot; as kMoeUp
+    kSlotDown = 4,  // one slot; the sums stay with the caller
 };
 
 struct FfnArgs {
@@ -184,11 +186,11 @@ __device__ __forceinline__ TokenRange expert_range(const FfnArgs &a, int expert)
 // Output row (kLinear: token, else slot) and X row of position p.
 template <int MODE>
 __device__ __forceinline__ int32_t out_row(const FfnArgs &a, int32_t p) {
-    return MODE == kLinear ? p : a.list[p];
+    return MODE == kMoeUp || MODE == kMoeDown ? a.list[p] : p;
 }
 template <int MODE>
 __device__ __forceinline__ int32_t x_row(const FfnArgs &a, int32_t row) {
-    return MODE == kMoeUp ? row / a.topk : row;
+    return MODE == kMoeUp || MODE == kSlotUp ? row / a.topk : row;
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -204,7 +206,7 @@ __device__ __forceinline__ void finish4(const FfnArgs &a, int expert, int split,
                 (a.alpha ? a.alpha[expert] : 1.0f) * sum[0];
         return;
     }
-    if (MODE == kMoeUp) {
+    if (MODE == kMoeUp || MODE == kSlotUp) {
         if (r >= a.m) return;
         const float al = a.alpha ? a.alpha[2 * expert] : 1.0f, au = a.alpha ? a.alpha[2 * expert + 1] : 1.0f;
         uint16_t p[4][kMaxPlanes];
@@ -418,12 +420,11 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// One workgroup owns R tiles of 16 rows of each of G matrices and up to 16
-// tokens at a time; its W waves take interleaved windows of 256 elements of K
-// of its part of K, U windows in flight each, and their sums are added in wave
-// order through LDS.  This is the shape for few tokens, where the weights'
-// bytes are the bound: every weight byte is read once, in 1 KiB instructions
-// (packed), and decoded once for all tokens.
+// The sums of R tiles of 16 rows of each of G matrices for up to 2 NX tokens: a
+// wave takes every `waves`-th window of 256 elements of K of its part of K from
+// window `wave` on, U in flight.  This is the shape for few tokens, where the
+// weights' bytes are the bound: every weight byte is read once, in 1 KiB
+// instructions (packed), and decoded once for all tokens.
 //
 // The tokens' elements of a window (512 bytes each) are read row by row, two
 // tokens per instruction, as far ahead as the weights, and go through a slot
@@ -432,17 +433,16 @@ __device__ __forceinline__ void wave_lds_fence() {
 // instruction would touch a different line in every lane.  The 16-byte pieces
 // are swizzled by the token, so the 16 lanes that read the same piece of 16
 // tokens hit distinct banks.  NX = instructions = half the tokens staged.
-template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int W, int NX>
-__device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
-                                            int32_t end, u32x4 *lds) {
+template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int NX>
+__device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
+                                            int32_t end, u32x4 *slot, int wave, int waves, f32x4 (&acc)[G][R]) {
     const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int li = lane & 15, kq = lane >> 4;
     const uint32_t k = static_cast<uint32_t>(a.k);
     const int wins = static_cast<int>((k + kWinElems - 1) / kWinElems);
     const int win0 = static_cast<int>(int64_t(split) * wins / a.splits);
     const int nwin = static_cast<int>(int64_t(split + 1) * wins / a.splits) - win0;
-    const int niter = nwin > wave ? (nwin - wave + W - 1) / W : 0;
+    const int niter = nwin > wave ? (nwin - wave + waves - 1) / waves : 0;
 
     const WeightTiles<PACKED, R> w0(a, G * int64_t(expert), row0, li, kq);
     const WeightTiles<PACKED, R> w1(a, G * int64_t(expert) + (G - 1), row0, li, kq);
@@ -462,13 +462,12 @@ __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_
             xo[j] = 2 * static_cast<uint32_t>(row) * static_cast<uint32_t>(a.ldx) + 16 * (lane & 31);
         }
     }
-    u32x4 *slot = lds + wave * (P * 2 * NX * 32);
     const int tok = li & (2 * NX - 1);   // columns past the staged tokens repeat them and are dropped
 
     u32x4 wq[U][G][R][2], xq[U][P][NX];
     uint32_t ws[U][G][R];
     auto issue = [&](int i, int u) {
-        const uint32_t win = static_cast<uint32_t>(win0 + wave + W * i);
+        const uint32_t win = static_cast<uint32_t>(win0 + wave + waves * i);
         const bool run = i < niter;
         const uint32_t xpast = run && win * kWinElems + 8 * (lane & 31) < k ? 0u : kOutOfRange;
 #pragma unroll
@@ -484,7 +483,10 @@ __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_
             if constexpr (G == 2) w1.load(r, win, past, wq[u][1][r], ws[u][1][r]);
         }
     };
-    f32x4 acc[G][R] = {};
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[g][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto consume = [&](int u) {
         wave_lds_fence();
 #pragma unroll
@@ -533,7 +535,22 @@ __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_
         }
     }
 
-    // sums of the waves, in wave order; wave r % W finishes row tile r
+}
+
+// One workgroup owns R tiles of 16 rows of each of G matrices and up to 2 NX
+// tokens; its W waves take the windows of its part of K in turn, and their sums
+// are added in wave order through LDS.
+template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int W, int NX>
+__device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
+                                            int32_t end, u32x4 *lds) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int li = lane & 15, kq = lane >> 4;
+    f32x4 acc[G][R];
+    stream_sums<BF16, PACKED, G, P, MODE, R, U, NX>(a, expert, row0, split, p0, end,
+                                                    lds + wave * (P * 2 * NX * 32), wave, W, acc);
+
+    // wave r % W finishes row tile r
     f32x4 *red = reinterpret_cast<f32x4 *>(lds);
     if (W > 1) {
         __syncthreads();
@@ -1263,6 +1280,135 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine(const CombineArgs
         if (a.residual) y[e] += load_as_float(a.residual, t * a.ldr + r + e, a.y_type);
         store_rounded(a.Y, t * a.ldy + r + e, a.y_type, y[e]);
     }
+}
+
+// ---------------------------------------------------------------- few slots
+// The MoE layer where few experts share tokens (one token above all): a slot is
+// taken by itself, so the slots need no sorting.  Its expert is chosen by each
+// workgroup that multiplies for it, and the down product's workgroups, which own
+// rows of a token's output, finish the output themselves: three launches, and no
+// partial outputs in memory.  7168 x 2048, 8 of 64 experts, one token: - us where
+// the five kernels take - us.
+
+constexpr int kUpTiles = 2, kUpWaves = 4;       // per workgroup: row tiles of gate and of up, waves
+constexpr int kDownTiles = 4, kDownWaves = 2;
+constexpr int kSlotWaves = 8;                   // of the slots' down product
+
+struct SlotArgs {
+    FfnArgs f;
+    RouteArgs r;
+};
+
+// The expert of rank j of token t, to every thread of the workgroup.  `weigh`
+// (workgroup-uniform): its weight, too, to memory.
+template <int THREADS>
+__device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j, bool weigh) {
+    __shared__ double score[kMaxExperts], keys[kMaxExperts], red[THREADS / kWave];
+    __shared__ int32_t rank[kMaxExperts], order[kMaxTopk];
+    constexpr int kWaves = THREADS / kWave;
+    const int experts = static_cast<int>(a.experts), thread = threadIdx.x, wave = thread / kWave;
+    double top = -INFINITY;
+    for (int e = thread; e < experts; e += THREADS) {
+        score[e] = logit(a, t, e);
+        rank[e] = 0;
+        top = fmax(top, score[e]);
+    }
+    Scores sc = {0.0, 0.0, a.scoring};
+    if (a.scoring == NVFP4_SCORE_SOFTMAX) {
+        top = wave_max64(top);
+        if (thread % kWave == 0) red[wave] = top;
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w) top = fmax(top, red[w]);
+        __syncthreads();
+        double sum = 0.0;
+        for (int e = thread; e < experts; e += THREADS) sum += exp(score[e] - top);
+        sum = wave_sum64(sum);
+        if (thread % kWave == 0) red[wave] = sum;
+        __syncthreads();
+        sum = 0.0;
+        for (int w = 0; w < kWaves; ++w) sum += red[w];
+        sc.top = top;
+        sc.sum = sum;
+    }
+    for (int e = thread; e < experts; e += THREADS) {
+        score[e] = sc.score(score[e]);
+        keys[e] = choice_key(a, e, score[e]);
+    }
+    __syncthreads();
+    // the waves share the comparisons
+    for (int e = thread % kWave; e < experts; e += kWave) {
+        const double key = keys[e];
+        int ahead = 0;
+#pragma unroll 4
+        for (int o = wave; o < experts; o += kWaves) {
+            const double other = keys[o];
+            ahead += other > key || (other == key && o < e);
+        }
+        atomicAdd(&rank[e], ahead);
+    }
+    __syncthreads();
+    for (int e = thread; e < experts; e += THREADS)
+        if (rank[e] < a.topk) order[rank[e]] = e;
+    __syncthreads();
+    const int expert = order[j];
+    if (weigh && thread == 0) {
+        double chosen = 0.0;
+        if (a.renormalize)
+            for (int i = 0; i < a.topk; ++i) chosen += score[order[i]];
+        a.choice[t * a.topk + j] = expert;
+        a.weights[t * a.topk + j] = routed_weight(a, score[expert], chosen);
+    }
+    return expert;
+}
+
+// h of one slot: workgroup = strip of rows and slot.
+template <bool BF16, bool PACKED>
+__global__ void __launch_bounds__(kUpWaves * kWave, 2) ffn_slot_up(const SlotArgs s) {
+    __shared__ u32x4 lds[stream_lds<2, 1, kUpTiles, kUpWaves, 1>()];
+    const uint32_t strips = static_cast<uint32_t>((s.f.m + kUpTiles * kTile - 1) / (kUpTiles * kTile));
+    const uint32_t slot = blockIdx.x / strips, strip = blockIdx.x - slot * strips;
+    const uint32_t token = slot / s.r.topk;
+    const int expert = __builtin_amdgcn_readfirstlane(
+        choose_slot<kUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
+    stream_pass<BF16, PACKED, 2, 1, kSlotUp, kUpTiles, 2, kUpWaves, 1>(s.f, expert, int64_t(strip) * kUpTiles * kTile, 0,
+                                                                       slot, slot + 1, lds);
+}
+
+// Y of 16 rows of one token: the waves share the token's slots, or several waves
+// a slot's K where there are fewer slots than waves; the slots' outputs are added
+// in the order of their ranks.
+template <bool PACKED, int P>
+__global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const SlotArgs s, const CombineArgs y) {
+    __shared__ u32x4 lds[kSlotWaves * P * 2 * 32];
+    __shared__ float sums[kMaxTopk > kSlotWaves ? kMaxTopk : kSlotWaves][kTile];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    // the workgroups of a strip lie on the same die, whose L2 serves experts that
+    // tokens share
+    const uint32_t tokens = static_cast<uint32_t>(y.tokens), b = blockIdx.x / kXcds;
+    const int64_t strip = int64_t(b / tokens) * kXcds + blockIdx.x % kXcds, t = b % tokens;
+    if (strip * kTile >= s.f.m) return;   // workgroup-uniform
+    const int topk = y.topk, share = topk < kSlotWaves ? kSlotWaves / topk : 1;
+    for (int j = wave / share; j < topk; j += kSlotWaves / share) {
+        const int32_t slot = static_cast<int32_t>(t * topk + j);
+        f32x4 acc[1][1];
+        stream_sums<true, PACKED, 1, P, kSlotDown, 1, 4, 1>(s.f, s.r.choice[slot], strip * kTile, 0, slot, slot + 1,
+                                                            lds + wave * (P * 2 * 32), wave % share, share, acc);
+        if (lane % 16 == 0)
+            *reinterpret_cast<f32x4 *>(&sums[j * share + wave % share][4 * (lane / 16)]) = acc[0][0];
+    }
+    __syncthreads();
+    if (threadIdx.x >= kTile) return;
+    const int64_t r = strip * kTile + threadIdx.x;
+    float out = 0.0f;
+    for (int j = 0; j < topk; ++j) {
+        const int64_t slot = t * topk + j;
+        float v = sums[j * share][threadIdx.x];
+        for (int i = 1; i < share; ++i) v += sums[j * share + i][threadIdx.x];
+        out += y.weights[slot] * ((s.f.alpha ? s.f.alpha[s.r.choice[slot]] : 1.0f) * v);
+    }
+    if (y.residual) out += load_as_float(y.residual, t * y.ldr + r, y.y_type);
+    store_rounded(y.Y, t * y.ldy + r, y.y_type, out);
 }
 
 }  // namespace

@@ -182,6 +182,13 @@ inline int64_t moe_groups(const nvfp4_moe_layer_t &l, int64_t tokens) {
     return tokens * l.topk < l.experts ? tokens * l.topk : l.experts;
 }
 
+// Whether slots are taken one by one rather than by expert.
+inline bool few_slots(const nvfp4_moe_layer_t &l, int64_t tokens) {
+    const int64_t slots = tokens * l.topk;
+    return (tokens == 1 || 4 * slots <= l.experts) && slots * ceil_div(l.inter, kTile) < kMaxTiles &&
+           tokens * (ceil_div(l.hidden, kTile) + 8) < kMaxTiles / 2;
+}
+
 // Parts of hidden that the logits are summed in: 512 elements each, while that
 // makes no more workgroups than there are compute units.
 inline int64_t route_splits(const nvfp4_moe_layer_t &l, int64_t tokens) {

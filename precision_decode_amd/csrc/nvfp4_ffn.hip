@@ -265,9 +265,6 @@ int check_moe(const MoeCall &c) {
     return NVFP4_GEMV_OK;
 }
 
-constexpr int kUpTiles = 2, kUpWaves = 4;       // per workgroup: row tiles of gate and of up, waves
-constexpr int kDownTiles = 4, kDownWaves = 2;
-
 template <bool BF16, bool PACKED>
 int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
     return run(ffn_stream<BF16, PACKED, 2, 1, kMoeUp, kUpTiles, 2, kUpWaves, 8>,
@@ -295,6 +292,15 @@ int launch_down(const FfnArgs &a, bool packed, bool fast, int planes, int64_t gr
     const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * groups));
     return planes == 2 ? launch_simple<true, 1, 2, kMoeDown>(a, packed, grid, stream)
                        : launch_simple<true, 1, 3, kMoeDown>(a, packed, grid, stream);
+}
+
+template <bool PACKED>
+int launch_slot_down(const SlotArgs &s, const CombineArgs &y, int planes, hipStream_t stream) {
+    void *args[] = {const_cast<SlotArgs *>(&s), const_cast<CombineArgs *>(&y)};
+    const void *fn = planes == 2 ? reinterpret_cast<const void *>(ffn_slot_down<PACKED, 2>)
+                                 : reinterpret_cast<const void *>(ffn_slot_down<PACKED, 3>);
+    const int64_t strips = ceil_div(ceil_div(s.f.m, kTile), kXcds) * kXcds;
+    return run(fn, dim3(static_cast<uint32_t>(strips * y.tokens)), kSlotWaves * kWave, args, stream);
 }
 
 int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
@@ -327,53 +333,48 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     const dim3 route_grid(static_cast<uint32_t>(ceil_div(l.experts, kTile) * r.splits),
                           static_cast<uint32_t>(ceil_div(c.tokens, kTile)));
     int s = run(bf16 ? route_logits<true> : route_logits<false>, route_grid, kRouteWaves * kWave, r, stream);
-    if (s == NVFP4_GEMV_OK) s = run(route_select, dim3(1), kSelectWaves * kWave, r, stream);
     if (s != NVFP4_GEMV_OK) return s;
 
     const int planes = c.y_type == NVFP4_OUT_F32 ? 3 : 2;
-    FfnArgs a = {};
-    a.splits = 1;
-    a.X = r.X;
-    a.ldx = c.ldx;
-    bool fast = fast_weight(l.W13, l.sf13, l.hidden);
-    if (fast && !aligned_rows(c.X, c.ldx)) {
+    FfnArgs up = {};
+    up.splits = 1;
+    up.X = r.X;
+    up.ldx = c.ldx;
+    bool fast_up = fast_weight(l.W13, l.sf13, l.hidden);
+    if (fast_up && !aligned_rows(c.X, c.ldx)) {
         s = copy_aligned(c.X, c.ldx, ws + w.x, c.tokens, l.hidden, stream);
         if (s != NVFP4_GEMV_OK) return s;
-        a.X = ws + w.x;
-        a.ldx = l.hidden;
+        up.X = ws + w.x;
+        up.ldx = l.hidden;
     }
-    fast = fast && c.tokens * a.ldx * 2 < kMaxStreamBytes;
-    a.plane = slots * l.inter;
-    a.W = l.W13;
-    a.sW = l.sf13;
-    a.alpha = l.alpha13;
-    a.Y = ws + w.h;
-    a.ldy = l.inter;
-    a.offsets = r.offsets;
-    a.list = r.list;
-    a.active = r.active;
-    a.n = c.tokens;
-    a.m = l.inter;
-    a.k = l.hidden;
-    a.topk = l.topk;
-    a.act = l.activation;
-    a.y_planes = planes;
-    s = bf16 ? launch_up<true>(a, packed, fast, r.groups, stream)
-             : launch_up<false>(a, packed, fast, r.groups, stream);
-    if (s != NVFP4_GEMV_OK) return s;
+    fast_up = fast_up && c.tokens * up.ldx * 2 < kMaxStreamBytes;
+    const bool fast_down = fast_weight(l.W2, l.sf2, l.inter) && slots * l.inter * 2 < kMaxStreamBytes;
+    up.plane = slots * l.inter;
+    up.W = l.W13;
+    up.sW = l.sf13;
+    up.alpha = l.alpha13;
+    up.Y = ws + w.h;
+    up.ldy = l.inter;
+    up.offsets = r.offsets;
+    up.list = r.list;
+    up.active = r.active;
+    up.n = c.tokens;
+    up.m = l.inter;
+    up.k = l.hidden;
+    up.topk = l.topk;
+    up.act = l.activation;
+    up.y_planes = planes;
 
-    a.X = ws + w.h;
-    a.ldx = l.inter;
-    a.W = l.W2;
-    a.sW = l.sf2;
-    a.alpha = l.alpha2;
-    a.Y = ws + w.part;
-    a.ldy = l.hidden;
-    a.m = l.hidden;
-    a.k = l.inter;
-    fast = fast_weight(l.W2, l.sf2, l.inter) && slots * l.inter * 2 < kMaxStreamBytes;
-    s = launch_down(a, packed, fast, planes, r.groups, stream);
-    if (s != NVFP4_GEMV_OK) return s;
+    FfnArgs down = up;
+    down.X = ws + w.h;
+    down.ldx = l.inter;
+    down.W = l.W2;
+    down.sW = l.sf2;
+    down.alpha = l.alpha2;
+    down.Y = ws + w.part;
+    down.ldy = l.hidden;
+    down.m = l.hidden;
+    down.k = l.inter;
 
     CombineArgs y = {};
     y.part = reinterpret_cast<const float *>(ws + w.part);
@@ -386,6 +387,24 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     y.hidden = l.hidden;
     y.topk = l.topk;
     y.y_type = c.y_type;
+
+    if (few_slots(l, c.tokens) && fast_up && fast_down) {
+        const SlotArgs u = {up, r}, d = {down, r};
+        const dim3 grid(static_cast<uint32_t>(ceil_div(l.inter, kUpTiles * kTile) * slots));
+        s = bf16 ? packed ? run(ffn_slot_up<true, true>, grid, kUpWaves * kWave, u, stream)
+                          : run(ffn_slot_up<true, false>, grid, kUpWaves * kWave, u, stream)
+            : packed ? run(ffn_slot_up<false, true>, grid, kUpWaves * kWave, u, stream)
+                     : run(ffn_slot_up<false, false>, grid, kUpWaves * kWave, u, stream);
+        if (s != NVFP4_GEMV_OK) return s;
+        return packed ? launch_slot_down<true>(d, y, planes, stream) : launch_slot_down<false>(d, y, planes, stream);
+    }
+
+    s = run(route_select, dim3(1), kSelectWaves * kWave, r, stream);
+    if (s == NVFP4_GEMV_OK)
+        s = bf16 ? launch_up<true>(up, packed, fast_up, r.groups, stream)
+                 : launch_up<false>(up, packed, fast_up, r.groups, stream);
+    if (s == NVFP4_GEMV_OK) s = launch_down(down, packed, fast_down, planes, r.groups, stream);
+    if (s != NVFP4_GEMV_OK) return s;
     return run(moe_combine,
                dim3(static_cast<uint32_t>(ceil_div(l.hidden, 4 * kCombineThreads)), static_cast<uint32_t>(c.tokens)),
                kCombineThreads, y, stream);
