@@ -247,6 +247,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():
+            # the handle itself: building a Stream object around it takes longer than a launch
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -603,34 +606,36 @@ def _named(table, name, what):
 def _float_type(dtype, what, f32=False):
     import torch
 
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return NVFP4_OUT_BF16
-    if dtype == torch.float16:
+    if dtype is torch.float16:
         return NVFP4_OUT_F16
-    if f32 and dtype == torch.float32:
+    if f32 and dtype is torch.float32:
         return NVFP4_OUT_F32
     raise ValueError(f"{what} must be bfloat16{', float16 or float32' if f32 else ' or float16'}")
 
 
 def _rows(t, what, shape, dtype=None):
     """Element stride of the rows of a 2-D device tensor whose columns are contiguous."""
-    if t.dim() != 2 or tuple(t.shape) != shape or not t.is_cuda or (dtype is not None and t.dtype != dtype):
+    if t.shape != shape or not t.is_cuda or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{what} must be a device tensor of shape {shape}"
                          f"{'' if dtype is None else f' and {dtype}'}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1:
         raise ValueError(f"{what} must have contiguous columns")
     # a single row's stride is free; torch reports anything there
-    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    ld = rows if shape[0] > 1 else shape[1]
     if ld < shape[1]:
         raise ValueError(f"{what} must have rows that do not overlap")
     return ld
 
 
 def _floats(t, count, what):
+    if t is None:
+        return
     import torch
 
-    if t is not None and (t.dtype != torch.float32 or t.numel() != count or not t.is_contiguous()
-                          or not t.is_cuda):
+    if t.dtype is not torch.float32 or t.numel() != count or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{what} must be a contiguous float32 device tensor of {count} values")
 
 
@@ -638,13 +643,11 @@ def _weight(codes, scales, groups, rows, k, packed, what):
     """Checks codes and scales of ``groups`` matrices of rows x k in either layout."""
     import torch
 
-    if packed:
-        want = nvfp4_mma_packed_sizes(groups, rows, k)
-    else:
-        want = (groups * rows * (k // 2), groups * rows * (k // 16))
-    for t, count, name in ((codes, want[0], "codes"), (scales, want[1], "scales")):
-        if t.dtype != torch.uint8 or t.numel() != count or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{what} {name} must be a contiguous uint8 device tensor of {count} bytes")
+    # packed: whole tiles of 16 rows and windows of 256 elements, as nvfp4_mma_packed_sizes says
+    count = groups * (-(-rows // 16) * 16) * (-(-k // 256) * 256) if packed else groups * rows * k
+    for t, want, name in ((codes, count // 2, "codes"), (scales, count // 16, "scales")):
+        if t.dtype is not torch.uint8 or t.numel() != want or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{what} {name} must be a contiguous uint8 device tensor of {want} bytes")
 
 
 def _output(out, out_dtype, n, m, x, residual, stream):
@@ -654,18 +657,25 @@ def _output(out, out_dtype, n, m, x, residual, stream):
 
     if out is None:
         dtype = x.dtype if out_dtype is None else out_dtype
-        _float_type(dtype, "out_dtype", f32=True)
+        y_type = _float_type(dtype, "out_dtype", f32=True)
         if isinstance(stream, torch.cuda.Stream):
             with torch.cuda.stream(stream):
                 out = torch.empty((n, m), dtype=dtype, device=x.device)
         else:
             out = torch.empty((n, m), dtype=dtype, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out_dtype differs from out's type")
-    y_type = _float_type(out.dtype, "out", f32=True)
-    ldy = _rows(out, "out", (n, m))
+        ldy = m
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out_dtype differs from out's type")
+        y_type = _float_type(out.dtype, "out", f32=True)
+        ldy = _rows(out, "out", (n, m))
     ldr = 0 if residual is None else _rows(residual, "residual", (n, m), out.dtype)
     return out, y_type, ldy, ldr
+
+
+def _address(t):
+    """Address of a tensor that has been checked to be on a device, or None."""
+    return None if t is None else t.data_ptr()
 
 
 def linear(x, codes, scales, m, alpha=None, bias=None, residual=None, activation="none", gated=False,
@@ -691,8 +701,11 @@ def linear(x, codes, scales, m, alpha=None, bias=None, residual=None, activation
     act = _named(_ACTIVATIONS, activation, "activation") | (NVFP4_ACT_GATED if gated else 0)
     out, y_type, ldy, ldr = _output(out, out_dtype, n, m, x, residual, stream)
     if n > 0:
-        nvfp4_linear_launch(x, x_type, ldx, codes, scales, NVFP4_W_PACKED if packed else NVFP4_W_ROW_MAJOR,
-                            alpha, bias, residual, ldr, out, y_type, ldy, n, m, k, act, stream)
+        _check(load().nvfp4_linear_launch(
+            x.data_ptr(), x_type, ldx, codes.data_ptr(), scales.data_ptr(),
+            NVFP4_W_PACKED if packed else NVFP4_W_ROW_MAJOR, _address(alpha), _address(bias),
+            _address(residual), ldr, out.data_ptr(), y_type, ldy, n, m, k, act, _stream(stream)),
+            "nvfp4_linear_launch")
     return out
 
 
@@ -729,6 +742,7 @@ class MoeLayer:
             activation=_named(_ACTIVATIONS, activation, "activation"),
             scoring=_named(_SCORINGS, scoring, "scoring"), renormalize=int(bool(renormalize)),
             routed_scale=routed_scale, reserved=0)
+        self.reference = ctypes.byref(self.struct)
 
 
 def _moe_struct(layer):
@@ -746,5 +760,7 @@ def moe_layer(x, layer, residual=None, out=None, out_dtype=None, stream=None):
     ldx = _rows(x, "x", (n, layer.hidden), layer.dtype)
     out, y_type, ldy, ldr = _output(out, out_dtype, n, layer.hidden, x, residual, stream)
     if n > 0:
-        nvfp4_moe_layer_launch(layer, x, ldx, residual, ldr, out, y_type, ldy, n, stream)
+        _check(load().nvfp4_moe_layer_launch(layer.reference, x.data_ptr(), ldx, _address(residual), ldr,
+                                             out.data_ptr(), y_type, ldy, n, _stream(stream)),
+               "nvfp4_moe_layer_launch")
     return out

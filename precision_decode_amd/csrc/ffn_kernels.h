@@ -356,20 +356,32 @@ __device__ __forceinline__ void decode32(u32x4 q, uint32_t s, u32x4 (&o)[4]) {
     }
 }
 
+// Weight layouts of the fast kernels.
+enum Layout {
+    kRows = 0,          // row-major, k a multiple of 64, codes on 16 bytes and scales on 4
+    kPackedTiles = 1,   // nvfp4_mma_pack_weight's
+    kRows16 = 2,        // row-major, any k and scales, codes on 4 bytes
+};
+
 constexpr int kWinCodeBytes = 2048, kWinScaleBytes = 256;   // of a packed window of a tile
 constexpr int kAnyRange = 0x7FFFFFF0;   // descriptor range where every used offset is known to be valid
 
 // The weights of one matrix as a workgroup reads them: R tiles of 16 rows from
 // row0, window by window (256 elements of K).  Lane i + 16 q holds, of row i of
-// each tile, the 64 elements from 64 q on: two 16-byte loads and their four
-// scales.  Rows past m and elements past k read zeros without touching memory.
-template <bool PACKED, int R>
+// each tile, the 64 elements from 64 q on, in two halves, and their four scales.
+// Rows past m and elements past k read zeros without touching memory; `left` is
+// the number of elements from the window on that exist.  L = kRows16: k is any
+// multiple of 16 and the scales have any alignment, so the codes come in loads of
+// a block each and the scales byte by byte.
+template <int L, int R>
 struct WeightTiles {
     __amdgpu_buffer_rsrc_t wdesc, sdesc;
     uint32_t code[R], scale[R];   // the lane's offsets at window 0 (or out of range)
+    int first;                    // the lane's first element of a window
 
-    __device__ __forceinline__ WeightTiles(const FfnArgs &a, int64_t matrix, int64_t row0, int li, int kq) {
-        if (PACKED) {
+    __device__ __forceinline__ WeightTiles(const FfnArgs &a, int64_t matrix, int64_t row0, int li, int kq)
+        : first(64 * kq) {
+        if (L == kPackedTiles) {
             const int64_t wins = (a.k + kWinElems - 1) / kWinElems, tiles = (a.m + kTile - 1) / kTile;
             const int64_t t0 = matrix * tiles + row0 / kTile;
             wdesc = buffer_of(a.W + t0 * wins * kWinCodeBytes, kAnyRange);
@@ -393,23 +405,43 @@ struct WeightTiles {
             }
         }
     }
-    // `past`: kOutOfRange when the lane's elements lie past k, else 0.  POLICY:
-    // kNonTemporal for weights that are read once.
+    __device__ __forceinline__ uint32_t past(int left, int block) const {
+        return first + 16 * block < left ? 0u : kOutOfRange;
+    }
+    // POLICY: kNonTemporal for weights that are read once.
     template <int POLICY>
-    __device__ __forceinline__ void load_half(int r, uint32_t window, uint32_t past, int h, u32x4 &q) const {
-        q = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                          wdesc, (code[r] | past) + h * (PACKED ? 1024 : 16),
-                                          window * (PACKED ? kWinCodeBytes : 128), POLICY));
+    __device__ __forceinline__ void load_half(int r, uint32_t window, int left, int h, u32x4 &q) const {
+        if constexpr (L == kRows16) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b64(
+                    wdesc, (code[r] + 16 * h + 8 * b) | past(left, 2 * h + b), window * 128, 0);
+                q[2 * b] = v[0];
+                q[2 * b + 1] = v[1];
+            }
+        } else {
+            q = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                              wdesc, (code[r] | past(left, 0)) + h * (L == kPackedTiles ? 1024 : 16),
+                                              window * (L == kPackedTiles ? kWinCodeBytes : 128), POLICY));
+        }
     }
     template <int POLICY>
-    __device__ __forceinline__ void load_scale(int r, uint32_t window, uint32_t past, uint32_t &s) const {
-        s = __builtin_amdgcn_raw_buffer_load_b32(sdesc, scale[r] | past, window * (PACKED ? kWinScaleBytes : 16),
-                                                 POLICY);
+    __device__ __forceinline__ void load_scale(int r, uint32_t window, int left, uint32_t &s) const {
+        if constexpr (L == kRows16) {
+            s = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                s |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sdesc, (scale[r] + b) | past(left, b), window * 16, 0))
+                     << (8 * b);
+        } else {
+            s = __builtin_amdgcn_raw_buffer_load_b32(sdesc, scale[r] | past(left, 0),
+                                                     window * (L == kPackedTiles ? kWinScaleBytes : 16), POLICY);
+        }
     }
-    __device__ __forceinline__ void load(int r, uint32_t window, uint32_t past, u32x4 (&q)[2], uint32_t &s) const {
-        load_half<kNonTemporal>(r, window, past, 0, q[0]);
-        load_half<kNonTemporal>(r, window, past, 1, q[1]);
-        load_scale<PACKED ? kNonTemporal : 0>(r, window, past, s);
+    __device__ __forceinline__ void load(int r, uint32_t window, int left, u32x4 (&q)[2], uint32_t &s) const {
+        load_half<kNonTemporal>(r, window, left, 0, q[0]);
+        load_half<kNonTemporal>(r, window, left, 1, q[1]);
+        load_scale<L == kPackedTiles ? kNonTemporal : 0>(r, window, left, s);
     }
 };
 
@@ -433,7 +465,7 @@ __device__ __forceinline__ void wave_lds_fence() {
 // instruction would touch a different line in every lane.  The 16-byte pieces
 // are swizzled by the token, so the 16 lanes that read the same piece of 16
 // tokens hit distinct banks.  NX = instructions = half the tokens staged.
-template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int NX>
+template <bool BF16, int L, int G, int P, int MODE, int R, int U, int NX>
 __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
                                             int32_t end, u32x4 *slot, int wave, int waves, f32x4 (&acc)[G][R]) {
     const int lane = threadIdx.x & (kWave - 1);
@@ -444,8 +476,8 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
     const int nwin = static_cast<int>(int64_t(split + 1) * wins / a.splits) - win0;
     const int niter = nwin > wave ? (nwin - wave + waves - 1) / waves : 0;
 
-    const WeightTiles<PACKED, R> w0(a, G * int64_t(expert), row0, li, kq);
-    const WeightTiles<PACKED, R> w1(a, G * int64_t(expert) + (G - 1), row0, li, kq);
+    const WeightTiles<L, R> w0(a, G * int64_t(expert), row0, li, kq);
+    const WeightTiles<L, R> w1(a, G * int64_t(expert) + (G - 1), row0, li, kq);
 
     // X: kLinear from token p0 on, else from row 0 (the host keeps rows * ldx in 31 bits)
     const uint8_t *xbase = a.X + (MODE == kLinear ? 2 * (int64_t(p0) * a.ldx) : 0);
@@ -476,11 +508,11 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
             for (int j = 0; j < NX; ++j)
                 xq[u][p][j] = __builtin_bit_cast(
                     u32x4, __builtin_amdgcn_raw_buffer_load_b128(xdesc[p], (xo[j] + win * 512) | xpast, 0, 0));
-        const uint32_t past = run && win * kWinElems + 64 * kq < k ? 0u : kOutOfRange;
+        const int left = run ? static_cast<int>(k - win * kWinElems) : 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            w0.load(r, win, past, wq[u][0][r], ws[u][0][r]);
-            if constexpr (G == 2) w1.load(r, win, past, wq[u][1][r], ws[u][1][r]);
+            w0.load(r, win, left, wq[u][0][r], ws[u][0][r]);
+            if constexpr (G == 2) w1.load(r, win, left, wq[u][1][r], ws[u][1][r]);
         }
     };
 #pragma unroll
@@ -540,14 +572,14 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
 // One workgroup owns R tiles of 16 rows of each of G matrices and up to 2 NX
 // tokens; its W waves take the windows of its part of K in turn, and their sums
 // are added in wave order through LDS.
-template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int W, int NX>
+template <bool BF16, int L, int G, int P, int MODE, int R, int U, int W, int NX>
 __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
                                             int32_t end, u32x4 *lds) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int li = lane & 15, kq = lane >> 4;
     f32x4 acc[G][R];
-    stream_sums<BF16, PACKED, G, P, MODE, R, U, NX>(a, expert, row0, split, p0, end,
+    stream_sums<BF16, L, G, P, MODE, R, U, NX>(a, expert, row0, split, p0, end,
                                                     lds + wave * (P * 2 * NX * 32), wave, W, acc);
 
     // wave r % W finishes row tile r
@@ -584,14 +616,14 @@ constexpr int stream_lds() {
     return W * kWave * (P * NX > G * R ? P * NX : G * R);
 }
 
-template <bool BF16, bool PACKED, int G, int P, int MODE, int R, int U, int W, int NXMAX>
+template <bool BF16, int L, int G, int P, int MODE, int R, int U, int W, int NXMAX>
 __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
     __shared__ u32x4 lds[stream_lds<G, P, R, W, NXMAX>()];
     const uint32_t strips = static_cast<uint32_t>((a.m + R * kTile - 1) / (R * kTile));
     const uint32_t q = blockIdx.x / strips;   // split, or place in the list of experts
     const int64_t row0 = int64_t(blockIdx.x - q * strips) * (R * kTile);
     if constexpr (MODE == kLinear) {
-        stream_pass<BF16, PACKED, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q, 0, static_cast<int32_t>(a.n), lds);
+        stream_pass<BF16, L, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q, 0, static_cast<int32_t>(a.n), lds);
     } else {
         const int expert = a.active[q];
         if (expert < 0) return;   // workgroup-uniform
@@ -600,13 +632,13 @@ __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
             const int32_t end = range.end - p > 2 * NXMAX ? p + 2 * NXMAX : range.end;
             const int n = end - p;   // workgroup-uniform
             if (n <= 2)
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 1>(a, expert, row0, 0, p, end, lds);
+                stream_pass<BF16, L, G, P, MODE, R, U, W, 1>(a, expert, row0, 0, p, end, lds);
             else if (n <= 4)
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 2>(a, expert, row0, 0, p, end, lds);
+                stream_pass<BF16, L, G, P, MODE, R, U, W, 2>(a, expert, row0, 0, p, end, lds);
             else if (NXMAX == 4 || n <= 8)
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, 4>(a, expert, row0, 0, p, end, lds);
+                stream_pass<BF16, L, G, P, MODE, R, U, W, 4>(a, expert, row0, 0, p, end, lds);
             else
-                stream_pass<BF16, PACKED, G, P, MODE, R, U, W, NXMAX>(a, expert, row0, 0, p, end, lds);
+                stream_pass<BF16, L, G, P, MODE, R, U, W, NXMAX>(a, expert, row0, 0, p, end, lds);
         }
     }
 }
@@ -722,7 +754,7 @@ struct TileShape {
 // tokens' copies, 15 for the weights' loads and 12-25 for the decode.  Tiles of
 // 256 x 256, whose 128 sums per lane leave too few registers to decode ahead,
 // took 236-263 us.
-template <bool BF16, bool PACKED, int G, int Q, int NT, int WM, int WN, int WK>
+template <bool BF16, int L, int G, int Q, int NT, int WM, int WN, int WK>
 __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     using S = TileShape<G, Q, NT, WM, WN, WK>;
     constexpr int RT = G * Q;
@@ -754,8 +786,8 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     const int win0 = static_cast<int>(int64_t(split) * wins / a.splits);
     const int win1 = static_cast<int>(int64_t(split + 1) * wins / a.splits);
 
-    const WeightTiles<PACKED, Q> w0(a, 0, row0, li, kq);
-    const WeightTiles<PACKED, Q> w1(a, G - 1, row0, li, kq);
+    const WeightTiles<L, Q> w0(a, 0, row0, li, kq);
+    const WeightTiles<L, Q> w1(a, G - 1, row0, li, kq);
 
     // staging: copy i of 4 tokens: lane l fills position l % 16 of token t = 4 i + l / 16
     // with piece (l % 16) ^ (t & 15); piece 4 q + c holds elements 64 q + 32 h + 8 c
@@ -778,18 +810,18 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
         constexpr int h = decltype(hc)::value;
         const int left = win < win1 ? static_cast<int>(k - win * kWinElems) : 0;   // elements from this window on
         lds_void_t *to = h == 0 ? (lds_void_t *)lds0 : (lds_void_t *)lds1;
-        const uint32_t past = 64 * kq < left ? 0u : kOutOfRange;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const WeightTiles<PACKED, Q> &w = r < Q ? w0 : w1;
-            w.template load_half<0>(r % Q, win, past, h, wq[h][r]);
-            if (h == 0) w.template load_scale<0>(r % Q, win, past, ws[slot][r]);
+            const WeightTiles<L, Q> &w = r < Q ? w0 : w1;
+            w.template load_half<0>(r % Q, win, left, h, wq[h][r]);
+            if (h == 0) w.template load_scale<0>(r % Q, win, left, ws[slot][r]);
         }
 #pragma unroll
         for (int j = 0; j < kCopies; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 xdesc, to + 16 * S::stage * kg + 1024 * (kCopies * gwave + j), 16,
-                xo[j] | (64 * ((piece >> 2) ^ (j & 3)) < left ? 0u : kOutOfRange),
+                xo[j] | (64 * ((piece >> 2) ^ (j & 3)) + (L == kRows16 ? 32 * h + 8 * (piece & 3) : 0) < left ? 0u
+                                                                                                       : kOutOfRange),
                 2 * (win * kWinElems + 32 * h), 0, 0);
     };
     f32x4 acc[RT][NT] = {};
@@ -993,9 +1025,9 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     }
 }
 
-template <bool BF16, bool PACKED, int G, int Q, int NT, int WM, int WN, int WK>
+template <bool BF16, int L, int G, int Q, int NT, int WM, int WN, int WK>
 __global__ void __launch_bounds__(WM *WN *WK *kWave, 2) ffn_tile(const FfnArgs a) {
-    tile_product<BF16, PACKED, G, Q, NT, WM, WN, WK>(a);
+    tile_product<BF16, L, G, Q, NT, WM, WN, WK>(a);
 }
 
 // ---------------------------------------------------------------- split sums
@@ -1362,7 +1394,7 @@ __device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j,
 }
 
 // h of one slot: workgroup = strip of rows and slot.
-template <bool BF16, bool PACKED>
+template <bool BF16, int L>
 __global__ void __launch_bounds__(kUpWaves * kWave, 2) ffn_slot_up(const SlotArgs s) {
     __shared__ u32x4 lds[stream_lds<2, 1, kUpTiles, kUpWaves, 1>()];
     const uint32_t strips = static_cast<uint32_t>((s.f.m + kUpTiles * kTile - 1) / (kUpTiles * kTile));
@@ -1370,14 +1402,14 @@ __global__ void __launch_bounds__(kUpWaves * kWave, 2) ffn_slot_up(const SlotArg
     const uint32_t token = slot / s.r.topk;
     const int expert = __builtin_amdgcn_readfirstlane(
         choose_slot<kUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
-    stream_pass<BF16, PACKED, 2, 1, kSlotUp, kUpTiles, 2, kUpWaves, 1>(s.f, expert, int64_t(strip) * kUpTiles * kTile, 0,
+    stream_pass<BF16, L, 2, 1, kSlotUp, kUpTiles, 2, kUpWaves, 1>(s.f, expert, int64_t(strip) * kUpTiles * kTile, 0,
                                                                        slot, slot + 1, lds);
 }
 
 // Y of 16 rows of one token: the waves share the token's slots, or several waves
 // a slot's K where there are fewer slots than waves; the slots' outputs are added
 // in the order of their ranks.
-template <bool PACKED, int P>
+template <int L, int P>
 __global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const SlotArgs s, const CombineArgs y) {
     __shared__ u32x4 lds[kSlotWaves * P * 2 * 32];
     __shared__ float sums[kMaxTopk > kSlotWaves ? kMaxTopk : kSlotWaves][kTile];
@@ -1392,7 +1424,7 @@ __global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const Slo
     for (int j = wave / share; j < topk; j += kSlotWaves / share) {
         const int32_t slot = static_cast<int32_t>(t * topk + j);
         f32x4 acc[1][1];
-        stream_sums<true, PACKED, 1, P, kSlotDown, 1, 4, 1>(s.f, s.r.choice[slot], strip * kTile, 0, slot, slot + 1,
+        stream_sums<true, L, 1, P, kSlotDown, 1, 4, 1>(s.f, s.r.choice[slot], strip * kTile, 0, slot, slot + 1,
                                                             lds + wave * (P * 2 * 32), wave % share, share, acc);
         if (lane % 16 == 0)
             *reinterpret_cast<f32x4 *>(&sums[j * share + wave % share][4 * (lane / 16)]) = acc[0][0];

@@ -56,10 +56,9 @@ int run(void (*fn)(A), dim3 grid, int threads, A a, hipStream_t stream) {
     return run(reinterpret_cast<const void *>(fn), grid, threads, args, stream);
 }
 
-template <bool BF16, int G, int P, int MODE>
-int launch_simple(const FfnArgs &a, bool packed, dim3 grid, hipStream_t stream) {
-    return run(packed ? ffn_simple<BF16, true, G, P, MODE> : ffn_simple<BF16, false, G, P, MODE>, grid,
-               kSimpleWaves * kWave, a, stream);
+template <bool BF16, bool PACKED, int G, int P, int MODE>
+int launch_simple(const FfnArgs &a, dim3 grid, hipStream_t stream) {
+    return run(ffn_simple<BF16, PACKED, G, P, MODE>, grid, kSimpleWaves * kWave, a, stream);
 }
 
 // ---------------------------------------------------------------- linear
@@ -117,49 +116,56 @@ int check_linear(const LinearCall &c) {
     return NVFP4_GEMV_OK;
 }
 
-template <bool BF16, bool PACKED, int G, int NX>
+template <bool BF16, int L, int G, int NX>
 int launch_linear_stream(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
     constexpr int R = stream_tiles(G == 2);
-    return run(ffn_stream<BF16, PACKED, G, 1, kLinear, R, 2, kStreamWaves, NX>,
+    return run(ffn_stream<BF16, L, G, 1, kLinear, R, 2, kStreamWaves, NX>,
                dim3(static_cast<uint32_t>(p.strips * p.splits)), kStreamWaves * kWave, a, stream);
 }
 
-template <bool BF16, bool PACKED, int G, int KIND>
+template <bool BF16, int L, int G, int KIND>
 int launch_tile(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
     constexpr TileKind t = G == 2 ? kGatedTileKinds[KIND % kNumGatedTileKinds] : kTileKinds[KIND];
-    return run(ffn_tile<BF16, PACKED, G, t.q, t.nt, t.wm, 1, t.wk>,
+    return run(ffn_tile<BF16, L, G, t.q, t.nt, t.wm, 1, t.wk>,
                dim3(static_cast<uint32_t>(p.strips * p.blocks * p.splits)), t.waves() * kWave, a, stream);
 }
 
-template <bool BF16, bool PACKED, int G>
+template <bool BF16, int L, int G>
 int launch_linear(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
     if (p.stream)
-        return a.n <= 2   ? launch_linear_stream<BF16, PACKED, G, 1>(a, p, stream)
-               : a.n <= 4 ? launch_linear_stream<BF16, PACKED, G, 2>(a, p, stream)
-               : a.n <= 8 ? launch_linear_stream<BF16, PACKED, G, 4>(a, p, stream)
-                          : launch_linear_stream<BF16, PACKED, G, 8>(a, p, stream);
+        return a.n <= 2   ? launch_linear_stream<BF16, L, G, 1>(a, p, stream)
+               : a.n <= 4 ? launch_linear_stream<BF16, L, G, 2>(a, p, stream)
+               : a.n <= 8 ? launch_linear_stream<BF16, L, G, 4>(a, p, stream)
+                          : launch_linear_stream<BF16, L, G, 8>(a, p, stream);
     switch (p.tile) {
-    case 0: return launch_tile<BF16, PACKED, G, 0>(a, p, stream);
-    case 1: return launch_tile<BF16, PACKED, G, 1>(a, p, stream);
-    case 2: return launch_tile<BF16, PACKED, G, 2>(a, p, stream);
-    case 3: return launch_tile<BF16, PACKED, G, 3>(a, p, stream);
-    case 4:
-        if constexpr (G == 1) return launch_tile<BF16, PACKED, 1, 4>(a, p, stream);
+    case 0: return launch_tile<BF16, L, G, 0>(a, p, stream);
+    case 1: return launch_tile<BF16, L, G, 1>(a, p, stream);
+    case 2: return launch_tile<BF16, L, G, 2>(a, p, stream);
+    case 3: return launch_tile<BF16, L, G, 3>(a, p, stream);
     }
-    return launch_simple<BF16, G, 1, kLinear>(
-        a, PACKED, dim3(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile))), stream);
+    if constexpr (G == 1) return launch_tile<BF16, L, 1, 4>(a, p, stream);
+    return NVFP4_GEMV_ERR_LAUNCH;   // the plan has no such shape
 }
 
-template <bool BF16>
-int launch_linear(const FfnArgs &a, const LinearPlan &p, bool packed, bool gated, hipStream_t stream) {
-    return packed ? gated ? launch_linear<BF16, true, 2>(a, p, stream) : launch_linear<BF16, true, 1>(a, p, stream)
-                  : gated ? launch_linear<BF16, false, 2>(a, p, stream) : launch_linear<BF16, false, 1>(a, p, stream);
+// Layout of a weight for the fast kernels, or kNoLayout for the simple one.
+constexpr int kNoLayout = -1;
+int layout_of(const void *W, const void *sf, int64_t k, int32_t w_layout) {
+    if (w_layout == NVFP4_W_PACKED) return kPackedTiles;
+    if (k % 64 == 0 && !misaligned(W, 16) && !misaligned(sf, 4)) return kRows;
+    return misaligned(W, 4) ? kNoLayout : kRows16;
 }
 
-// Whether the weight's pointers and K suit the fast kernels.
-bool fast_weight(const void *W, const void *sf, int64_t k) {
-    return k % 64 == 0 && !misaligned(W, 16) && !misaligned(sf, 4);
+template <bool BF16, int G>
+int launch_linear(const FfnArgs &a, const LinearPlan &p, int layout, hipStream_t stream) {
+    switch (layout) {
+    case kRows: return launch_linear<BF16, kRows, G>(a, p, stream);
+    case kPackedTiles: return launch_linear<BF16, kPackedTiles, G>(a, p, stream);
+    case kRows16: return launch_linear<BF16, kRows16, G>(a, p, stream);
+    }
+    return launch_simple<BF16, false, G, 1, kLinear>(
+        a, dim3(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile))), stream);
 }
+
 // Whether rows start on 16-byte boundaries, `piece` elements being 16 bytes.
 bool aligned_rows16(const void *p, int64_t ld, int64_t piece) { return !misaligned(p, 16) && ld % piece == 0; }
 bool aligned_rows(const void *X, int64_t ldx) { return aligned_rows16(X, ldx, 8); }
@@ -173,7 +179,8 @@ int copy_aligned(const void *X, int64_t ldx, void *to, int64_t rows, int64_t k, 
 }
 
 LinearPlan plan_of(const LinearCall &c) {
-    return plan_linear(c.n, c.m, c.k, c.gated(), fast_weight(c.W, c.sfW, c.k), aligned_rows(c.X, c.ldx));
+    return plan_linear(c.n, c.m, c.k, c.gated(), layout_of(c.W, c.sfW, c.k, c.w_layout) != kNoLayout,
+                       aligned_rows(c.X, c.ldx));
 }
 
 int linear(const LinearCall &c, const LinearPlan &p, uint8_t *ws, hipStream_t stream) {
@@ -206,9 +213,10 @@ int linear(const LinearCall &c, const LinearPlan &p, uint8_t *ws, hipStream_t st
     a.part = p.part_bytes > 0 ? reinterpret_cast<float *>(ws) : nullptr;
     const int64_t piece = 16 / type_bytes(c.y_type);
     a.vec = aligned_rows16(c.Y, c.ldy, piece) && (!c.residual || aligned_rows16(c.residual, c.ldr, piece));
-    const bool packed = c.w_layout == NVFP4_W_PACKED;
-    const int s = c.x_type == NVFP4_OUT_BF16 ? launch_linear<true>(a, p, packed, c.gated(), stream)
-                                             : launch_linear<false>(a, p, packed, c.gated(), stream);
+    const int layout = layout_of(c.W, c.sfW, c.k, c.w_layout);
+    const int s = c.x_type == NVFP4_OUT_BF16
+                      ? c.gated() ? launch_linear<true, 2>(a, p, layout, stream) : launch_linear<true, 1>(a, p, layout, stream)
+                  : c.gated() ? launch_linear<false, 2>(a, p, layout, stream) : launch_linear<false, 1>(a, p, layout, stream);
     if (s != NVFP4_GEMV_OK || !a.part) return s;
     const dim3 grid(static_cast<uint32_t>(ceil_div(c.n * ceil_div(c.m, 4), kFinishThreads)));
     return c.gated() ? run(linear_finish<2>, grid, kFinishThreads, a, stream)
@@ -265,40 +273,54 @@ int check_moe(const MoeCall &c) {
     return NVFP4_GEMV_OK;
 }
 
-template <bool BF16, bool PACKED>
+template <bool BF16, int L>
 int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
-    return run(ffn_stream<BF16, PACKED, 2, 1, kMoeUp, kUpTiles, 2, kUpWaves, 8>,
+    return run(ffn_stream<BF16, L, 2, 1, kMoeUp, kUpTiles, 2, kUpWaves, 8>,
                dim3(static_cast<uint32_t>(ceil_div(a.m, kUpTiles * kTile) * groups)), kUpWaves * kWave, a, stream);
 }
 
-template <bool PACKED, int P>
+template <int L, int P>
 int stream_down(const FfnArgs &a, int64_t groups, hipStream_t stream) {
-    return run(ffn_stream<true, PACKED, 1, P, kMoeDown, kDownTiles, 2, kDownWaves, 4>,
+    return run(ffn_stream<true, L, 1, P, kMoeDown, kDownTiles, 2, kDownWaves, 4>,
                dim3(static_cast<uint32_t>(ceil_div(a.m, kDownTiles * kTile) * groups)), kDownWaves * kWave, a,
                stream);
 }
 
 template <bool BF16>
-int launch_up(const FfnArgs &a, bool packed, bool fast, int64_t groups, hipStream_t stream) {
-    if (fast) return packed ? stream_up<BF16, true>(a, groups, stream) : stream_up<BF16, false>(a, groups, stream);
+int launch_up(const FfnArgs &a, int layout, bool packed, int64_t groups, hipStream_t stream) {
+    switch (layout) {
+    case kRows: return stream_up<BF16, kRows>(a, groups, stream);
+    case kPackedTiles: return stream_up<BF16, kPackedTiles>(a, groups, stream);
+    case kRows16: return stream_up<BF16, kRows16>(a, groups, stream);
+    }
     const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * groups));
-    return launch_simple<BF16, 2, 1, kMoeUp>(a, packed, grid, stream);
+    return packed ? launch_simple<BF16, true, 2, 1, kMoeUp>(a, grid, stream)
+                  : launch_simple<BF16, false, 2, 1, kMoeUp>(a, grid, stream);
 }
 
-int launch_down(const FfnArgs &a, bool packed, bool fast, int planes, int64_t groups, hipStream_t stream) {
-    if (fast && planes == 2)
-        return packed ? stream_down<true, 2>(a, groups, stream) : stream_down<false, 2>(a, groups, stream);
-    if (fast) return packed ? stream_down<true, 3>(a, groups, stream) : stream_down<false, 3>(a, groups, stream);
+template <int P>
+int launch_down(const FfnArgs &a, int layout, bool packed, int64_t groups, hipStream_t stream) {
+    switch (layout) {
+    case kRows: return stream_down<kRows, P>(a, groups, stream);
+    case kPackedTiles: return stream_down<kPackedTiles, P>(a, groups, stream);
+    case kRows16: return stream_down<kRows16, P>(a, groups, stream);
+    }
     const dim3 grid(static_cast<uint32_t>(ceil_div(a.m, kTile) * groups));
-    return planes == 2 ? launch_simple<true, 1, 2, kMoeDown>(a, packed, grid, stream)
-                       : launch_simple<true, 1, 3, kMoeDown>(a, packed, grid, stream);
+    return packed ? launch_simple<true, true, 1, P, kMoeDown>(a, grid, stream)
+                  : launch_simple<true, false, 1, P, kMoeDown>(a, grid, stream);
 }
 
-template <bool PACKED>
+template <int L>
+int launch_slot_up(const SlotArgs &s, bool bf16, int64_t slots, hipStream_t stream) {
+    return run(bf16 ? ffn_slot_up<true, L> : ffn_slot_up<false, L>,
+               dim3(static_cast<uint32_t>(ceil_div(s.f.m, kUpTiles * kTile) * slots)), kUpWaves * kWave, s, stream);
+}
+
+template <int L>
 int launch_slot_down(const SlotArgs &s, const CombineArgs &y, int planes, hipStream_t stream) {
     void *args[] = {const_cast<SlotArgs *>(&s), const_cast<CombineArgs *>(&y)};
-    const void *fn = planes == 2 ? reinterpret_cast<const void *>(ffn_slot_down<PACKED, 2>)
-                                 : reinterpret_cast<const void *>(ffn_slot_down<PACKED, 3>);
+    const void *fn = planes == 2 ? reinterpret_cast<const void *>(ffn_slot_down<L, 2>)
+                                 : reinterpret_cast<const void *>(ffn_slot_down<L, 3>);
     const int64_t strips = ceil_div(ceil_div(s.f.m, kTile), kXcds) * kXcds;
     return run(fn, dim3(static_cast<uint32_t>(strips * y.tokens)), kSlotWaves * kWave, args, stream);
 }
@@ -307,7 +329,7 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     if (c.tokens == 0) return NVFP4_GEMV_OK;
     const nvfp4_moe_layer_t &l = *c.layer;
     const MoeWorkspace w = moe_workspace(l, c.tokens);
-    const bool packed = l.w_layout == NVFP4_W_PACKED, bf16 = l.x_type == NVFP4_OUT_BF16;
+    const bool bf16 = l.x_type == NVFP4_OUT_BF16, packed = l.w_layout == NVFP4_W_PACKED;
     const int64_t slots = c.tokens * l.topk;
 
     RouteArgs r = {};
@@ -340,15 +362,15 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     up.splits = 1;
     up.X = r.X;
     up.ldx = c.ldx;
-    bool fast_up = fast_weight(l.W13, l.sf13, l.hidden);
-    if (fast_up && !aligned_rows(c.X, c.ldx)) {
+    int up_layout = layout_of(l.W13, l.sf13, l.hidden, l.w_layout);
+    if (up_layout != kNoLayout && !aligned_rows(c.X, c.ldx)) {
         s = copy_aligned(c.X, c.ldx, ws + w.x, c.tokens, l.hidden, stream);
         if (s != NVFP4_GEMV_OK) return s;
         up.X = ws + w.x;
         up.ldx = l.hidden;
     }
-    fast_up = fast_up && c.tokens * up.ldx * 2 < kMaxStreamBytes;
-    const bool fast_down = fast_weight(l.W2, l.sf2, l.inter) && slots * l.inter * 2 < kMaxStreamBytes;
+    if (c.tokens * up.ldx * 2 >= kMaxStreamBytes) up_layout = kNoLayout;
+    const int down_layout = slots * l.inter * 2 < kMaxStreamBytes ? layout_of(l.W2, l.sf2, l.inter, l.w_layout) : kNoLayout;
     up.plane = slots * l.inter;
     up.W = l.W13;
     up.sW = l.sf13;
@@ -388,22 +410,24 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     y.topk = l.topk;
     y.y_type = c.y_type;
 
-    if (few_slots(l, c.tokens) && fast_up && fast_down) {
+    if (few_slots(l, c.tokens) && up_layout != kNoLayout && down_layout != kNoLayout) {
         const SlotArgs u = {up, r}, d = {down, r};
-        const dim3 grid(static_cast<uint32_t>(ceil_div(l.inter, kUpTiles * kTile) * slots));
-        s = bf16 ? packed ? run(ffn_slot_up<true, true>, grid, kUpWaves * kWave, u, stream)
-                          : run(ffn_slot_up<true, false>, grid, kUpWaves * kWave, u, stream)
-            : packed ? run(ffn_slot_up<false, true>, grid, kUpWaves * kWave, u, stream)
-                     : run(ffn_slot_up<false, false>, grid, kUpWaves * kWave, u, stream);
+        s = up_layout == kRows          ? launch_slot_up<kRows>(u, bf16, slots, stream)
+            : up_layout == kPackedTiles ? launch_slot_up<kPackedTiles>(u, bf16, slots, stream)
+                                        : launch_slot_up<kRows16>(u, bf16, slots, stream);
         if (s != NVFP4_GEMV_OK) return s;
-        return packed ? launch_slot_down<true>(d, y, planes, stream) : launch_slot_down<false>(d, y, planes, stream);
+        return down_layout == kRows          ? launch_slot_down<kRows>(d, y, planes, stream)
+               : down_layout == kPackedTiles ? launch_slot_down<kPackedTiles>(d, y, planes, stream)
+                                             : launch_slot_down<kRows16>(d, y, planes, stream);
     }
 
     s = run(route_select, dim3(1), kSelectWaves * kWave, r, stream);
     if (s == NVFP4_GEMV_OK)
-        s = bf16 ? launch_up<true>(up, packed, fast_up, r.groups, stream)
-                 : launch_up<false>(up, packed, fast_up, r.groups, stream);
-    if (s == NVFP4_GEMV_OK) s = launch_down(down, packed, fast_down, planes, r.groups, stream);
+        s = bf16 ? launch_up<true>(up, up_layout, packed, r.groups, stream)
+                 : launch_up<false>(up, up_layout, packed, r.groups, stream);
+    if (s == NVFP4_GEMV_OK)
+        s = planes == 2 ? launch_down<2>(down, down_layout, packed, r.groups, stream)
+                        : launch_down<3>(down, down_layout, packed, r.groups, stream);
     if (s != NVFP4_GEMV_OK) return s;
     return run(moe_combine,
                dim3(static_cast<uint32_t>(ceil_div(l.hidden, 4 * kCombineThreads)), static_cast<uint32_t>(c.tokens)),
@@ -436,7 +460,7 @@ extern "C" {
 
 size_t nvfp4_linear_workspace_size(int64_t n, int64_t m, int64_t k, int32_t activation) {
     if (check_linear_shape(n, m, k, NVFP4_W_ROW_MAJOR) != NVFP4_GEMV_OK) return 0;
-    return plan_linear(n, m, k, (activation & NVFP4_ACT_GATED) != 0, k % 64 == 0, false).ws_bytes();
+    return plan_linear(n, m, k, (activation & NVFP4_ACT_GATED) != 0, true, false).ws_bytes();
 }
 
 int nvfp4_linear_launch_ws(const void *X, int32_t x_type, int64_t ldx, const uint8_t *W,
