@@ -620,10 +620,13 @@ template <bool BF16, int L, int G, int P, int MODE, int R, int U, int W, int NXM
 __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
     __shared__ u32x4 lds[stream_lds<G, P, R, W, NXMAX>()];
     const uint32_t strips = static_cast<uint32_t>((a.m + R * kTile - 1) / (R * kTile));
-    const uint32_t q = blockIdx.x / strips;   // split, or place in the list of experts
+    const uint32_t q = blockIdx.x / strips;   // block of tokens and split, or place in the list of experts
     const int64_t row0 = int64_t(blockIdx.x - q * strips) * (R * kTile);
     if constexpr (MODE == kLinear) {
-        stream_pass<BF16, L, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q, 0, static_cast<int32_t>(a.n), lds);
+        const int32_t block = q / a.splits, p = block * 2 * NXMAX;
+        const int32_t left = static_cast<int32_t>(a.n) - p;
+        stream_pass<BF16, L, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q - block * a.splits, p,
+                                                         left < 2 * NXMAX ? p + left : p + 2 * NXMAX, lds);
     } else {
         const int expert = a.active[q];
         if (expert < 0) return;   // workgroup-uniform
@@ -746,14 +749,14 @@ struct TileShape {
 // the same piece of 16 tokens hit distinct banks.  Two buffers are two variables:
 // in one, every read would wait for the copies into the other half.
 //
-// 4096 tokens x (4096 x 7168), bf16, in 256 x 128 tiles: 227 us, 1.06 PFLOP/s
-// (fp16 211 us), where a library's bf16 product reaches 1.54.  Without the loads
-// and the decode, so with matrix instructions and LDS reads alone, the same loop
-// takes 180 us, without the LDS reads 167: the matrix cores do not sustain their
-// nominal rate on such operands, and what the kernel adds is 20 us for the
-// tokens' copies, 15 for the weights' loads and 12-25 for the decode.  Tiles of
-// 256 x 256, whose 128 sums per lane leave too few registers to decode ahead,
-// took 236-263 us.
+// 4096 tokens x (4096 x 7168) in 256 x 256 tiles: bf16 210 us, 1.15 PFLOP/s,
+// fp16 191 us, where a library's bf16 product reaches 1.54.  256 x 128 tiles,
+// which decode every weight for half as many tokens, take 230-260 and 205 us.  Of
+// those, without the loads and the decode, so with matrix instructions and LDS
+// reads alone, the same loop takes 180 us, without the LDS reads 167: the matrix
+// cores do not sustain their nominal rate on such operands; the tokens' copies
+// add 20 us, the weights' loads 15 and the decode 12 (fp16) or 25.  Waves of 64
+// rows by 128 tokens decode as little, but spill or leave one wave per SIMD.
 template <bool BF16, int L, int G, int Q, int NT, int WM, int WN, int WK>
 __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     using S = TileShape<G, Q, NT, WM, WN, WK>;
@@ -825,10 +828,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
                 2 * (win * kWinElems + 32 * h), 0, 0);
     };
     f32x4 acc[RT][NT] = {};
-    // Operands of this step of 32 elements and, where the registers allow it, of
-    // the next.
-    constexpr bool kAhead = RT * NT <= 16;
-    u32x4 wo[kAhead ? 2 : 1][RT];
+    u32x4 wo[2][RT];   // operands of this step of 32 elements and of the next
     auto decode = [&](u32x4 q, int c, int h, uint32_t s, u32x4 &o) {
         const uint32_t b = s >> (16 * h + 8 * (c / 2));
         if constexpr (BF16) {
@@ -840,9 +840,10 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
         __asm__ volatile("" : "+v"(o));
     };
     // One stage: 4 steps of 32 elements, each in groups of two token tiles.  A
-    // group reads the next group's tokens and, kAhead, decodes part of the next
-    // step's weights (of the next stage's first one at the end) between its
-    // products.
+    // group reads the next group's tokens and decodes part of the next step's
+    // weights (of the next stage's first one at the end) between its products.
+    // The empty asm statements hold each product to its group: the compiler would
+    // gather them, and the registers they need, across the whole stage.
     auto compute = [&](auto hc) {
         constexpr int h = decltype(hc)::value;
         constexpr int kPairs = NT / 2;
@@ -855,9 +856,6 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
         phase_fence();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            if (!kAhead)
-#pragma unroll
-                for (int r = 0; r < RT; ++r) decode(wq[h][r], c, h, ws[0][r], wo[0][r]);
 #pragma unroll
             for (int t = 0; t < kPairs; ++t) {
                 const int g = (c * kPairs + t) & 1;
@@ -866,24 +864,22 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
                     for (int i = 0; i < 2; ++i)
                         read(t + 1 < kPairs ? c : c + 1, t + 1 < kPairs ? 2 * (t + 1) + i : i, xv[g ^ 1][i]);
                 }
-                if (kAhead)
 #pragma unroll
-                    for (int r = RT * t / kPairs; r < RT * (t + 1) / kPairs; ++r) {
-                        if (c < 3) decode(wq[h][r], c + 1, h, ws[0][r], wo[(c + 1) & 1][r]);
-                        else decode(wq[1 - h][r], 0, 1 - h, ws[h][r], wo[0][r]);
-                    }
+                for (int r = RT * t / kPairs; r < RT * (t + 1) / kPairs; ++r) {
+                    if (c < 3) decode(wq[h][r], c + 1, h, ws[0][r], wo[(c + 1) & 1][r]);
+                    else decode(wq[1 - h][r], 0, 1 - h, ws[h][r], wo[0][r]);
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
-                        acc[r][2 * t + i] = mfma<BF16>(wo[kAhead ? c & 1 : 0][r], xv[g][i], acc[r][2 * t + i]);
-                if (kAhead) {
-                    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                        acc[r][2 * t + i] = mfma<BF16>(wo[c & 1][r], xv[g][i], acc[r][2 * t + i]);
+                // issue order: the reads, then VALU operations between the products
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
-                    for (int i = 0; i < 2 * RT; ++i) {
-                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x002, BF16 ? 4 : 2, 0);
-                    }
+                for (int i = 0; i < 2 * RT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, BF16 ? 4 : 2, 0);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -900,7 +896,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     load(h0, win0 + kg, 0);
     wait_vmcnt<0>();
 #pragma unroll
-    for (int r = 0; r < (kAhead ? RT : 0); ++r) decode(wq[0][r], 0, 0, ws[0][r], wo[0][r]);
+    for (int r = 0; r < RT; ++r) decode(wq[0][r], 0, 0, ws[0][r], wo[0][r]);
     lds_barrier();
     for (int win = win0 + kg; win < win1 + kg; win += WK) {
         load(h1, win, 0);
@@ -1323,7 +1319,6 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine(const CombineArgs
 // the five kernels take - us.
 
 constexpr int kUpTiles = 2, kUpWaves = 4;       // per workgroup: row tiles of gate and of up, waves
-constexpr int kDownTiles = 4, kDownWaves = 2;
 constexpr int kSlotWaves = 8;                   // of the slots' down product
 
 struct SlotArgs {

@@ -85,7 +85,7 @@ inline int check_moe_shape(const nvfp4_moe_layer_t &l, int64_t tokens) {
 }
 
 // ---------------------------------------------------------------- linear
-constexpr int64_t kStreamTokens = 16;   // most tokens the stream kernel takes
+constexpr int64_t kStreamTokens = 16;   // tokens of a workgroup of the stream kernel
 constexpr int64_t kComputeUnits = 256;  // CUs of an MI355X (8 XCDs x 32)
 constexpr int kStreamWaves = 8;
 
@@ -95,18 +95,38 @@ constexpr int stream_tiles(bool gated) { return gated ? 1 : 1; }
 // Shapes of the tile kernel, largest first.  A workgroup owns rows() rows of each
 // matrix and tokens() tokens; its wk groups of wm waves take the windows of K in
 // turn.  A wave holds q row tiles of each matrix times nt token tiles.
+// us[i]: what a weight of 28 windows (k = 7168) takes where every compute unit
+// has i + 1 workgroups, as measured with bf16 (0: they do not fit).
 struct TileKind {
     int q, nt, wm, wk;
+    float us[4];
     constexpr int rows() const { return kTile * q * wm; }
     constexpr int tokens() const { return kTile * nt; }
     constexpr int waves() const { return wm * wk; }
 };
-constexpr TileKind kTileKinds[] = {{2, 8, 8, 1}, {2, 8, 4, 2}, {2, 4, 4, 2}, {1, 4, 4, 2}, {1, 2, 4, 2}};
+constexpr TileKind kTileKinds[] = {
+    {2, 16, 8, 1, {210, 0, 0, 0}}, {2, 8, 8, 1, {111, 0, 0, 0}}, {2, 8, 4, 2, {70, 0, 0, 0}},
+    {2, 4, 4, 2, {41, 72, 0, 0}},  {1, 4, 4, 2, {32, 50, 0, 0}}, {1, 2, 4, 2, {20, 36, 50, 61}}};
 // two matrices: half the rows of each, so that a wave holds as many sums
-constexpr TileKind kGatedTileKinds[] = {{1, 8, 8, 1}, {1, 8, 4, 2}, {1, 4, 4, 2}, {1, 2, 4, 2}};
-constexpr int kNumTileKinds = 5, kNumGatedTileKinds = 4;
-constexpr int64_t kEnoughTiles = 192;   // three quarters of the compute units busy
-constexpr int64_t kTileSplitWins = 14;  // fewest windows of a workgroup for which a split of K pays
+constexpr TileKind kGatedTileKinds[] = {
+    {1, 16, 8, 1, {210, 0, 0, 0}}, {1, 8, 8, 1, {111, 0, 0, 0}}, {1, 8, 4, 2, {70, 0, 0, 0}},
+    {1, 4, 4, 2, {41, 72, 0, 0}},  {1, 2, 4, 2, {28, 45, 0, 0}}};
+constexpr int kNumTileKinds = 6, kNumGatedTileKinds = 5;
+// the stream kernel's, for 16 tokens and for one and two matrices
+constexpr float kStreamUs[2][4] = {{8, 10, 0, 0}, {11, 18, 0, 0}};
+constexpr float kFinishUs = 6;           // a second kernel that adds the sums of a split of K
+constexpr float kFinishBytesPerUs = 3e6;
+constexpr int64_t kMaxSplits = 8;
+
+// Time of `count` workgroups that go over `wins` windows each.
+inline float rounds_us(const float (&us)[4], int64_t count, int64_t wins) {
+    int most = 4;
+    while (us[most - 1] == 0) --most;
+    const int64_t per = ceil_div(count, kComputeUnits);   // on the busiest compute unit
+    const int64_t rest = per % most;
+    return (static_cast<float>(per / most) * us[most - 1] + (rest ? us[rest - 1] : 0.0f)) *
+           static_cast<float>(wins) / 28.0f;
+}
 
 struct LinearPlan {
     bool stream;        // stream kernel
@@ -119,38 +139,47 @@ struct LinearPlan {
     size_t ws_bytes() const { return ws_round(part_bytes) + ws_round(x_bytes); }
 };
 
-// `fast`: the weight's alignment and k allow the fast kernels; `x_aligned`: so
-// do X's rows.  Up to 16 tokens: the stream kernel, K split while the workgroups
-// leave compute units idle and every wave keeps a window of its own.  More: the
-// tile kernel in the largest shape that keeps three quarters of the compute
-// units busy (a larger tile reads and decodes less per product; 7168 x 4096
-// weights in us with tiles of 256 x 128, 128 x 128, 128 x 64, 64 x 64:
-// 256 tokens 96, 60, 37, 32; 512 tokens 96, 61, 41, 50; 1024 tokens 98, 70, 72,
-// 93; 4096 tokens 225, 264, -, -), else in the smallest with K split while
-// every workgroup keeps 14 windows (64 tokens, 28 windows: 20.7 us whole, 17.8
-// in two; 32 tokens, 7168 rows, 8 windows: 9.4 us whole, 12.4 in two, since the
-// sums go through memory and a second kernel).
+// `fast`: the weight's alignment allows the fast kernels; `x_aligned`: so do X's
+// rows.  Up to 16 tokens: the stream kernel, K split while the workgroups leave
+// compute units idle and every wave keeps a window of its own.  More: what the
+// times above say is fastest, of the stream kernel in blocks of 16 tokens, which
+// reads and decodes the weights once a block but has the most workgroups, and the
+// shapes of the tile kernel, which read and decode the less per product the
+// larger they are, with K whole or split.  Measured, in us, for 256 x 256,
+// 256 x 128, 128 x 128, 128 x 64, 64 x 64 tiles on 4096 x 7168: 256 tokens -, 96,
+// 60, 37, 32; 512 tokens -, 96, 61, 41, 50; 1024 tokens -, 98, 70, 72, 93; 4096
+// tokens 210, 240, 264, -, -.  K whole and split: 64 tokens 20.7 and 17.8 (in
+// two); 32 tokens, 7168 x 2048, 9.4 and 12.4.
 inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool fast, bool x_aligned) {
     LinearPlan p = {};
     p.splits = 1;
     p.tile = -1;
     if (!fast || n == 0) return p;
     const int64_t wins = ceil_div(k, kWinElems);
-    p.stream = n <= kStreamTokens;
-    if (p.stream) {
-        p.strips = ceil_div(m, kTile * stream_tiles(gated));
-        p.blocks = 1;
+    p.stream = true;
+    p.strips = ceil_div(m, kTile * stream_tiles(gated));
+    p.blocks = ceil_div(n, kStreamTokens);
+    if (n <= kStreamTokens) {
         while (p.strips * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
     } else {
+        float best = rounds_us(kStreamUs[gated], p.strips * p.blocks, wins);
         const int kinds = gated ? kNumGatedTileKinds : kNumTileKinds;
-        for (p.tile = 0;; ++p.tile) {
-            const TileKind &t = gated ? kGatedTileKinds[p.tile] : kTileKinds[p.tile];
-            p.strips = ceil_div(m, t.rows());
-            p.blocks = ceil_div(n, t.tokens());
-            if (p.tile == kinds - 1 || p.strips * p.blocks >= kEnoughTiles) break;
+        for (int i = 0; i < kinds; ++i) {
+            const TileKind &t = gated ? kGatedTileKinds[i] : kTileKinds[i];
+            const int64_t strips = ceil_div(m, t.rows()), blocks = ceil_div(n, t.tokens());
+            for (int64_t s = 1; s <= kMaxSplits && s <= wins; s *= 2) {
+                float us = rounds_us(t.us, strips * blocks * s, ceil_div(wins, s));
+                if (s > 1)
+                    us += kFinishUs + static_cast<float>(s * n * m) * (gated ? 16.0f : 8.0f) / kFinishBytesPerUs;
+                if (us >= best) continue;
+                best = us;
+                p.stream = false;
+                p.tile = i;
+                p.strips = strips;
+                p.blocks = blocks;
+                p.splits = s;
+            }
         }
-        while (p.strips * p.blocks * p.splits < kEnoughTiles && wins >= 2 * p.splits * kTileSplitWins)
-            p.splits *= 2;
     }
     if (p.splits > 1)
         p.part_bytes = static_cast<size_t>(p.splits) * n * m * (gated ? 2 : 1) * sizeof(float);
@@ -180,6 +209,12 @@ constexpr int64_t kMaxStreamBytes = 0x7FFFFFF0;   // row offsets the stream kern
 // Most experts that can have slots.
 inline int64_t moe_groups(const nvfp4_moe_layer_t &l, int64_t tokens) {
     return tokens * l.topk < l.experts ? tokens * l.topk : l.experts;
+}
+
+// Whether the workgroups of `tiles` row tiles each would leave compute units with
+// less than two: then every tile has its own.
+inline bool few_workgroups(int64_t rows, int tiles, int64_t groups) {
+    return ceil_div(rows, tiles * kTile) * groups < 2 * kComputeUnits;
 }
 
 // Whether slots are taken one by one rather than by expert.

@@ -120,7 +120,7 @@ template <bool BF16, int L, int G, int NX>
 int launch_linear_stream(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
     constexpr int R = stream_tiles(G == 2);
     return run(ffn_stream<BF16, L, G, 1, kLinear, R, 2, kStreamWaves, NX>,
-               dim3(static_cast<uint32_t>(p.strips * p.splits)), kStreamWaves * kWave, a, stream);
+               dim3(static_cast<uint32_t>(p.strips * p.blocks * p.splits)), kStreamWaves * kWave, a, stream);
 }
 
 template <bool BF16, int L, int G, int KIND>
@@ -142,8 +142,9 @@ int launch_linear(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
     case 1: return launch_tile<BF16, L, G, 1>(a, p, stream);
     case 2: return launch_tile<BF16, L, G, 2>(a, p, stream);
     case 3: return launch_tile<BF16, L, G, 3>(a, p, stream);
+    case 4: return launch_tile<BF16, L, G, 4>(a, p, stream);
     }
-    if constexpr (G == 1) return launch_tile<BF16, L, 1, 4>(a, p, stream);
+    if constexpr (G == 1) return launch_tile<BF16, L, 1, 5>(a, p, stream);
     return NVFP4_GEMV_ERR_LAUNCH;   // the plan has no such shape
 }
 
@@ -273,17 +274,31 @@ int check_moe(const MoeCall &c) {
     return NVFP4_GEMV_OK;
 }
 
+// The experts' products, in workgroups of R row tiles and W waves.  Many row
+// tiles per workgroup read and stage the tokens less often; where they would
+// leave compute units idle, a workgroup takes one.
+template <bool BF16, int L, int R, int W>
+int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
+    return run(ffn_stream<BF16, L, 2, 1, kMoeUp, R, 2, W, 8>,
+               dim3(static_cast<uint32_t>(ceil_div(a.m, R * kTile) * groups)), W * kWave, a, stream);
+}
 template <bool BF16, int L>
 int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
-    return run(ffn_stream<BF16, L, 2, 1, kMoeUp, kUpTiles, 2, kUpWaves, 8>,
-               dim3(static_cast<uint32_t>(ceil_div(a.m, kUpTiles * kTile) * groups)), kUpWaves * kWave, a, stream);
+    return few_workgroups(a.m, kUpTiles, groups) ? stream_up<BF16, L, 1, kUpWaves>(a, groups, stream)
+                                                 : stream_up<BF16, L, kUpTiles, kUpWaves>(a, groups, stream);
 }
 
+constexpr int kDownTiles = 4, kDownWaves = 2, kDownFewWaves = 4;
+
+template <int L, int P, int R, int W>
+int stream_down(const FfnArgs &a, int64_t groups, hipStream_t stream) {
+    return run(ffn_stream<true, L, 1, P, kMoeDown, R, 2, W, 4>,
+               dim3(static_cast<uint32_t>(ceil_div(a.m, R * kTile) * groups)), W * kWave, a, stream);
+}
 template <int L, int P>
 int stream_down(const FfnArgs &a, int64_t groups, hipStream_t stream) {
-    return run(ffn_stream<true, L, 1, P, kMoeDown, kDownTiles, 2, kDownWaves, 4>,
-               dim3(static_cast<uint32_t>(ceil_div(a.m, kDownTiles * kTile) * groups)), kDownWaves * kWave, a,
-               stream);
+    return few_workgroups(a.m, kDownTiles, groups) ? stream_down<L, P, 1, kDownFewWaves>(a, groups, stream)
+                                                   : stream_down<L, P, kDownTiles, kDownWaves>(a, groups, stream);
 }
 
 template <bool BF16>

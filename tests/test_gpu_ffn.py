@@ -88,15 +88,16 @@ def test_linear_sizes(n, m, k, layout):
         linear_case(rng, n, m, k, x=x, gated=gated, layout=layout)
 
 
-@pytest.mark.parametrize("n,m,k", [(2817, 2050, 320), (1409, 2050, 832), (769, 2050, 1088), (385, 2050, 576),
-                                   (97, 2050, 1024), (40, 520, 8192)])
+@pytest.mark.parametrize("n,m,k", [(5377, 2050, 320), (2817, 2050, 320), (1409, 2050, 832), (769, 2050, 1088), (385, 2050, 576),
+                                   (97, 2050, 1024), (40, 520, 8192), (17, 80, 16384), (48, 7000, 448)])
 def test_linear_every_tile_shape(n, m, k):
     """Weights that take each shape of the tile kernel, largest tiles first, then K split."""
     print(f"linear tiles {n} {m} {k}", flush=True)
     rng = np.random.default_rng(n)
-    linear_case(rng, n, m, k, x="bf16", bias=True, residual="in place", act="silu", layout="packed", ldy=2056)
-    linear_case(rng, n, m, k, x="f16", y="f32", act="gelu", bias=True, residual="in place", ldx=k + 8, ldy=2052)
-    linear_case(rng, n, (m + 1) // 2, k, x="f16", gated=True, bias=True, act="gelu_tanh", layout="packed", ldy=2059)
+    ld = max(m, 2048) // 8 * 8 + 8   # whole 16-byte pieces
+    linear_case(rng, n, m, k, x="bf16", bias=True, residual="in place", act="silu", layout="packed", ldy=ld)
+    linear_case(rng, n, m, k, x="f16", y="f32", act="gelu", bias=True, residual="in place", ldx=k + 8, ldy=ld + 4)
+    linear_case(rng, n, (m + 1) // 2, k, x="f16", gated=True, bias=True, act="gelu_tanh", layout="packed", ldy=ld + 3)
     linear_case(rng, n, (m + 1) // 2, k, x="bf16", y="f32", gated=True, residual="apart", act="relu", ldx=k + 1)
 
 
