@@ -363,6 +363,17 @@ enum Layout {
     kRows16 = 2,        // row-major, any k and scales, codes on 4 bytes
 };
 
+// The four scales of a lane's 64 elements, as loaded: put together only when they
+// are used, since before that the loads would have to be waited for.
+template <int L>
+struct ScaleWord {
+    uint32_t part[L == kRows16 ? 4 : 1];
+    __device__ __forceinline__ uint32_t value() const {
+        if constexpr (L == kRows16) return part[0] | part[1] << 8 | part[2] << 16 | part[3] << 24;
+        else return part[0];
+    }
+};
+
 constexpr int kWinCodeBytes = 2048, kWinScaleBytes = 256;   // of a packed window of a tile
 constexpr int kAnyRange = 0x7FFFFFF0;   // descriptor range where every used offset is known to be valid
 
@@ -426,19 +437,17 @@ struct WeightTiles {
         }
     }
     template <int POLICY>
-    __device__ __forceinline__ void load_scale(int r, uint32_t window, int left, uint32_t &s) const {
+    __device__ __forceinline__ void load_scale(int r, uint32_t window, int left, ScaleWord<L> &s) const {
         if constexpr (L == kRows16) {
-            s = 0;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-                s |= uint32_t(__builtin_amdgcn_raw_buffer_load_b8(sdesc, (scale[r] + b) | past(left, b), window * 16, 0))
-                     << (8 * b);
+                s.part[b] = __builtin_amdgcn_raw_buffer_load_b8(sdesc, (scale[r] + b) | past(left, b), window * 16, 0);
         } else {
-            s = __builtin_amdgcn_raw_buffer_load_b32(sdesc, scale[r] | past(left, 0),
-                                                     window * (L == kPackedTiles ? kWinScaleBytes : 16), POLICY);
+            s.part[0] = __builtin_amdgcn_raw_buffer_load_b32(sdesc, scale[r] | past(left, 0),
+                                                             window * (L == kPackedTiles ? kWinScaleBytes : 16), POLICY);
         }
     }
-    __device__ __forceinline__ void load(int r, uint32_t window, int left, u32x4 (&q)[2], uint32_t &s) const {
+    __device__ __forceinline__ void load(int r, uint32_t window, int left, u32x4 (&q)[2], ScaleWord<L> &s) const {
         load_half<kNonTemporal>(r, window, left, 0, q[0]);
         load_half<kNonTemporal>(r, window, left, 1, q[1]);
         load_scale<L == kPackedTiles ? kNonTemporal : 0>(r, window, left, s);
@@ -497,7 +506,7 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
     const int tok = li & (2 * NX - 1);   // columns past the staged tokens repeat them and are dropped
 
     u32x4 wq[U][G][R][2], xq[U][P][NX];
-    uint32_t ws[U][G][R];
+    ScaleWord<L> ws[U][G][R];
     auto issue = [&](int i, int u) {
         const uint32_t win = static_cast<uint32_t>(win0 + wave + waves * i);
         const bool run = i < niter;
@@ -541,7 +550,7 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     u32x4 wo[4];
-                    decode32<BF16, h>(wq[u][g][r][h], ws[u][g][r], wo);
+                    decode32<BF16, h>(wq[u][g][r][h], ws[u][g][r].value(), wo);
 #pragma unroll
                     for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -808,7 +817,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
                      64 * ((piece >> 2) ^ (j & 3)) + 8 * (piece & 3));
     }
     u32x4 wq[2][RT];
-    uint32_t ws[2][RT];
+    ScaleWord<L> ws[2][RT];
     auto load = [&](auto hc, int win, int slot) {
         constexpr int h = decltype(hc)::value;
         const int left = win < win1 ? static_cast<int>(k - win * kWinElems) : 0;   // elements from this window on
@@ -866,8 +875,8 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
                 }
 #pragma unroll
                 for (int r = RT * t / kPairs; r < RT * (t + 1) / kPairs; ++r) {
-                    if (c < 3) decode(wq[h][r], c + 1, h, ws[0][r], wo[(c + 1) & 1][r]);
-                    else decode(wq[1 - h][r], 0, 1 - h, ws[h][r], wo[0][r]);
+                    if (c < 3) decode(wq[h][r], c + 1, h, ws[0][r].value(), wo[(c + 1) & 1][r]);
+                    else decode(wq[1 - h][r], 0, 1 - h, ws[h][r].value(), wo[0][r]);
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -896,7 +905,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     load(h0, win0 + kg, 0);
     wait_vmcnt<0>();
 #pragma unroll
-    for (int r = 0; r < RT; ++r) decode(wq[0][r], 0, 0, ws[0][r], wo[0][r]);
+    for (int r = 0; r < RT; ++r) decode(wq[0][r], 0, 0, ws[0][r].value(), wo[0][r]);
     lds_barrier();
     for (int win = win0 + kg; win < win1 + kg; win += WK) {
         load(h1, win, 0);
@@ -1318,7 +1327,7 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine(const CombineArgs
 // partial outputs in memory.  7168 x 2048, 8 of 64 experts, one token: - us where
 // the five kernels take - us.
 
-constexpr int kUpTiles = 2, kUpWaves = 4;       // per workgroup: row tiles of gate and of up, waves
+constexpr int kSlotUpWaves = 4;
 constexpr int kSlotWaves = 8;                   // of the slots' down product
 
 struct SlotArgs {
@@ -1390,14 +1399,14 @@ __device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j,
 
 // h of one slot: workgroup = strip of rows and slot.
 template <bool BF16, int L>
-__global__ void __launch_bounds__(kUpWaves * kWave, 2) ffn_slot_up(const SlotArgs s) {
-    __shared__ u32x4 lds[stream_lds<2, 1, kUpTiles, kUpWaves, 1>()];
-    const uint32_t strips = static_cast<uint32_t>((s.f.m + kUpTiles * kTile - 1) / (kUpTiles * kTile));
+__global__ void __launch_bounds__(kSlotUpWaves * kWave, 2) ffn_slot_up(const SlotArgs s) {
+    __shared__ u32x4 lds[stream_lds<2, 1, kSlotUpTiles, kSlotUpWaves, 1>()];
+    const uint32_t strips = static_cast<uint32_t>((s.f.m + kSlotUpTiles * kTile - 1) / (kSlotUpTiles * kTile));
     const uint32_t slot = blockIdx.x / strips, strip = blockIdx.x - slot * strips;
     const uint32_t token = slot / s.r.topk;
     const int expert = __builtin_amdgcn_readfirstlane(
-        choose_slot<kUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
-    stream_pass<BF16, L, 2, 1, kSlotUp, kUpTiles, 2, kUpWaves, 1>(s.f, expert, int64_t(strip) * kUpTiles * kTile, 0,
+        choose_slot<kSlotUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
+    stream_pass<BF16, L, 2, 1, kSlotUp, kSlotUpTiles, 2, kSlotUpWaves, 1>(s.f, expert, int64_t(strip) * kSlotUpTiles * kTile, 0,
                                                                        slot, slot + 1, lds);
 }
 
@@ -1408,6 +1417,7 @@ template <int L, int P>
 __global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const SlotArgs s, const CombineArgs y) {
     __shared__ u32x4 lds[kSlotWaves * P * 2 * 32];
     __shared__ float sums[kMaxTopk > kSlotWaves ? kMaxTopk : kSlotWaves][kTile];
+    __shared__ float weights[kMaxTopk], alphas[kMaxTopk];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     // the workgroups of a strip lie on the same die, whose L2 serves experts that
@@ -1416,6 +1426,14 @@ __global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const Slo
     const int64_t strip = int64_t(b / tokens) * kXcds + blockIdx.x % kXcds, t = b % tokens;
     if (strip * kTile >= s.f.m) return;   // workgroup-uniform
     const int topk = y.topk, share = topk < kSlotWaves ? kSlotWaves / topk : 1;
+    if (static_cast<int>(threadIdx.x) < topk) {   // for the end, ahead of the weights
+        const int64_t slot = t * topk + threadIdx.x;
+        weights[threadIdx.x] = y.weights[slot];
+        alphas[threadIdx.x] = s.f.alpha ? s.f.alpha[s.r.choice[slot]] : 1.0f;
+    }
+    const bool last = threadIdx.x < kTile;
+    const int64_t r = strip * kTile + threadIdx.x;
+    const float residual = last && y.residual ? load_as_float(y.residual, t * y.ldr + r, y.y_type) : 0.0f;
     for (int j = wave / share; j < topk; j += kSlotWaves / share) {
         const int32_t slot = static_cast<int32_t>(t * topk + j);
         f32x4 acc[1][1];
@@ -1425,16 +1443,14 @@ __global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const Slo
             *reinterpret_cast<f32x4 *>(&sums[j * share + wave % share][4 * (lane / 16)]) = acc[0][0];
     }
     __syncthreads();
-    if (threadIdx.x >= kTile) return;
-    const int64_t r = strip * kTile + threadIdx.x;
+    if (!last) return;
     float out = 0.0f;
     for (int j = 0; j < topk; ++j) {
-        const int64_t slot = t * topk + j;
         float v = sums[j * share][threadIdx.x];
         for (int i = 1; i < share; ++i) v += sums[j * share + i][threadIdx.x];
-        out += y.weights[slot] * ((s.f.alpha ? s.f.alpha[s.r.choice[slot]] : 1.0f) * v);
+        out += weights[j] * (alphas[j] * v);
     }
-    if (y.residual) out += load_as_float(y.residual, t * y.ldr + r, y.y_type);
+    if (y.residual) out += residual;
     store_rounded(y.Y, t * y.ldy + r, y.y_type, out);
 }
 

@@ -114,6 +114,7 @@ constexpr TileKind kGatedTileKinds[] = {
 constexpr int kNumTileKinds = 6, kNumGatedTileKinds = 5;
 // the stream kernel's, for 16 tokens and for one and two matrices
 constexpr float kStreamUs[2][4] = {{8, 10, 0, 0}, {11, 18, 0, 0}};
+constexpr float kRoundUs = 3;            // until a workgroup has its first operands
 constexpr float kFinishUs = 6;           // a second kernel that adds the sums of a split of K
 constexpr float kFinishBytesPerUs = 3e6;
 constexpr int64_t kMaxSplits = 8;
@@ -124,8 +125,9 @@ inline float rounds_us(const float (&us)[4], int64_t count, int64_t wins) {
     while (us[most - 1] == 0) --most;
     const int64_t per = ceil_div(count, kComputeUnits);   // on the busiest compute unit
     const int64_t rest = per % most;
-    return (static_cast<float>(per / most) * us[most - 1] + (rest ? us[rest - 1] : 0.0f)) *
-           static_cast<float>(wins) / 28.0f;
+    return static_cast<float>(ceil_div(per, most)) * kRoundUs +
+           (static_cast<float>(per / most) * us[most - 1] + (rest ? us[rest - 1] : 0.0f)) *
+               static_cast<float>(wins) / 28.0f;
 }
 
 struct LinearPlan {
@@ -217,11 +219,27 @@ inline bool few_workgroups(int64_t rows, int tiles, int64_t groups) {
     return ceil_div(rows, tiles * kTile) * groups < 2 * kComputeUnits;
 }
 
-// Whether slots are taken one by one rather than by expert.
+// Whether slots are taken one by one rather than by expert.  An expert that
+// several slots share is then read for each, mostly from the caches, at 0.2 us
+// per MB (7168 x 2048, 8 of 64 experts: 2 tokens 42 MB, 3 tokens 92 MB, 4 tokens
+// 158 MB; 97, 141 and 177 us against 98, 124 and 150 by expert), and every
+// workgroup of the up product chooses its expert itself; what it saves is two
+// launches and the partial outputs, about 9 us.
+constexpr double kFewSlotsBytes = 40e6;
+constexpr int64_t kFewSlotsWorkgroups = 1024;
+constexpr int kSlotUpTiles = 2;   // row tiles of gate and of up of a workgroup
+
 inline bool few_slots(const nvfp4_moe_layer_t &l, int64_t tokens) {
     const int64_t slots = tokens * l.topk;
-    return (tokens == 1 || 4 * slots <= l.experts) && slots * ceil_div(l.inter, kTile) < kMaxTiles &&
-           tokens * (ceil_div(l.hidden, kTile) + 8) < kMaxTiles / 2;
+    if (slots * ceil_div(l.inter, kTile) >= kMaxTiles || tokens * (ceil_div(l.hidden, kTile) + 8) >= kMaxTiles / 2)
+        return false;
+    if (tokens == 1) return true;
+    double idle = 1.0;   // chance that an expert has no slot, for independent choices
+    for (int64_t i = 0; i < tokens && idle > 1e-6; ++i)
+        idle *= 1.0 - static_cast<double>(l.topk) / static_cast<double>(l.experts);
+    const double again = static_cast<double>(slots) - static_cast<double>(l.experts) * (1.0 - idle);
+    return slots * ceil_div(l.inter, kSlotUpTiles * kTile) <= kFewSlotsWorkgroups &&
+           again * static_cast<double>(l.hidden) * static_cast<double>(l.inter) * 27.0 / 16.0 <= kFewSlotsBytes;
 }
 
 // Parts of hidden that the logits are summed in: 512 elements each, while that

@@ -274,6 +274,8 @@ int check_moe(const MoeCall &c) {
     return NVFP4_GEMV_OK;
 }
 
+constexpr int kUpTiles = 2, kUpWaves = 4, kDownTiles = 4, kDownWaves = 2, kDownFewWaves = 4;
+
 // The experts' products, in workgroups of R row tiles and W waves.  Many row
 // tiles per workgroup read and stage the tokens less often; where they would
 // leave compute units idle, a workgroup takes one.
@@ -287,8 +289,6 @@ int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
     return few_workgroups(a.m, kUpTiles, groups) ? stream_up<BF16, L, 1, kUpWaves>(a, groups, stream)
                                                  : stream_up<BF16, L, kUpTiles, kUpWaves>(a, groups, stream);
 }
-
-constexpr int kDownTiles = 4, kDownWaves = 2, kDownFewWaves = 4;
 
 template <int L, int P, int R, int W>
 int stream_down(const FfnArgs &a, int64_t groups, hipStream_t stream) {
@@ -328,7 +328,7 @@ int launch_down(const FfnArgs &a, int layout, bool packed, int64_t groups, hipSt
 template <int L>
 int launch_slot_up(const SlotArgs &s, bool bf16, int64_t slots, hipStream_t stream) {
     return run(bf16 ? ffn_slot_up<true, L> : ffn_slot_up<false, L>,
-               dim3(static_cast<uint32_t>(ceil_div(s.f.m, kUpTiles * kTile) * slots)), kUpWaves * kWave, s, stream);
+               dim3(static_cast<uint32_t>(ceil_div(s.f.m, kSlotUpTiles * kTile) * slots)), kSlotUpWaves * kWave, s, stream);
 }
 
 template <int L>
