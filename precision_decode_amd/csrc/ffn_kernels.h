@@ -567,15 +567,20 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
         issue(u, u);
         phase_fence();
     }
-    for (int i = 0; i < niter; i += U) {
+    // the last windows apart, so that no loads are issued that are not used: even
+    // those out of range, which cause no traffic, take their time
+    int i = 0;
+    for (; i + U < niter; i += U) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u < niter) consume(u);   // wave-uniform
-            issue(i + u + U, u);             // past the wave's windows: zeros, no traffic
+            consume(u);
+            issue(i + u + U, u);   // past the wave's windows: zeros
             phase_fence();
         }
     }
-
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (i + u < niter) consume(u);   // wave-uniform
 }
 
 // One workgroup owns R tiles of 16 rows of each of G matrices and up to 2 NX
@@ -1181,11 +1186,18 @@ struct Scores {
         return scoring == NVFP4_SCORE_SOFTMAX ? exp(z - top) / sum : 1.0 / (1.0 + exp(-z));
     }
 };
+constexpr int kLogitLoads = 16;
 __device__ __forceinline__ double logit(const RouteArgs &a, int64_t t, int e) {
     const double *z = a.logits + t * a.experts + e;
-    double v = z[0];
-#pragma unroll 4
-    for (int s = 1; s < a.splits; ++s) v += z[s * a.tokens * a.experts];
+    const int64_t stride = a.tokens * a.experts;
+    double v = 0.0;
+    for (int s0 = 0; s0 < a.splits; s0 += kLogitLoads) {   // the loads of a round together
+        double part[kLogitLoads];
+#pragma unroll
+        for (int s = 0; s < kLogitLoads; ++s) part[s] = s0 + s < a.splits ? z[(s0 + s) * stride] : 0.0;
+#pragma unroll
+        for (int s = 0; s < kLogitLoads; ++s) v += part[s];
+    }
     return v;
 }
 // The key experts are chosen by; a NaN counts as the least.
@@ -1197,71 +1209,65 @@ __device__ __forceinline__ float routed_weight(const RouteArgs &a, double score,
     return static_cast<float>((a.renormalize ? score / chosen : score) * double(a.routed_scale));
 }
 
-constexpr int kSelectWaves = 16;
-constexpr int kSelectLds = 32768;   // bytes of scores and keys
-
-// Tokens that one workgroup of route_select chooses for at a time.
-inline __host__ __device__ int select_tokens(int64_t experts) {
-    const int64_t n = kSelectLds / 16 / experts;
-    return static_cast<int>(n < 1 ? 1 : n < kSelectWaves ? n : kSelectWaves);
+// Chooses the experts of one token by one wave: an expert's rank is the number
+// of experts ahead of it (a larger key, or an equal one at a lower index), so the
+// ranks are a permutation whatever the keys hold, and rank j < topk is slot
+// token * topk + j.  score, keys, order: the wave's own LDS.
+__device__ __forceinline__ void choose_token(const RouteArgs &a, int64_t t, double *score, double *keys,
+                                             int32_t *order) {
+    const int lane = threadIdx.x % kWave, experts = static_cast<int>(a.experts);
+    Scores sc = {-INFINITY, 0.0, a.scoring};
+    for (int e = lane; e < experts; e += kWave) {
+        score[e] = logit(a, t, e);
+        sc.top = fmax(sc.top, score[e]);
+    }
+    if (a.scoring == NVFP4_SCORE_SOFTMAX) {
+        sc.top = wave_max64(sc.top);
+        for (int e = lane; e < experts; e += kWave) sc.sum += exp(score[e] - sc.top);
+        sc.sum = wave_sum64(sc.sum);
+    }
+    for (int e = lane; e < experts; e += kWave) {
+        score[e] = sc.score(score[e]);
+        keys[e] = choice_key(a, e, score[e]);
+    }
+    wave_lds_fence();
+    double chosen = 0.0;
+    for (int e = lane; e < experts; e += kWave) {
+        const double key = keys[e];
+        int rank = 0;
+#pragma unroll 8
+        for (int o = 0; o < experts; ++o) {
+            const double other = keys[o];
+            rank += other > key || (other == key && o < e);
+        }
+        if (rank < a.topk) {
+            chosen += score[e];
+            order[rank] = e;
+            a.choice[t * a.topk + rank] = e;
+        }
+    }
+    chosen = wave_sum64(chosen);
+    wave_lds_fence();
+    for (int j = lane; j < a.topk; j += kWave)
+        a.weights[t * a.topk + j] = routed_weight(a, score[order[j]], chosen);
+    wave_lds_fence();
 }
 
-// One workgroup chooses the experts of every token, a wave per token at a
-// time: an expert's rank is the number of experts ahead of it (a larger key,
-// or an equal one at a lower index), so the ranks are a permutation whatever
-// the keys hold, and rank j < topk is slot token * topk + j.  Then the slots
-// are sorted by expert; the order inside an expert comes from an atomic and
-// may differ between runs, but nothing depends on it: every slot is a column
-// of its own in the products.
-__global__ void __launch_bounds__(kSelectWaves * kWave) route_select(const RouteArgs a) {
-    __shared__ double lds[kSelectLds / 8];
-    __shared__ int32_t count[kMaxExperts], cursor[kMaxExperts], order[kSelectWaves][kMaxTopk];
+// The slots sorted by expert, from the choice, by one workgroup: the offsets of
+// the experts, the list of slots and the list of experts that have any.  The order
+// inside an expert comes from an atomic and may differ between runs, but nothing
+// depends on it: every slot is a column of its own in the products.
+__device__ __forceinline__ void sort_slots(const RouteArgs &a) {
+    __shared__ int32_t count[kMaxExperts], cursor[kMaxExperts];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int experts = static_cast<int>(a.experts), each = select_tokens(a.experts);
-    double *score = lds + wave * 2 * experts, *keys = score + experts;
+    const int experts = static_cast<int>(a.experts);
+    const int64_t slots = a.tokens * a.topk;
     for (int e = threadIdx.x; e < experts; e += blockDim.x) count[e] = 0;
+    __syncthreads();   // and the choice, where this workgroup made it
+    for (int64_t s = threadIdx.x; s < slots; s += blockDim.x) atomicAdd(&count[a.choice[s]], 1);
     __syncthreads();
-    for (int64_t t = wave; t < a.tokens && wave < each; t += each) {
-        Scores sc = {-INFINITY, 0.0, a.scoring};
-        for (int e = lane; e < experts; e += kWave) {
-            score[e] = logit(a, t, e);
-            sc.top = fmax(sc.top, score[e]);
-        }
-        if (a.scoring == NVFP4_SCORE_SOFTMAX) {
-            sc.top = wave_max64(sc.top);
-            for (int e = lane; e < experts; e += kWave) sc.sum += exp(score[e] - sc.top);
-            sc.sum = wave_sum64(sc.sum);
-        }
-        for (int e = lane; e < experts; e += kWave) {
-            score[e] = sc.score(score[e]);
-            keys[e] = choice_key(a, e, score[e]);
-        }
-        wave_lds_fence();
-        double chosen = 0.0;
-        for (int e = lane; e < experts; e += kWave) {
-            const double key = keys[e];
-            int rank = 0;
-#pragma unroll 8
-            for (int o = 0; o < experts; ++o) {
-                const double other = keys[o];
-                rank += other > key || (other == key && o < e);
-            }
-            if (rank < a.topk) {
-                chosen += score[e];
-                order[wave][rank] = e;
-                a.choice[t * a.topk + rank] = e;
-                atomicAdd(&count[e], 1);
-            }
-        }
-        chosen = wave_sum64(chosen);
-        wave_lds_fence();
-        for (int j = lane; j < a.topk; j += kWave)
-            a.weights[t * a.topk + j] = routed_weight(a, score[order[wave][j]], chosen);
-        wave_lds_fence();
-    }
-    __syncthreads();
-    // offsets and the list of experts with slots: lane l of wave 0 sums its run of
-    // experts, the runs are scanned (slots in the low half, experts in the high)
+    // lane l of wave 0 sums its run of experts, the runs are scanned (slots in the
+    // low half, experts in the high)
     if (wave == 0) {
         const int per = (experts + kWave - 1) / kWave;
         const int e0 = lane * per;
@@ -1286,10 +1292,36 @@ __global__ void __launch_bounds__(kSelectWaves * kWave) route_select(const Route
         for (int i = total + lane; i < a.groups; i += kWave) a.active[i] = -1;
     }
     __syncthreads();
-    const int64_t slots = a.tokens * a.topk;
     for (int64_t s = threadIdx.x; s < slots; s += blockDim.x)
         a.list[atomicAdd(&cursor[a.choice[s]], 1)] = static_cast<int32_t>(s);
 }
+
+// Few tokens: choice and sorting by one workgroup, a wave per token at a time.
+// More: each its own kernel, a workgroup per kChooseWaves tokens (64 experts x 64
+// tokens: - us, by one workgroup 28).
+constexpr int kSelectWaves = 16, kChooseWaves = 4;
+constexpr int kSelectLds = 32768;   // bytes of scores and keys
+
+__global__ void __launch_bounds__(kSelectWaves * kWave) route_select(const RouteArgs a) {
+    __shared__ double lds[kSelectLds / 8];
+    __shared__ int32_t order[kSelectWaves][kMaxTopk];
+    const int wave = threadIdx.x / kWave, experts = static_cast<int>(a.experts);
+    const int fit = kSelectLds / 16 / experts, each = fit < kSelectWaves ? fit : kSelectWaves;   // at least 2
+    double *score = lds + wave * 2 * experts;
+    for (int64_t t = wave; t < a.tokens && wave < each; t += each)
+        choose_token(a, t, score, score + experts, order[wave]);
+    sort_slots(a);
+}
+
+__global__ void __launch_bounds__(kChooseWaves * kWave) route_choose(const RouteArgs a) {
+    __shared__ double lds[kChooseWaves][2 * kMaxExperts];
+    __shared__ int32_t order[kChooseWaves][kMaxTopk];
+    const int wave = threadIdx.x / kWave;
+    const int64_t t = int64_t(blockIdx.x) * kChooseWaves + wave;
+    if (t < a.tokens) choose_token(a, t, lds[wave], lds[wave] + a.experts, order[wave]);
+}
+
+__global__ void __launch_bounds__(kSelectWaves * kWave) route_sort(const RouteArgs a) { sort_slots(a); }
 
 // ---------------------------------------------------------------- combination
 struct CombineArgs {

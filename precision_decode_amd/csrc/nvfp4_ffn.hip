@@ -11,8 +11,8 @@
 // tokens are the B operand, so a lane ends with four consecutive rows of one
 // token, which the epilogue finishes and stores together.
 //
-// The MoE layer runs as route_logits, route_select, the gate/up product, the
-// down product and moe_combine.  Each slot (a token and one of its experts)
+// The MoE layer runs as route_logits, the choice of experts, the gate/up product,
+// the down product and moe_combine.  Each slot (a token and one of its experts)
 // is a column of the expert's products; h = f(gate) up goes through the
 // workspace as bf16 planes (the value, the rest of its rounding, ...) that
 // the down product multiplies one after another into the same sums.
@@ -436,7 +436,12 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
                                              : launch_slot_down<kRows16>(d, y, planes, stream);
     }
 
-    s = run(route_select, dim3(1), kSelectWaves * kWave, r, stream);
+    if (c.tokens <= kSelectWaves) {
+        s = run(route_select, dim3(1), kSelectWaves * kWave, r, stream);
+    } else {
+        s = run(route_choose, dim3(static_cast<uint32_t>(ceil_div(c.tokens, kChooseWaves))), kChooseWaves * kWave, r, stream);
+        if (s == NVFP4_GEMV_OK) s = run(route_sort, dim3(1), kSelectWaves * kWave, r, stream);
+    }
     if (s == NVFP4_GEMV_OK)
         s = bf16 ? launch_up<true>(up, up_layout, packed, r.groups, stream)
                  : launch_up<false>(up, up_layout, packed, r.groups, stream);
