@@ -1438,7 +1438,7 @@ __global__ void __launch_bounds__(kSlotUpWaves * kWave, 2) ffn_slot_up(const Slo
     const uint32_t token = slot / s.r.topk;
     const int expert = __builtin_amdgcn_readfirstlane(
         choose_slot<kSlotUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
-    stream_pass<BF16, L, 2, 1, kSlotUp, kSlotUpTiles, 2, kSlotUpWaves, 1>(s.f, expert, int64_t(strip) * kSlotUpTiles * kTile, 0,
+    stream_pass<BF16, L, 2, 1, kSlotUp, kSlotUpTiles, 3, kSlotUpWaves, 1>(s.f, expert, int64_t(strip) * kSlotUpTiles * kTile, 0,
                                                                        slot, slot + 1, lds);
 }
 
@@ -1469,7 +1469,7 @@ __global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const Slo
     for (int j = wave / share; j < topk; j += kSlotWaves / share) {
         const int32_t slot = static_cast<int32_t>(t * topk + j);
         f32x4 acc[1][1];
-        stream_sums<true, L, 1, P, kSlotDown, 1, 4, 1>(s.f, s.r.choice[slot], strip * kTile, 0, slot, slot + 1,
+        stream_sums<true, L, 1, P, kSlotDown, 1, 2, 1>(s.f, s.r.choice[slot], strip * kTile, 0, slot, slot + 1,
                                                             lds + wave * (P * 2 * 32), wave % share, share, acc);
         if (lane % 16 == 0)
             *reinterpret_cast<f32x4 *>(&sums[j * share + wave % share][4 * (lane / 16)]) = acc[0][0];

@@ -86,6 +86,7 @@ inline int check_moe_shape(const nvfp4_moe_layer_t &l, int64_t tokens) {
 
 // ---------------------------------------------------------------- linear
 constexpr int64_t kStreamTokens = 16;   // tokens of a workgroup of the stream kernel
+constexpr int64_t kStreamOnlyTokens = 8;
 constexpr int64_t kComputeUnits = 256;  // CUs of an MI355X (8 XCDs x 32)
 constexpr int kStreamWaves = 8;
 
@@ -113,7 +114,7 @@ constexpr TileKind kGatedTileKinds[] = {
     {1, 4, 4, 2, {41, 72, 0, 0}},  {1, 2, 4, 2, {28, 45, 0, 0}}};
 constexpr int kNumTileKinds = 6, kNumGatedTileKinds = 5;
 // the stream kernel's, for 16 tokens and for one and two matrices
-constexpr float kStreamUs[2][4] = {{8, 10, 0, 0}, {11, 18, 0, 0}};
+constexpr float kStreamUs[2][4] = {{9, 11.5f, 0, 0}, {11, 18, 0, 0}};
 constexpr float kRoundUs = 3;            // until a workgroup has its first operands
 constexpr float kFinishUs = 6;           // a second kernel that adds the sums of a split of K
 constexpr float kFinishBytesPerUs = 3e6;
@@ -142,7 +143,7 @@ struct LinearPlan {
 };
 
 // `fast`: the weight's alignment allows the fast kernels; `x_aligned`: so do X's
-// rows.  Up to 16 tokens: the stream kernel, K split while the workgroups leave
+// rows.  Up to 8 tokens: the stream kernel, K split while the workgroups leave
 // compute units idle and every wave keeps a window of its own.  More: what the
 // times above say is fastest, of the stream kernel in blocks of 16 tokens, which
 // reads and decodes the weights once a block but has the most workgroups, and the
@@ -150,7 +151,7 @@ struct LinearPlan {
 // larger they are, with K whole or split.  Measured, in us, for 256 x 256,
 // 256 x 128, 128 x 128, 128 x 64, 64 x 64 tiles on 4096 x 7168: 256 tokens -, 96,
 // 60, 37, 32; 512 tokens -, 96, 61, 41, 50; 1024 tokens -, 98, 70, 72, 93; 4096
-// tokens 210, 240, 264, -, -.  K whole and split: 64 tokens 20.7 and 17.8 (in
+// tokens 204, 240, 264, -, -.  K whole and split: 64 tokens 20.7 and 17.8 (in
 // two); 32 tokens, 7168 x 2048, 9.4 and 12.4.
 inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool fast, bool x_aligned) {
     LinearPlan p = {};
@@ -158,21 +159,22 @@ inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool 
     p.tile = -1;
     if (!fast || n == 0) return p;
     const int64_t wins = ceil_div(k, kWinElems);
+    const auto finish_us = [&](int64_t s) {
+        return s == 1 ? 0.0f : kFinishUs + static_cast<float>(s * n * m) * (gated ? 16.0f : 8.0f) / kFinishBytesPerUs;
+    };
     p.stream = true;
     p.strips = ceil_div(m, kTile * stream_tiles(gated));
     p.blocks = ceil_div(n, kStreamTokens);
-    if (n <= kStreamTokens) {
-        while (p.strips * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
-    } else {
-        float best = rounds_us(kStreamUs[gated], p.strips * p.blocks, wins);
+    while (p.strips * p.blocks * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
+    if (n > kStreamOnlyTokens) {
+        float best = rounds_us(kStreamUs[gated], p.strips * p.blocks * p.splits, ceil_div(wins, p.splits)) +
+                     finish_us(p.splits);
         const int kinds = gated ? kNumGatedTileKinds : kNumTileKinds;
         for (int i = 0; i < kinds; ++i) {
             const TileKind &t = gated ? kGatedTileKinds[i] : kTileKinds[i];
             const int64_t strips = ceil_div(m, t.rows()), blocks = ceil_div(n, t.tokens());
             for (int64_t s = 1; s <= kMaxSplits && s <= wins; s *= 2) {
-                float us = rounds_us(t.us, strips * blocks * s, ceil_div(wins, s));
-                if (s > 1)
-                    us += kFinishUs + static_cast<float>(s * n * m) * (gated ? 16.0f : 8.0f) / kFinishBytesPerUs;
+                const float us = rounds_us(t.us, strips * blocks * s, ceil_div(wins, s)) + finish_us(s);
                 if (us >= best) continue;
                 best = us;
                 p.stream = false;
@@ -226,8 +228,8 @@ inline bool few_workgroups(int64_t rows, int tiles, int64_t groups) {
 // workgroup of the up product chooses its expert itself; what it saves is two
 // launches and the partial outputs, about 9 us.
 constexpr double kFewSlotsBytes = 40e6;
-constexpr int64_t kFewSlotsWorkgroups = 1024;
-constexpr int kSlotUpTiles = 2;   // row tiles of gate and of up of a workgroup
+constexpr int64_t kFewSlotsWorkgroups = 2048;
+constexpr int kSlotUpTiles = 1;   // row tiles of gate and of up of a workgroup
 
 inline bool few_slots(const nvfp4_moe_layer_t &l, int64_t tokens) {
     const int64_t slots = tokens * l.topk;
