@@ -61,9 +61,9 @@
  * ceil(hidden/16) or ceil(inter/16) < 2^24.
  * Alignment: X, Wr, residual and Y to their element, float arrays to 4 bytes,
  * the workspace to 256; packed codes to 16 bytes and packed scales to 4.
- * Row-major codes aligned to 16 bytes and scales to 4 with k % 64 == 0 take the
- * fast kernels, others a slower one.  An X whose rows are not 16-byte aligned
- * is first copied into the workspace.
+ * Row-major codes that are not aligned to 4 bytes take a slower kernel.  More
+ * than a few tokens of an X whose rows are not 16-byte aligned are first copied
+ * into the workspace by the linear layer.
  */
 #ifndef NVFP4_FFN_H
 #define NVFP4_FFN_H

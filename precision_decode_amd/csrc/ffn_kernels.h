@@ -473,7 +473,8 @@ __device__ __forceinline__ void wave_lds_fence() {
 // 16-byte operand pieces: read straight from memory in operand order, each
 // instruction would touch a different line in every lane.  The 16-byte pieces
 // are swizzled by the token, so the 16 lanes that read the same piece of 16
-// tokens hit distinct banks.  NX = instructions = half the tokens staged.
+// tokens hit distinct banks.  NX = instructions = half the tokens staged.  The
+// tokens' rows need no alignment beyond their elements'.
 template <bool BF16, int L, int G, int P, int MODE, int R, int U, int NX>
 __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
                                             int32_t end, u32x4 *slot, int wave, int waves, f32x4 (&acc)[G][R]) {

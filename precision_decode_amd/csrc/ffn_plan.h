@@ -187,7 +187,7 @@ inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool 
     }
     if (p.splits > 1)
         p.part_bytes = static_cast<size_t>(p.splits) * n * m * (gated ? 2 : 1) * sizeof(float);
-    if (!x_aligned) p.x_bytes = static_cast<size_t>(n) * k * 2;
+    if (!x_aligned && !p.stream) p.x_bytes = static_cast<size_t>(n) * k * 2;
     return p;
 }
 
@@ -203,7 +203,6 @@ struct MoeWorkspace {
     size_t weights;   // float [slots]
     size_t h;         // bf16 [planes][slots][inter]
     size_t part;      // float [slots][hidden]
-    size_t x;         // 16-bit [tokens][hidden]: aligned copy of X
     size_t total;
 };
 
@@ -269,7 +268,6 @@ inline MoeWorkspace moe_workspace(const nvfp4_moe_layer_t &l, int64_t tokens) {
     w.weights = take(slots * 4);
     w.h = take(kMaxPlanes * slots * l.inter * 2);
     w.part = take(slots * l.hidden * 4);
-    w.x = take(static_cast<size_t>(tokens) * l.hidden * 2);
     w.total = at;
     return w;
 }

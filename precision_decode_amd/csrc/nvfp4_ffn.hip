@@ -378,12 +378,6 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     up.X = r.X;
     up.ldx = c.ldx;
     int up_layout = layout_of(l.W13, l.sf13, l.hidden, l.w_layout);
-    if (up_layout != kNoLayout && !aligned_rows(c.X, c.ldx)) {
-        s = copy_aligned(c.X, c.ldx, ws + w.x, c.tokens, l.hidden, stream);
-        if (s != NVFP4_GEMV_OK) return s;
-        up.X = ws + w.x;
-        up.ldx = l.hidden;
-    }
     if (c.tokens * up.ldx * 2 >= kMaxStreamBytes) up_layout = kNoLayout;
     const int down_layout = slots * l.inter * 2 < kMaxStreamBytes ? layout_of(l.W2, l.sf2, l.inter, l.w_layout) : kNoLayout;
     up.plane = slots * l.inter;
