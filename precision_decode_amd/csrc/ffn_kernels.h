@@ -584,9 +584,130 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
         if (i + u < niter) consume(u);   // wave-uniform
 }
 
+// The same sums for one token, in VALU dot products.  On the matrix cores 15 of 16
+// columns would be dropped, and a weight costs the VALU, which bounds the stream,
+// more there: bf16 elements take 32 operations per 16 to be decoded with their
+// scale; here 8 conversions, 8 dot products of two elements and one multiply-add
+// with the block's scale (7168 x 16384, bf16: 16.0 -> 14.4 us).  Lane i + 16 q ends
+// with the sum of row i of every tile, the same for all q.  The token's elements
+// of a window go through the wave's LDS slot, every lane quarter's 128 bytes 16
+// bytes further, so that the quarters' reads hit distinct banks.
+constexpr int kDotSlot = 4 * (8 + 1);   // 16-byte pieces of a plane
+
+template <bool BF16>
+__device__ __forceinline__ float dot8(uint32_t q, u32x4 x, float s) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    if constexpr (BF16) {
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 0),
+                                            __builtin_bit_cast(bf16x2, uint32_t(x.x)), s, false);
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 1),
+                                            __builtin_bit_cast(bf16x2, uint32_t(x.y)), s, false);
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 2),
+                                            __builtin_bit_cast(bf16x2, uint32_t(x.z)), s, false);
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 3),
+                                               __builtin_bit_cast(bf16x2, uint32_t(x.w)), s, false);
+    } else {
+        s = __builtin_amdgcn_fdot2(e2m1x2_f16<0>(q), halves(x.x), s, false);
+        s = __builtin_amdgcn_fdot2(e2m1x2_f16<1>(q), halves(x.y), s, false);
+        s = __builtin_amdgcn_fdot2(e2m1x2_f16<2>(q), halves(x.z), s, false);
+        return __builtin_amdgcn_fdot2(e2m1x2_f16<3>(q), halves(x.w), s, false);
+    }
+}
+
+template <bool BF16, int L, int G, int P, int MODE, int R, int U>
+__device__ __forceinline__ void dot_sums(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
+                                         u32x4 *slot, int wave, int waves, float (&acc)[G][R]) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int li = lane & 15, kq = lane >> 4;
+    const uint32_t k = static_cast<uint32_t>(a.k);
+    const int wins = static_cast<int>((k + kWinElems - 1) / kWinElems);
+    const int win0 = static_cast<int>(int64_t(split) * wins / a.splits);
+    const int nwin = static_cast<int>(int64_t(split + 1) * wins / a.splits) - win0;
+    const int niter = nwin > wave ? (nwin - wave + waves - 1) / waves : 0;
+
+    const WeightTiles<L, R> w0(a, G * int64_t(expert), row0, li, kq);
+    const WeightTiles<L, R> w1(a, G * int64_t(expert) + (G - 1), row0, li, kq);
+    const int64_t row = MODE == kLinear ? p0 : x_row<MODE>(a, out_row<MODE>(a, p0));
+    __amdgpu_buffer_rsrc_t xdesc[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) xdesc[p] = buffer_of(a.X + 2 * (row * a.ldx + p * a.plane), kAnyRange);
+
+    u32x4 wq[U][G][R][2], xq[U][P];
+    ScaleWord<L> ws[U][G][R];
+    auto issue = [&](int i, int u) {
+        const uint32_t win = static_cast<uint32_t>(win0 + wave + waves * i);
+        const int left = i < niter ? static_cast<int>(k - win * kWinElems) : 0;
+        const uint32_t xo = lane < 32 && 8 * lane < left ? 16 * lane : kOutOfRange;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            xq[u][p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xdesc[p], xo, win * 512, 0));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            w0.load(r, win, left, wq[u][0][r], ws[u][0][r]);
+            if constexpr (G == 2) w1.load(r, win, left, wq[u][1][r], ws[u][1][r]);
+        }
+    };
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[g][r] = 0.0f;
+    auto consume = [&](int u) {
+        wave_lds_fence();
+        if (lane < 32)
+#pragma unroll
+            for (int p = 0; p < P; ++p) slot[p * kDotSlot + lane + (lane >> 3)] = xq[u][p];
+        wave_lds_fence();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {   // blocks of 16 elements
+            u32x4 xv[P][2];
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) xv[p][c] = slot[p * kDotSlot + 9 * kq + 2 * b + c];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int p = 0; p < P; ++p) s = dot8<BF16>(wq[u][g][r][b / 2][2 * (b & 1) + c], xv[p][c], s);
+                    acc[g][r] = __builtin_fmaf(e4m3x2_f32(ws[u][g][r].value() >> (8 * b)).x, s, acc[g][r]);
+                }
+        }
+    };
+
+    phase_fence();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        issue(u, u);
+        phase_fence();
+    }
+    int i = 0;
+    for (; i + U < niter; i += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            consume(u);
+            issue(i + u + U, u);
+            phase_fence();
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (i + u < niter) consume(u);   // wave-uniform
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {   // the four quarters of a row
+            acc[g][r] += __shfl_xor(acc[g][r], 16);
+            acc[g][r] += __shfl_xor(acc[g][r], 32);
+        }
+}
+
 // One workgroup owns R tiles of 16 rows of each of G matrices and up to 2 NX
-// tokens; its W waves take the windows of its part of K in turn, and their sums
-// are added in wave order through LDS.
+// tokens (NX = 0: one, in dot products); its W waves take the windows of its part
+// of K in turn, and their sums are added in wave order through LDS.
 template <bool BF16, int L, int G, int P, int MODE, int R, int U, int W, int NX>
 __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
                                             int32_t end, u32x4 *lds) {
@@ -594,41 +715,58 @@ __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int li = lane & 15, kq = lane >> 4;
     f32x4 acc[G][R];
-    stream_sums<BF16, L, G, P, MODE, R, U, NX>(a, expert, row0, split, p0, end,
-                                                    lds + wave * (P * 2 * NX * 32), wave, W, acc);
-
-    // wave r % W finishes row tile r
-    f32x4 *red = reinterpret_cast<f32x4 *>(lds);
-    if (W > 1) {
+    // the sums of wave w, matrix g and tile r, four rows of a token, for this lane
+    const f32x4 *red = reinterpret_cast<const f32x4 *>(lds);
+    auto at = [&](int w, int g, int r) {
+        return NX == 0 ? ((w * G + g) * R + r) * 4 + kq : ((w * G + g) * R + r) * kWave + lane;
+    };
+    if constexpr (NX == 0) {
+        float sum[G][R];
+        dot_sums<BF16, L, G, P, MODE, R, U>(a, expert, row0, split, p0, lds + wave * (P * kDotSlot), wave, W, sum);
         __syncthreads();
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int r = 0; r < R; ++r) red[((wave * G + g) * R + r) * kWave + lane] = acc[g][r];
+            for (int r = 0; r < R; ++r)
+                if (lane < kTile) reinterpret_cast<float *>(lds)[((wave * G + g) * R + r) * kTile + lane] = sum[g][r];
         __syncthreads();
+    } else {
+        stream_sums<BF16, L, G, P, MODE, R, U, NX>(a, expert, row0, split, p0, end, lds + wave * (P * 2 * NX * 32), wave,
+                                                   W, acc);
+        if (W > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int r = 0; r < R; ++r) reinterpret_cast<f32x4 *>(lds)[at(wave, g, r)] = acc[g][r];
+            __syncthreads();
+        }
     }
+    // wave r % W finishes row tile r
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (W > 1 && r % W != wave) continue;
         f32x4 sum[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            sum[g] = acc[g][r];
-            if (W > 1) {
-                sum[g] = red[(g * R + r) * kWave + lane];
-                for (int w = 1; w < W; ++w) sum[g] += red[((w * G + g) * R + r) * kWave + lane];
+            if (NX > 0 && W == 1) {
+                sum[g] = acc[g][r];
+                continue;
             }
+            sum[g] = red[at(0, g, r)];
+            for (int w = 1; w < W; ++w) sum[g] += red[at(w, g, r)];
         }
-        if (p0 + li < end && li < 2 * NX)
+        if (p0 + li < end && li < (NX == 0 ? 1 : 2 * NX))
             finish4<MODE, G>(a, expert, split, out_row<MODE>(a, p0 + li), row0 + r * kTile + 4 * kq, sum);
     }
     if (MODE != kLinear && W > 1) __syncthreads();   // before the next pass writes LDS
 }
 
-// LDS of a stream workgroup: the waves' slots, later their sums.
+// LDS of a stream workgroup in 16-byte pieces: the waves' slots, later their sums.
 template <int G, int P, int R, int W, int NX>
 constexpr int stream_lds() {
-    return W * kWave * (P * NX > G * R ? P * NX : G * R);
+    return NX == 0 ? W * (P * kDotSlot > G * R * 4 ? P * kDotSlot : G * R * 4)
+                   : W * kWave * (P * NX > G * R ? P * NX : G * R);
 }
 
 template <bool BF16, int L, int G, int P, int MODE, int R, int U, int W, int NXMAX>
@@ -638,10 +776,10 @@ __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
     const uint32_t q = blockIdx.x / strips;   // block of tokens and split, or place in the list of experts
     const int64_t row0 = int64_t(blockIdx.x - q * strips) * (R * kTile);
     if constexpr (MODE == kLinear) {
-        const int32_t block = q / a.splits, p = block * 2 * NXMAX;
-        const int32_t left = static_cast<int32_t>(a.n) - p;
+        constexpr int32_t kTokens = NXMAX == 0 ? 1 : 2 * NXMAX;
+        const int32_t block = q / a.splits, p = block * kTokens, left = static_cast<int32_t>(a.n) - p;
         stream_pass<BF16, L, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q - block * a.splits, p,
-                                                         left < 2 * NXMAX ? p + left : p + 2 * NXMAX, lds);
+                                                         left < kTokens ? p + left : p + kTokens, lds);
     } else {
         const int expert = a.active[q];
         if (expert < 0) return;   // workgroup-uniform
@@ -1125,8 +1263,8 @@ constexpr int kRouteDepth = 4;   // steps of 32 elements a wave loads at a time
 // these agree to some 14 digits.  The fp64 matrix instruction takes 4 elements of
 // K, one per lane quarter; a lane loads 8 consecutive ones at a time, so
 // instruction j of a step of 32 multiplies elements 8 q + j of all quarters q.
-// 64 experts x 7168: 1 token - us, 16 tokens - us, 64 tokens - us (summed by the
-// VALU, an expert per workgroup, they took 5, 58 and 53 us).
+// 64 experts x 7168: 1 or 16 tokens 4.7 us, 64 tokens of 4096 5.4 us (summed by
+// the VALU, an expert per workgroup, they took 5, 58 and 53 us).
 template <bool BF16>
 __global__ void __launch_bounds__(kRouteWaves * kWave) route_logits(const RouteArgs a) {
     __shared__ double red[kRouteWaves - 1][4][kWave];
@@ -1299,7 +1437,7 @@ __device__ __forceinline__ void sort_slots(const RouteArgs &a) {
 
 // Few tokens: choice and sorting by one workgroup, a wave per token at a time.
 // More: each its own kernel, a workgroup per kChooseWaves tokens (64 experts x 64
-// tokens: - us, by one workgroup 28).
+// tokens: 7 + 5 us, by one workgroup 28).
 constexpr int kSelectWaves = 16, kChooseWaves = 4;
 constexpr int kSelectLds = 32768;   // bytes of scores and keys
 
@@ -1357,8 +1495,9 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine(const CombineArgs
 // taken by itself, so the slots need no sorting.  Its expert is chosen by each
 // workgroup that multiplies for it, and the down product's workgroups, which own
 // rows of a token's output, finish the output themselves: three launches, and no
-// partial outputs in memory.  7168 x 2048, 8 of 64 experts, one token: - us where
-// the five kernels take - us.
+// partial outputs in memory.  7168 x 2048, 8 of 64 experts, one token: 52 us
+// (logits 4.7, up product with the choice 28, down product 17), where the five
+// kernels take 65; the weights' 198 MB take 31 at the rate of a large read.
 
 constexpr int kSlotUpWaves = 4;
 constexpr int kSlotWaves = 8;                   // of the slots' down product
@@ -1439,8 +1578,8 @@ __global__ void __launch_bounds__(kSlotUpWaves * kWave, 2) ffn_slot_up(const Slo
     const uint32_t token = slot / s.r.topk;
     const int expert = __builtin_amdgcn_readfirstlane(
         choose_slot<kSlotUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
-    stream_pass<BF16, L, 2, 1, kSlotUp, kSlotUpTiles, 3, kSlotUpWaves, 1>(s.f, expert, int64_t(strip) * kSlotUpTiles * kTile, 0,
-                                                                       slot, slot + 1, lds);
+    stream_pass<BF16, L, 2, 1, kSlotUp, kSlotUpTiles, 3, kSlotUpWaves, 1>(s.f, expert, int64_t(strip) * kSlotUpTiles * kTile,
+                                                                          0, slot, slot + 1, lds);
 }
 
 // Y of 16 rows of one token: the waves share the token's slots, or several waves
@@ -1471,9 +1610,9 @@ __global__ void __launch_bounds__(kSlotWaves * kWave, 2) ffn_slot_down(const Slo
         const int32_t slot = static_cast<int32_t>(t * topk + j);
         f32x4 acc[1][1];
         stream_sums<true, L, 1, P, kSlotDown, 1, 2, 1>(s.f, s.r.choice[slot], strip * kTile, 0, slot, slot + 1,
-                                                            lds + wave * (P * 2 * 32), wave % share, share, acc);
-        if (lane % 16 == 0)
-            *reinterpret_cast<f32x4 *>(&sums[j * share + wave % share][4 * (lane / 16)]) = acc[0][0];
+                                                       lds + wave * (P * 2 * 32), wave % share, share, acc);
+        if (lane % kTile == 0)
+            *reinterpret_cast<f32x4 *>(&sums[j * share + wave % share][4 * (lane / kTile)]) = acc[0][0];
     }
     __syncthreads();
     if (!last) return;

@@ -88,10 +88,10 @@ inline int check_moe_shape(const nvfp4_moe_layer_t &l, int64_t tokens) {
 constexpr int64_t kStreamTokens = 16;   // tokens of a workgroup of the stream kernel
 constexpr int64_t kStreamOnlyTokens = 8;
 constexpr int64_t kComputeUnits = 256;  // CUs of an MI355X (8 XCDs x 32)
-constexpr int kStreamWaves = 8;
-
-// Row tiles per matrix of a stream workgroup of the linear layer.
-constexpr int stream_tiles(bool gated) { return gated ? 1 : 1; }
+// Waves of a stream workgroup: 4 where the workgroups go round the compute units
+// twice, else 8 (14336 x 4096, 896 workgroups: 1 token 9.8 and 12.2 us, 4 tokens
+// 11.4 and 13.7; 37 tokens of 1001 x 2064, 189 workgroups: 15.4 and 9.3).
+constexpr int kStreamWaves = 8, kStreamWavesMany = 4;
 
 // Shapes of the tile kernel, largest first.  A workgroup owns rows() rows of each
 // matrix and tokens() tokens; its wk groups of wm waves take the windows of K in
@@ -134,6 +134,7 @@ inline float rounds_us(const float (&us)[4], int64_t count, int64_t wins) {
 struct LinearPlan {
     bool stream;        // stream kernel
     int tile;           // shape of the tile kernel, or -1; neither: the simple kernel
+    int waves;          // of a stream workgroup
     int64_t strips;     // workgroups along the rows
     int64_t blocks;     // workgroups along the tokens
     int64_t splits;     // workgroups along K
@@ -163,9 +164,10 @@ inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool 
         return s == 1 ? 0.0f : kFinishUs + static_cast<float>(s * n * m) * (gated ? 16.0f : 8.0f) / kFinishBytesPerUs;
     };
     p.stream = true;
-    p.strips = ceil_div(m, kTile * stream_tiles(gated));
+    p.strips = ceil_div(m, kTile);
     p.blocks = ceil_div(n, kStreamTokens);
     while (p.strips * p.blocks * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
+    p.waves = p.strips * p.blocks * p.splits >= 2 * kComputeUnits ? kStreamWavesMany : kStreamWaves;
     if (n > kStreamOnlyTokens) {
         float best = rounds_us(kStreamUs[gated], p.strips * p.blocks * p.splits, ceil_div(wins, p.splits)) +
                      finish_us(p.splits);

@@ -118,9 +118,11 @@ int check_linear(const LinearCall &c) {
 
 template <bool BF16, int L, int G, int NX>
 int launch_linear_stream(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
-    constexpr int R = stream_tiles(G == 2);
-    return run(ffn_stream<BF16, L, G, 1, kLinear, R, 2, kStreamWaves, NX>,
-               dim3(static_cast<uint32_t>(p.strips * p.blocks * p.splits)), kStreamWaves * kWave, a, stream);
+    const dim3 grid(static_cast<uint32_t>(p.strips * p.blocks * p.splits));
+    return p.waves == kStreamWaves
+               ? run(ffn_stream<BF16, L, G, 1, kLinear, 1, 2, kStreamWaves, NX>, grid, kStreamWaves * kWave, a, stream)
+               : run(ffn_stream<BF16, L, G, 1, kLinear, 1, 2, kStreamWavesMany, NX>, grid, kStreamWavesMany * kWave, a,
+                     stream);
 }
 
 template <bool BF16, int L, int G, int KIND>
@@ -133,7 +135,8 @@ int launch_tile(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
 template <bool BF16, int L, int G>
 int launch_linear(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
     if (p.stream)
-        return a.n <= 2   ? launch_linear_stream<BF16, L, G, 1>(a, p, stream)
+        return a.n == 1   ? launch_linear_stream<BF16, L, G, 0>(a, p, stream)
+               : a.n == 2 ? launch_linear_stream<BF16, L, G, 1>(a, p, stream)
                : a.n <= 4 ? launch_linear_stream<BF16, L, G, 2>(a, p, stream)
                : a.n <= 8 ? launch_linear_stream<BF16, L, G, 4>(a, p, stream)
                           : launch_linear_stream<BF16, L, G, 8>(a, p, stream);
