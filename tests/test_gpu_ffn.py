@@ -101,6 +101,26 @@ def test_linear_every_tile_shape(n, m, k):
     linear_case(rng, n, (m + 1) // 2, k, x="bf16", y="f32", gated=True, residual="apart", act="relu", ldx=k + 1)
 
 
+@pytest.mark.parametrize("n,m,k", [(1, 8200, 320), (2, 8193, 448), (4, 8200, 80), (7, 8230, 640), (16, 8209, 576)])
+def test_linear_few_tokens_many_rows(n, m, k):
+    """Enough row tiles for the smaller workgroups of the stream kernel."""
+    rng = np.random.default_rng(n + 100)
+    linear_case(rng, n, m, k, x="bf16", act="silu", bias=True, layout="row" if k % 64 else "packed")
+    linear_case(rng, n, m, k, x="f16", y="f32", gated=True, act="gelu", residual="apart", ldx=k + 1, xoff=1)
+
+
+def test_linear_rows_four_million_elements_apart():
+    """Token offsets past 32 bits."""
+    rng = np.random.default_rng(18)
+    codes, scales = weight(rng, 1, 48, 64)
+    dc, ds = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    far = torch.zeros((300, 1 << 22), dtype=torch.bfloat16, device="cuda")[:, 64:128]
+    for n in (5, 40, 300):
+        x = torch.from_numpy(rng.standard_normal((n, 64))).to(torch.bfloat16).cuda()
+        far[:n] = x
+        assert torch.equal(pd.linear(far[:n], dc, ds, 48), pd.linear(x, dc, ds, 48))
+
+
 @pytest.mark.parametrize("k", [16, 32, 48, 80, 112, 144, 240, 272, 1040, 2064])
 def test_linear_row_major_k_of_whole_blocks(k):
     rng = np.random.default_rng(k)
@@ -191,7 +211,7 @@ def test_linear_repeats_bit_for_bit():
 # ---------------------------------------------------------------- MoE
 def moe_case(rng, tokens, experts, topk, hidden, inter, x="bf16", y=None, act="silu", scoring="softmax",
              route_bias=False, renormalize=True, scale=1.0, residual=None, layout="row", ldx=0, xoff=0,
-             ldy=0, alpha=True, edit=None, stream=None, ws=False):
+             ldy=0, alpha=True, edit=None, stream=None, ws=False, woff=0):
     y = y or x
     c13, s13 = weight(rng, 2 * experts, inter, hidden)
     c2, s2 = weight(rng, experts, hidden, inter)
@@ -208,7 +228,7 @@ def moe_case(rng, tokens, experts, topk, hidden, inter, x="bf16", y=None, act="s
         w13 = pd.pack_weight(dev(c13), dev(s13))
         w2 = pd.pack_weight(dev(c2), dev(s2))
     else:
-        w13, w2 = (bytes_at(c13), bytes_at(s13)), (bytes_at(c2), bytes_at(s2))
+        w13, w2 = (bytes_at(c13, woff), bytes_at(s13, woff)), (bytes_at(c2, woff), bytes_at(s2, woff))
     layer = pd.MoeLayer(device(rt, x).contiguous(), *w13, *w2, inter=inter, topk=topk, alpha13=dev(a13),
                         alpha2=dev(a2), route_bias=dev(rb), activation=act, scoring=scoring,
                         renormalize=renormalize, routed_scale=scale, packed=layout == "packed")
@@ -272,6 +292,46 @@ def test_moe_strided_and_unaligned_input():
 
 def test_moe_more_than_one_pass_of_tokens_per_expert():
     moe_case(np.random.default_rng(23), 150, 2, 2, 192, 128, layout="packed", alpha=False)
+
+
+@pytest.mark.parametrize("tokens,experts,topk,hidden,inter", [
+    (12, 7, 4, 128, 768), (16, 40, 6, 80, 400), (5, 1024, 64, 64, 112), (17, 1000, 3, 64, 64),
+    (300, 70, 8, 1024, 256), (90, 130, 5, 1088, 192)])
+def test_moe_by_expert(tokens, experts, topk, hidden, inter):
+    """Sizes at which slots are sorted by expert: few and many tokens, experts up to the most,
+    few and many workgroups, several passes of tokens per expert."""
+    print(f"moe by expert {tokens} {experts} {topk} {hidden} {inter}", flush=True)
+    rng = np.random.default_rng(tokens + experts)
+    odd = hidden % 64 or inter % 64
+    moe_case(rng, tokens, experts, topk, hidden, inter, layout="row" if odd else "packed", residual="apart")
+    moe_case(rng, tokens, experts, topk, hidden, inter, x="f16", y="f32", scoring="sigmoid", route_bias=True,
+             renormalize=False, scale=0.5, ldx=hidden + 1)
+
+
+@pytest.mark.parametrize("woff", [1, 4])
+def test_moe_misaligned_weights(woff):
+    rng = np.random.default_rng(28)
+    moe_case(rng, 3, 6, 2, 128, 192, woff=woff)
+    moe_case(rng, 40, 6, 2, 128, 192, x="f16", y="f32", woff=woff)
+
+
+def test_moe_rows_four_million_elements_apart():
+    """Token offsets past 32 bits: within what the fast kernels can address, and past it."""
+    rng = np.random.default_rng(29)
+    c13, s13 = weight(rng, 12, 64, 64)
+    c2, s2 = weight(rng, 6, 64, 64)
+    dev = lambda v: torch.from_numpy(v).cuda()
+    layer = pd.MoeLayer(torch.from_numpy(rng.standard_normal((6, 64))).to(torch.bfloat16).cuda(),
+                        *pd.pack_weight(dev(c13), dev(s13)), *pd.pack_weight(dev(c2), dev(s2)), inter=64, topk=2,
+                        alpha13=torch.full((6, 2), 0.01, device="cuda"), packed=True)
+    far = torch.zeros((300, 1 << 22), dtype=torch.bfloat16, device="cuda")[:, 64:128]
+    for n in (2, 60, 300):
+        x = torch.from_numpy(rng.standard_normal((n, 64))).to(torch.bfloat16).cuda()
+        far[:n] = x
+        a = pd.moe_layer(far[:n], layer, out_dtype=torch.float32)
+        b = pd.moe_layer(x, layer, out_dtype=torch.float32)
+        # other kernels may add in another order: some 1e-6 of the largest output
+        assert float((a - b).abs().max()) <= 1e-5 * float(b.abs().max()), n
 
 
 def test_moe_ties_go_to_the_lowest_index():

@@ -10,6 +10,8 @@
   GEMV plan (``precision_decode_amd/csrc/mma_plan.h``: shape rules, variants,
   defaults, launch plan) and checks 200000 random shapes and tunings against
   what the kernels assume, and the default rules.
+* ``tests/host/ffn_plan_check.cpp`` does the same for the plan of the linear
+  layer and the MoE layer (``precision_decode_amd/csrc/ffn_plan.h``).
 * ``tests/host/oracle_check.c`` compiles the oracle's C sums
   (``oracle/nvfp4_ref.c``) with gcc and runs them on exact-size buffers.
 """
@@ -52,6 +54,16 @@ def test_mma_plan_under_sanitizers(tmp_path):
            os.path.join(HOST, "mma_plan_check.cpp"), "-o", exe]
     run = build_and_run(cmd, exe)
     assert run.returncode == 0 and "mma_plan_check ok" in run.stdout, run.stdout + run.stderr
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_ffn_plan_under_sanitizers(tmp_path):
+    exe = str(tmp_path / "ffn_plan_check")
+    cmd = ["g++", "-std=c++17", *SAN, "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(ROOT, "precision_decode_amd", "csrc"),
+           os.path.join(HOST, "ffn_plan_check.cpp"), "-o", exe]
+    run = build_and_run(cmd, exe)
+    assert run.returncode == 0 and "ffn_plan_check ok" in run.stdout, run.stdout + run.stderr
 
 
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
