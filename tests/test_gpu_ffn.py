@@ -441,3 +441,23 @@ def test_streams_do_not_share_workspaces():
     torch.cuda.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 40])
+def test_feed_forward_example(tokens, capsys):
+    """The example's block, captured and replayed, and its step against the same layers on
+    the oracle's weights."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "feed_forward.py")
+    spec = importlib.util.spec_from_file_location("feed_forward_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(["--tokens", str(tokens), "--hidden", "512", "--inter", "256", "--experts", "8", "--topk", "2",
+                         "--steps", "3"])
+    assert "equals" in capsys.readouterr().out
+    y = example.Block(512, 256, 8, 2).step(torch.randn((tokens, 512), device="cuda").to(torch.bfloat16),
+                                           torch.zeros((tokens, 512), dtype=torch.bfloat16, device="cuda"))
+    # unit-size weights and inputs: outputs of unit size
+    assert bool(y.isfinite().all()) and 0.2 < float(y.float().std()) < 5.0
