@@ -1241,15 +1241,40 @@ struct RouteArgs {
     float routed_scale;
 };
 
+// op over the 64 lanes, the same value in every lane: DPP exchanges inside
+// 16-lane rows, then swaps of rows and of 32-lane halves, as wave_sum.
+template <typename OP>
+__device__ __forceinline__ double wave_reduce64(double v, OP op) {
+    const auto joined = [](uint32_t lo, uint32_t hi) {
+        return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+    };
+    const auto dpp = [&](auto ctrl) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        constexpr int c = decltype(ctrl)::value;
+        v = op(v, joined(__builtin_amdgcn_mov_dpp(static_cast<int>(u), c, 0xF, 0xF, false),
+                         __builtin_amdgcn_mov_dpp(static_cast<int>(u >> 32), c, 0xF, 0xF, false)));
+    };
+    dpp(std::integral_constant<int, 0xB1>{});    // quad_perm [1,0,3,2]
+    dpp(std::integral_constant<int, 0x4E>{});    // quad_perm [2,3,0,1]
+    dpp(std::integral_constant<int, 0x141>{});   // row_half_mirror
+    dpp(std::integral_constant<int, 0x140>{});   // row_mirror
+    uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t lo = static_cast<uint32_t>(u), hi = static_cast<uint32_t>(u >> 32);
+    const auto l16 = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto h16 = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    v = op(joined(l16[0], h16[0]), joined(l16[1], h16[1]));
+    u = __builtin_bit_cast(uint64_t, v);
+    lo = static_cast<uint32_t>(u);
+    hi = static_cast<uint32_t>(u >> 32);
+    const auto l32 = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+    const auto h32 = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    return op(joined(l32[0], h32[0]), joined(l32[1], h32[1]));
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    return wave_reduce64(v, [](double a, double b) { return a + b; });
 }
 __device__ __forceinline__ double wave_max64(double v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o));
-    return v;
+    return wave_reduce64(v, [](double a, double b) { return fmax(a, b); });
 }
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
@@ -1316,15 +1341,6 @@ __global__ void __launch_bounds__(kRouteWaves * kWave) route_logits(const RouteA
     }
 }
 
-// A token's score of an expert with logit z, once the softmax's maximum and sum
-// are known.
-struct Scores {
-    double top, sum;
-    int scoring;
-    __device__ __forceinline__ double score(double z) const {
-        return scoring == NVFP4_SCORE_SOFTMAX ? exp(z - top) / sum : 1.0 / (1.0 + exp(-z));
-    }
-};
 constexpr int kLogitLoads = 16;
 __device__ __forceinline__ double logit(const RouteArgs &a, int64_t t, int e) {
     const double *z = a.logits + t * a.experts + e;
@@ -1355,18 +1371,17 @@ __device__ __forceinline__ float routed_weight(const RouteArgs &a, double score,
 __device__ __forceinline__ void choose_token(const RouteArgs &a, int64_t t, double *score, double *keys,
                                              int32_t *order) {
     const int lane = threadIdx.x % kWave, experts = static_cast<int>(a.experts);
-    Scores sc = {-INFINITY, 0.0, a.scoring};
+    const bool softmax = a.scoring == NVFP4_SCORE_SOFTMAX;
+    double top = -INFINITY, sum = 0.0;
     for (int e = lane; e < experts; e += kWave) {
         score[e] = logit(a, t, e);
-        sc.top = fmax(sc.top, score[e]);
+        top = fmax(top, score[e]);
     }
-    if (a.scoring == NVFP4_SCORE_SOFTMAX) {
-        sc.top = wave_max64(sc.top);
-        for (int e = lane; e < experts; e += kWave) sc.sum += exp(score[e] - sc.top);
-        sc.sum = wave_sum64(sc.sum);
-    }
+    if (softmax) top = wave_max64(top);
+    for (int e = lane; e < experts; e += kWave) sum += score[e] = softmax ? exp(score[e] - top) : exp(-score[e]);
+    if (softmax) sum = wave_sum64(sum);
     for (int e = lane; e < experts; e += kWave) {
-        score[e] = sc.score(score[e]);
+        score[e] = softmax ? score[e] / sum : 1.0 / (1.0 + score[e]);
         keys[e] = choice_key(a, e, score[e]);
     }
     wave_lds_fence();
@@ -1511,7 +1526,7 @@ struct SlotArgs {
 // (workgroup-uniform): its weight, too, to memory.
 template <int THREADS>
 __device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j, bool weigh) {
-    __shared__ double score[kMaxExperts], keys[kMaxExperts], red[THREADS / kWave];
+    __shared__ double score[kMaxExperts], keys[kMaxExperts], red[2][THREADS / kWave];
     __shared__ int32_t rank[kMaxExperts], order[kMaxTopk];
     constexpr int kWaves = THREADS / kWave;
     const int experts = static_cast<int>(a.experts), thread = threadIdx.x, wave = thread / kWave;
@@ -1521,25 +1536,24 @@ __device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j,
         rank[e] = 0;
         top = fmax(top, score[e]);
     }
-    Scores sc = {0.0, 0.0, a.scoring};
-    if (a.scoring == NVFP4_SCORE_SOFTMAX) {
+    const bool softmax = a.scoring == NVFP4_SCORE_SOFTMAX;
+    double sum = 0.0;
+    if (softmax) {
         top = wave_max64(top);
-        if (thread % kWave == 0) red[wave] = top;
+        if (thread % kWave == 0) red[0][wave] = top;
         __syncthreads();
-        for (int w = 0; w < kWaves; ++w) top = fmax(top, red[w]);
-        __syncthreads();
-        double sum = 0.0;
-        for (int e = thread; e < experts; e += THREADS) sum += exp(score[e] - top);
+        for (int w = 0; w < kWaves; ++w) top = fmax(top, red[0][w]);
+    }
+    for (int e = thread; e < experts; e += THREADS) sum += score[e] = softmax ? exp(score[e] - top) : exp(-score[e]);
+    if (softmax) {
         sum = wave_sum64(sum);
-        if (thread % kWave == 0) red[wave] = sum;
+        if (thread % kWave == 0) red[1][wave] = sum;
         __syncthreads();
         sum = 0.0;
-        for (int w = 0; w < kWaves; ++w) sum += red[w];
-        sc.top = top;
-        sc.sum = sum;
+        for (int w = 0; w < kWaves; ++w) sum += red[1][w];
     }
     for (int e = thread; e < experts; e += THREADS) {
-        score[e] = sc.score(score[e]);
+        score[e] = softmax ? score[e] / sum : 1.0 / (1.0 + score[e]);
         keys[e] = choice_key(a, e, score[e]);
     }
     __syncthreads();
