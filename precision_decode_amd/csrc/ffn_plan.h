@@ -113,8 +113,9 @@ constexpr TileKind kGatedTileKinds[] = {
     {1, 16, 8, 1, {210, 0, 0, 0}}, {1, 8, 8, 1, {111, 0, 0, 0}}, {1, 8, 4, 2, {70, 0, 0, 0}},
     {1, 4, 4, 2, {41, 72, 0, 0}},  {1, 2, 4, 2, {28, 45, 0, 0}}};
 constexpr int kNumTileKinds = 6, kNumGatedTileKinds = 5;
-// the stream kernel's, for 16 tokens and for one and two matrices
-constexpr float kStreamUs[2][4] = {{9, 11.5f, 0, 0}, {11, 18, 0, 0}};
+// the stream kernel's, for up to 8 and up to 16 tokens, one and two matrices
+constexpr float kStreamUs[2][2][4] = {{{6, 8, 0, 0}, {8, 12, 0, 0}}, {{9, 11.5f, 0, 0}, {11, 18, 0, 0}}};
+constexpr int64_t kMaxStreamSplits = 64;
 constexpr float kRoundUs = 3;            // until a workgroup has its first operands
 constexpr float kFinishUs = 6;           // a second kernel that adds the sums of a split of K
 constexpr float kFinishBytesPerUs = 3e6;
@@ -144,16 +145,15 @@ struct LinearPlan {
 };
 
 // `fast`: the weight's alignment allows the fast kernels; `x_aligned`: so do X's
-// rows.  Up to 8 tokens: the stream kernel, K split while the workgroups leave
-// compute units idle and every wave keeps a window of its own.  More: what the
-// times above say is fastest, of the stream kernel in blocks of 16 tokens, which
-// reads and decodes the weights once a block but has the most workgroups, and the
-// shapes of the tile kernel, which read and decode the less per product the
-// larger they are, with K whole or split.  Measured, in us, for 256 x 256,
-// 256 x 128, 128 x 128, 128 x 64, 64 x 64 tiles on 4096 x 7168: 256 tokens -, 96,
-// 60, 37, 32; 512 tokens -, 96, 61, 41, 50; 1024 tokens -, 98, 70, 72, 93; 4096
-// tokens 204, 240, 264, -, -.  K whole and split: 64 tokens 20.7 and 17.8 (in
-// two); 32 tokens, 7168 x 2048, 9.4 and 12.4.
+// rows.  What the times above say is fastest: up to 8 tokens of the stream kernel
+// with K whole or split, for more also of the stream kernel in blocks of 16
+// tokens, which reads and decodes the weights once a block but has the most
+// workgroups, and the shapes of the tile kernel, which read and decode the less
+// per product the larger they are.  Measured, in us, for 256 x 256, 256 x 128,
+// 128 x 128, 128 x 64, 64 x 64 tiles on 4096 x 7168: 256 tokens -, 96, 60, 37, 32;
+// 512 tokens -, 96, 61, 41, 50; 1024 tokens -, 98, 70, 72, 93; 4096 tokens 204,
+// 240, 264, -, -.  K whole and split: 64 tokens 20.7 and 17.8 (in two); 32 tokens,
+// 7168 x 2048, 9.4 and 12.4.
 inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool fast, bool x_aligned) {
     LinearPlan p = {};
     p.splits = 1;
@@ -166,11 +166,16 @@ inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool 
     p.stream = true;
     p.strips = ceil_div(m, kTile);
     p.blocks = ceil_div(n, kStreamTokens);
-    while (p.strips * p.blocks * p.splits < kComputeUnits && wins >= 2 * p.splits * kStreamWaves) p.splits *= 2;
+    float best = 0.0f;
+    for (int64_t s = 1; s <= kMaxStreamSplits && (s == 1 || wins >= s * kStreamWaves); s *= 2) {
+        const float us = rounds_us(kStreamUs[n > kStreamOnlyTokens][gated], p.strips * p.blocks * s, ceil_div(wins, s)) +
+                         finish_us(s);
+        if (s > 1 && us >= best) continue;
+        best = us;
+        p.splits = s;
+    }
     p.waves = p.strips * p.blocks * p.splits >= 2 * kComputeUnits ? kStreamWavesMany : kStreamWaves;
     if (n > kStreamOnlyTokens) {
-        float best = rounds_us(kStreamUs[gated], p.strips * p.blocks * p.splits, ceil_div(wins, p.splits)) +
-                     finish_us(p.splits);
         const int kinds = gated ? kNumGatedTileKinds : kNumTileKinds;
         for (int i = 0; i < kinds; ++i) {
             const TileKind &t = gated ? kGatedTileKinds[i] : kTileKinds[i];
