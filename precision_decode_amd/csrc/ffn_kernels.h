@@ -1236,7 +1236,7 @@ struct RouteArgs {
     int32_t *offsets, *choice, *list, *active;
     float *weights;
     int64_t tokens, experts, hidden;
-    int32_t splits, groups;     // groups: entries of active
+    int32_t splits, groups;     // splits 0: no logits, see own_logits; groups: entries of active
     int32_t topk, scoring, renormalize;
     float routed_scale;
 };
@@ -1510,7 +1510,8 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine(const CombineArgs
 // taken by itself, so the slots need no sorting.  Its expert is chosen by each
 // workgroup that multiplies for it, and the down product's workgroups, which own
 // rows of a token's output, finish the output themselves: three launches, and no
-// partial outputs in memory.  7168 x 2048, 8 of 64 experts, one token: 52 us
+// partial outputs in memory.  Where the router is small the workgroups of the up
+// product compute the logits, too: two launches.  7168 x 2048, 8 of 64 experts, one token: 52 us
 // (logits 4.7, up product with the choice 28, down product 17), where the five
 // kernels take 65; the weights' 198 MB take 31 at the rate of a large read.
 
@@ -1522,17 +1523,55 @@ struct SlotArgs {
     RouteArgs r;
 };
 
+// The logits of one token by a workgroup, in fp64 as route_logits: a wave takes
+// four experts at a time, a lane 8 elements of hidden.
+template <bool BF16, int THREADS>
+__device__ __forceinline__ void own_logits(const RouteArgs &a, int64_t t, double *score) {
+    constexpr int kEach = 4;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, experts = static_cast<int>(a.experts);
+    const uint8_t *x = a.X + 2 * t * a.ldx;
+    for (int e0 = kEach * wave; e0 < experts; e0 += kEach * (THREADS / kWave)) {
+        double s[kEach] = {};
+        for (int64_t i = 8 * lane; i < a.hidden; i += 8 * kWave) {
+            u32x4 xv, wv[kEach];
+            __builtin_memcpy(&xv, x + 2 * i, 16);
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int64_t e = e0 + k < experts ? e0 + k : experts - 1;
+                __builtin_memcpy(&wv[k], a.router + 2 * (e * a.hidden + i), 16);
+            }
+            const auto value = [](const u32x4 &v, int j) {
+                const uint16_t b = static_cast<uint16_t>(v[j / 2] >> (16 * (j & 1)));
+                return double(BF16 ? bf16_value(b) : static_cast<float>(__builtin_bit_cast(_Float16, b)));
+            };
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) s[k] = __builtin_fma(value(wv[k], j), value(xv, j), s[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            s[k] = wave_sum64(s[k]);
+            if (lane == 0 && e0 + k < experts) score[e0 + k] = s[k];
+        }
+    }
+}
+
 // The expert of rank j of token t, to every thread of the workgroup.  `weigh`
 // (workgroup-uniform): its weight, too, to memory.
-template <int THREADS>
+template <bool BF16, int THREADS>
 __device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j, bool weigh) {
     __shared__ double score[kMaxExperts], keys[kMaxExperts], red[2][THREADS / kWave];
     __shared__ int32_t rank[kMaxExperts], order[kMaxTopk];
     constexpr int kWaves = THREADS / kWave;
     const int experts = static_cast<int>(a.experts), thread = threadIdx.x, wave = thread / kWave;
     double top = -INFINITY;
+    if (a.splits == 0) {   // uniform: a small router
+        own_logits<BF16, THREADS>(a, t, score);
+        __syncthreads();
+    }
     for (int e = thread; e < experts; e += THREADS) {
-        score[e] = logit(a, t, e);
+        if (a.splits > 0) score[e] = logit(a, t, e);
         rank[e] = 0;
         top = fmax(top, score[e]);
     }
@@ -1591,7 +1630,7 @@ __global__ void __launch_bounds__(kSlotUpWaves * kWave, 2) ffn_slot_up(const Slo
     const uint32_t slot = blockIdx.x / strips, strip = blockIdx.x - slot * strips;
     const uint32_t token = slot / s.r.topk;
     const int expert = __builtin_amdgcn_readfirstlane(
-        choose_slot<kSlotUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
+        choose_slot<BF16, kSlotUpWaves * kWave>(s.r, token, slot - token * s.r.topk, strip == 0));
     stream_pass<BF16, L, 2, 1, kSlotUp, kSlotUpTiles, 3, kSlotUpWaves, 1>(s.f, expert, int64_t(strip) * kSlotUpTiles * kTile,
                                                                           0, slot, slot + 1, lds);
 }

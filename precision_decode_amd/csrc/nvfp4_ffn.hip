@@ -370,11 +370,6 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     r.scoring = l.scoring;
     r.renormalize = l.renormalize;
     r.routed_scale = l.routed_scale;
-    const dim3 route_grid(static_cast<uint32_t>(ceil_div(l.experts, kTile) * r.splits),
-                          static_cast<uint32_t>(ceil_div(c.tokens, kTile)));
-    int s = run(bf16 ? route_logits<true> : route_logits<false>, route_grid, kRouteWaves * kWave, r, stream);
-    if (s != NVFP4_GEMV_OK) return s;
-
     const int planes = c.y_type == NVFP4_OUT_F32 ? 3 : 2;
     FfnArgs up = {};
     up.splits = 1;
@@ -422,7 +417,17 @@ int moe(const MoeCall &c, uint8_t *ws, hipStream_t stream) {
     y.topk = l.topk;
     y.y_type = c.y_type;
 
-    if (few_slots(l, c.tokens) && up_layout != kNoLayout && down_layout != kNoLayout) {
+    const bool few = few_slots(l, c.tokens) && up_layout != kNoLayout && down_layout != kNoLayout;
+    int s = NVFP4_GEMV_OK;
+    if (few && small_router(l)) {
+        r.splits = 0;
+    } else {
+        const dim3 grid(static_cast<uint32_t>(ceil_div(l.experts, kTile) * r.splits),
+                        static_cast<uint32_t>(ceil_div(c.tokens, kTile)));
+        s = run(bf16 ? route_logits<true> : route_logits<false>, grid, kRouteWaves * kWave, r, stream);
+        if (s != NVFP4_GEMV_OK) return s;
+    }
+    if (few) {
         const SlotArgs u = {up, r}, d = {down, r};
         s = up_layout == kRows          ? launch_slot_up<kRows>(u, bf16, slots, stream)
             : up_layout == kPackedTiles ? launch_slot_up<kPackedTiles>(u, bf16, slots, stream)
