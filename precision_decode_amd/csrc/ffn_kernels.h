@@ -52,7 +52,7 @@ struct FfnArgs {
     int32_t y_planes;           // kMoeUp: planes of h to write
     float *part;                // kLinear with K split: [split][n][matrices][m] sums, or NULL
     int32_t splits;             // workgroups along K
-    int32_t vec;                // kLinear: rows of Y and of the residual start on 16-byte boundaries
+    int32_t passes;             // MoE: workgroups along an expert's slots
 };
 
 // ---------------------------------------------------------------- arithmetic
@@ -773,7 +773,7 @@ template <bool BF16, int L, int G, int P, int MODE, int R, int U, int W, int NXM
 __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
     __shared__ u32x4 lds[stream_lds<G, P, R, W, NXMAX>()];
     const uint32_t strips = static_cast<uint32_t>((a.m + R * kTile - 1) / (R * kTile));
-    const uint32_t q = blockIdx.x / strips;   // block of tokens and split, or place in the list of experts
+    const uint32_t q = blockIdx.x / strips;   // block of tokens and split, or place in the list of experts and pass
     const int64_t row0 = int64_t(blockIdx.x - q * strips) * (R * kTile);
     if constexpr (MODE == kLinear) {
         constexpr int32_t kTokens = NXMAX == 0 ? 1 : 2 * NXMAX;
@@ -781,10 +781,11 @@ __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
         stream_pass<BF16, L, G, P, MODE, R, U, W, NXMAX>(a, 0, row0, q - block * a.splits, p,
                                                          left < kTokens ? p + left : p + kTokens, lds);
     } else {
-        const int expert = a.active[q];
+        const uint32_t place = q / a.passes, pass = q - place * a.passes;
+        const int expert = a.active[place];
         if (expert < 0) return;   // workgroup-uniform
         const TokenRange range = expert_range<MODE>(a, expert);
-        for (int32_t p = range.first; p < range.end; p += 2 * NXMAX) {
+        for (int32_t p = range.first + pass * 2 * NXMAX; p < range.end; p += a.passes * 2 * NXMAX) {
             const int32_t end = range.end - p > 2 * NXMAX ? p + 2 * NXMAX : range.end;
             const int n = end - p;   // workgroup-uniform
             if (n <= 2)
@@ -800,19 +801,18 @@ __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
 }
 
 // ---------------------------------------------------------------- tile kernel
-// 8 consecutive values of a row of Y's type; `whole`: all 8 exist and the row
-// starts on a 16-byte boundary.
+// 8 consecutive values of a row of Y's type, aligned to their elements only: 16
+// bytes go in one access all the same.
 struct Row8 {
     u32x4 v[2];
 };
 __device__ __forceinline__ Row8 load_row8(const void *p, int64_t i, int type) {
     Row8 o;
     if (type == NVFP4_OUT_F32) {
-        const u32x4 *from = reinterpret_cast<const u32x4 *>(static_cast<const float *>(p) + i);
-        o.v[0] = from[0];
-        o.v[1] = from[1];
+        __builtin_memcpy(&o, static_cast<const float *>(p) + i, 32);
     } else {
-        o.v[0] = o.v[1] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + i);
+        __builtin_memcpy(&o.v[0], static_cast<const uint16_t *>(p) + i, 16);
+        o.v[1] = o.v[0];
     }
     return o;
 }
@@ -833,15 +833,13 @@ __device__ __forceinline__ uint32_t round16x2(float lo, float hi, bool bf16) {
 }
 __device__ __forceinline__ void store_row8(void *p, int64_t i, int type, const float (&z)[8]) {
     if (type == NVFP4_OUT_F32) {
-        f32x4 *to = reinterpret_cast<f32x4 *>(static_cast<float *>(p) + i);
-        to[0] = f32x4{z[0], z[1], z[2], z[3]};
-        to[1] = f32x4{z[4], z[5], z[6], z[7]};
+        __builtin_memcpy(static_cast<float *>(p) + i, z, 32);
         return;
     }
     u32x4 o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = round16x2(z[2 * e], z[2 * e + 1], type == NVFP4_OUT_BF16);
-    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p) + i) = o;
+    __builtin_memcpy(static_cast<uint16_t *>(p) + i, &o, 16);
 }
 
 // Orders the workgroup's LDS accesses around the barrier and leaves global
@@ -1098,7 +1096,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     const int64_t r = row0 + 8 * (lane % kGroups);
     const int64_t first = tok0 + kTile * NT * wn + lane / kGroups;   // the lane's first token
     const int rows = a.m - r < 8 ? static_cast<int>(a.m - r) : 8;    // of the lane's 8, those that exist
-    const bool vec = a.vec != 0 && rows == 8;
+    const bool whole = rows == 8;
     const float al = a.alpha ? a.alpha[0] : 1.0f, au = G == 2 && a.alpha ? a.alpha[1] : 1.0f;
     float b[G][8];
 #pragma unroll
@@ -1110,7 +1108,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
 #pragma unroll
         for (int i = 0; i < kIters; ++i) {
             const int64_t row = first + kTile * t + kStep * i;
-            if (a.residual && vec && t < NT && row < a.n) to[i] = load_row8(a.residual, row * a.ldr + r, a.y_type);
+            if (a.residual && whole && t < NT && row < a.n) to[i] = load_row8(a.residual, row * a.ldr + r, a.y_type);
         }
     };
     if (!a.part) fetch(S::out_tiles * kg, res[0]);
@@ -1141,7 +1139,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const float(&v)[8] = g == 0 ? z : u;
-                    if (a.m % 4 == 0 && rows == 8) {
+                    if (whole) {
                         store_row8(to, g * a.m, NVFP4_OUT_F32, v);
                     } else {
 #pragma unroll
@@ -1157,7 +1155,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
             if constexpr (G == 2)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[e] *= u[e] * au + b[1][e];
-            if (vec) {
+            if (whole) {
                 if (a.residual) add_row8(res[0][i], a.y_type, z);
                 store_row8(a.Y, row * a.ldy + r, a.y_type, z);
                 continue;

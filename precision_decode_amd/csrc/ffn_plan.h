@@ -227,6 +227,16 @@ inline bool few_workgroups(int64_t rows, int tiles, int64_t groups) {
     return ceil_div(rows, tiles * kTile) * groups < 2 * kComputeUnits;
 }
 
+// Workgroups that share an expert's slots, `each` of the call's workgroups taking
+// `tokens_each` of them at a time: as many as twice the average number of slots
+// needs, as long as the call stays within four workgroups per compute unit (44
+// tokens on all 6 experts of 384 x 192: 48 -> 32 us).
+inline int32_t slot_passes(int64_t tokens, int64_t topk, int64_t groups, int64_t tokens_each, int64_t each) {
+    const int64_t twice = ceil_div(2 * tokens * topk, groups);
+    const int64_t need = ceil_div(twice < tokens ? twice : tokens, tokens_each), room = 4 * kComputeUnits / each;
+    return static_cast<int32_t>(need < room ? need : room < 1 ? 1 : room);
+}
+
 // Whether slots are taken one by one rather than by expert.  An expert that
 // several slots share is then read for each, mostly from the caches, at 0.2 us
 // per MB (7168 x 2048, 8 of 64 experts: 2 tokens 42 MB, 3 tokens 92 MB, 4 tokens

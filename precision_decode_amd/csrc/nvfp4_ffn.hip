@@ -170,9 +170,7 @@ int launch_linear(const FfnArgs &a, const LinearPlan &p, int layout, hipStream_t
         a, dim3(static_cast<uint32_t>(ceil_div(a.m, kTile) * ceil_div(a.n, kTile))), stream);
 }
 
-// Whether rows start on 16-byte boundaries, `piece` elements being 16 bytes.
-bool aligned_rows16(const void *p, int64_t ld, int64_t piece) { return !misaligned(p, 16) && ld % piece == 0; }
-bool aligned_rows(const void *X, int64_t ldx) { return aligned_rows16(X, ldx, 8); }
+bool aligned_rows(const void *X, int64_t ldx) { return !misaligned(X, 16) && ldx % 8 == 0; }
 
 int copy_aligned(const void *X, int64_t ldx, void *to, int64_t rows, int64_t k, hipStream_t stream) {
     const uint16_t *x = static_cast<const uint16_t *>(X);
@@ -215,8 +213,6 @@ int linear(const LinearCall &c, const LinearPlan &p, uint8_t *ws, hipStream_t st
     a.y_type = c.y_type;
     a.splits = static_cast<int32_t>(p.splits);
     a.part = p.part_bytes > 0 ? reinterpret_cast<float *>(ws) : nullptr;
-    const int64_t piece = 16 / type_bytes(c.y_type);
-    a.vec = aligned_rows16(c.Y, c.ldy, piece) && (!c.residual || aligned_rows16(c.residual, c.ldr, piece));
     const int layout = layout_of(c.W, c.sfW, c.k, c.w_layout);
     const int s = c.x_type == NVFP4_OUT_BF16
                       ? c.gated() ? launch_linear<true, 2>(a, p, layout, stream) : launch_linear<true, 1>(a, p, layout, stream)
@@ -283,9 +279,12 @@ constexpr int kUpTiles = 2, kUpWaves = 4, kDownTiles = 4, kDownWaves = 2, kDownF
 // tiles per workgroup read and stage the tokens less often; where they would
 // leave compute units idle, a workgroup takes one.
 template <bool BF16, int L, int R, int W>
-int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
-    return run(ffn_stream<BF16, L, 2, 1, kMoeUp, R, 2, W, 8>,
-               dim3(static_cast<uint32_t>(ceil_div(a.m, R * kTile) * groups)), W * kWave, a, stream);
+int stream_up(FfnArgs a, int64_t groups, hipStream_t stream) {
+    constexpr int NX = 8;
+    const int64_t each = ceil_div(a.m, R * kTile) * groups;
+    a.passes = slot_passes(a.n, a.topk, groups, 2 * NX, each);
+    return run(ffn_stream<BF16, L, 2, 1, kMoeUp, R, 2, W, NX>, dim3(static_cast<uint32_t>(each * a.passes)), W * kWave, a,
+               stream);
 }
 template <bool BF16, int L>
 int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
@@ -294,9 +293,12 @@ int stream_up(const FfnArgs &a, int64_t groups, hipStream_t stream) {
 }
 
 template <int L, int P, int R, int W>
-int stream_down(const FfnArgs &a, int64_t groups, hipStream_t stream) {
-    return run(ffn_stream<true, L, 1, P, kMoeDown, R, 2, W, 4>,
-               dim3(static_cast<uint32_t>(ceil_div(a.m, R * kTile) * groups)), W * kWave, a, stream);
+int stream_down(FfnArgs a, int64_t groups, hipStream_t stream) {
+    constexpr int NX = 4;
+    const int64_t each = ceil_div(a.m, R * kTile) * groups;
+    a.passes = slot_passes(a.n, a.topk, groups, 2 * NX, each);
+    return run(ffn_stream<true, L, 1, P, kMoeDown, R, 2, W, NX>, dim3(static_cast<uint32_t>(each * a.passes)), W * kWave, a,
+               stream);
 }
 template <int L, int P>
 int stream_down(const FfnArgs &a, int64_t groups, hipStream_t stream) {

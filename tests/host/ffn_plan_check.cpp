@@ -96,6 +96,9 @@ void check_moe(const nvfp4_moe_layer_t &l, int64_t tokens) {
     CHECK(w.h - w.weights >= slots * 4);
     CHECK(w.part - w.h >= kMaxPlanes * slots * l.inter * 2);
     CHECK(w.total - w.part >= slots * l.hidden * 4);
+    const int64_t each = ceil_div(l.inter, kTile) * groups;
+    const int32_t passes = slot_passes(tokens, l.topk, groups, 16, each);
+    CHECK(passes >= 1 && (passes == 1 || passes * each <= 4 * kComputeUnits));
     if (few_slots(l, tokens)) {
         CHECK(int64_t(slots) * ceil_div(l.inter, kSlotUpTiles * kTile) * 256 < (int64_t(1) << 32));
         CHECK(ceil_div(ceil_div(l.hidden, kTile), 8) * 8 * tokens * 512 < (int64_t(1) << 32));
