@@ -773,7 +773,8 @@ template <bool BF16, int L, int G, int P, int MODE, int R, int U, int W, int NXM
 __global__ void __launch_bounds__(W * kWave, 2) ffn_stream(const FfnArgs a) {
     __shared__ u32x4 lds[stream_lds<G, P, R, W, NXMAX>()];
     const uint32_t strips = static_cast<uint32_t>((a.m + R * kTile - 1) / (R * kTile));
-    const uint32_t q = blockIdx.x / strips;   // block of tokens and split, or place in the list of experts and pass
+    // block of tokens and split, or place in the list of experts and pass
+    const uint32_t q = blockIdx.x / strips;
     const int64_t row0 = int64_t(blockIdx.x - q * strips) * (R * kTile);
     if constexpr (MODE == kLinear) {
         constexpr int32_t kTokens = NXMAX == 0 ? 1 : 2 * NXMAX;
@@ -848,17 +849,6 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// Word c (elements 8 c .. 8 c + 7) of a lane's 32 codes; v: the two block scales
-// of the 32 elements.
-template <bool BF16>
-__device__ __forceinline__ u32x4 decode_word(u32x4 q, int c, f32x2 v) {
-    if constexpr (BF16) return decode8(q[c], c < 2 ? v.x : v.y);
-    else {
-        const _Float16 s = static_cast<_Float16>(c < 2 ? v.x : v.y);
-        return __builtin_bit_cast(u32x4, decode8(q[c], f16x2{s, s}));
-    }
 }
 
 constexpr int kStageElems = 128;    // K elements of one stage: half of every lane's part of a window
