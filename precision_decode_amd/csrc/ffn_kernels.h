@@ -375,7 +375,10 @@ struct ScaleWord {
 };
 
 constexpr int kWinCodeBytes = 2048, kWinScaleBytes = 256;   // of a packed window of a tile
-constexpr int kAnyRange = 0x7FFFFFF0;   // descriptor range where every used offset is known to be valid
+// Descriptor range where every used offset is known to be valid: kReach as the
+// descriptor's unsigned 32 bits, so that kOutOfRange is the first offset past it.
+constexpr int kAnyRange = static_cast<int>(static_cast<uint32_t>(kReach));
+static_assert(kReach == int64_t(kOutOfRange), "offsets from kOutOfRange on read zeros");
 
 // The weights of one matrix as a workgroup reads them: R tiles of 16 rows from
 // row0, window by window (256 elements of K).  Lane i + 16 q holds, of row i of

@@ -24,6 +24,7 @@ constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTopk = 64;
 constexpr int64_t kMaxTokens = 65535;              // of a MoE call (a grid's second dimension)
 constexpr int64_t kMaxTiles = int64_t(1) << 24;    // workgroups of 256 threads: below 2^32 threads
+constexpr int64_t kReach = int64_t(1) << 31;       // bytes that a kernel's 32-bit offsets reach from a base
 constexpr size_t kWsAlign = 256;
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -113,6 +114,15 @@ constexpr TileKind kGatedTileKinds[] = {
     {1, 16, 8, 1, {210, 0, 0, 0}}, {1, 8, 8, 1, {111, 0, 0, 0}}, {1, 8, 4, 2, {70, 0, 0, 0}},
     {1, 4, 4, 2, {41, 72, 0, 0}},  {1, 2, 4, 2, {28, 45, 0, 0}}};
 constexpr int kNumTileKinds = 6, kNumGatedTileKinds = 5;
+// The rows of a workgroup's tokens lie up to kMaxK elements apart and are read by
+// offsets from the first one's: 256 tokens take the whole reach, to the last byte.
+template <int N>
+constexpr bool tokens_in_reach(const TileKind (&kinds)[N]) {
+    for (const TileKind &t : kinds)
+        if (t.tokens() * kMaxK * 2 > kReach) return false;
+    return true;
+}
+static_assert(tokens_in_reach(kTileKinds) && tokens_in_reach(kGatedTileKinds), "token offsets within the reach");
 // the stream kernel's, for up to 8 and up to 16 tokens, one and two matrices
 constexpr float kStreamUs[2][2][4] = {{{6, 8, 0, 0}, {8, 12, 0, 0}}, {{9, 11.5f, 0, 0}, {11, 18, 0, 0}}};
 constexpr int64_t kMaxStreamSplits = 64;
@@ -214,7 +224,7 @@ struct MoeWorkspace {
 };
 
 constexpr int kMaxPlanes = 3;
-constexpr int64_t kMaxStreamBytes = 0x7FFFFFF0;   // row offsets the stream kernel can form
+constexpr int64_t kMaxStreamBytes = kReach;       // of the rows that the stream kernel picks its tokens from
 
 // Most experts that can have slots.
 inline int64_t moe_groups(const nvfp4_moe_layer_t &l, int64_t tokens) {
