@@ -596,18 +596,34 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
 // of a window go through the wave's LDS slot, every lane quarter's 128 bytes 16
 // bytes further, so that the quarters' reads hit distinct banks.
 constexpr int kDotSlot = 4 * (8 + 1);   // 16-byte pieces of a plane
+// A block is summed before its scale is known to make its products smaller: 16
+// products of a bf16 value and a code reach 96 times the largest fp32 value, so
+// the codes are converted to 2^-7 times their value and the scales to 2^7 times
+// theirs, both exactly and at no cost.  A product of a bf16 value and a code so
+// converted is a multiple of 2^-141, and fp32 subnormals are kept by every step, so
+// nothing is lost below either.  fp16 values are at most 65504.
+constexpr float kDotDown = 0x1p-7f, kDotUp = 0x1p7f;
+template <bool BF16>
+__device__ __forceinline__ float dot_scale(uint32_t s) {
+    if constexpr (BF16) {
+        const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(s, kDotUp, false);
+        return v.x;
+    } else {
+        return e4m3x2_f32(s).x;
+    }
+}
 
 template <bool BF16>
 __device__ __forceinline__ float dot8(uint32_t q, u32x4 x, float s) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     if constexpr (BF16) {
-        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 0),
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, kDotDown, 0),
                                             __builtin_bit_cast(bf16x2, uint32_t(x.x)), s, false);
-        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 1),
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, kDotDown, 1),
                                             __builtin_bit_cast(bf16x2, uint32_t(x.y)), s, false);
-        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 2),
+        s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, kDotDown, 2),
                                             __builtin_bit_cast(bf16x2, uint32_t(x.z)), s, false);
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, 1.0f, 3),
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, kDotDown, 3),
                                                __builtin_bit_cast(bf16x2, uint32_t(x.w)), s, false);
     } else {
         s = __builtin_amdgcn_fdot2(e2m1x2_f16<0>(q), halves(x.x), s, false);
@@ -676,7 +692,7 @@ __device__ __forceinline__ void dot_sums(const FfnArgs &a, int expert, int64_t r
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int p = 0; p < P; ++p) s = dot8<BF16>(wq[u][g][r][b / 2][2 * (b & 1) + c], xv[p][c], s);
-                    acc[g][r] = __builtin_fmaf(e4m3x2_f32(ws[u][g][r].value() >> (8 * b)).x, s, acc[g][r]);
+                    acc[g][r] = __builtin_fmaf(dot_scale<BF16>(ws[u][g][r].value() >> (8 * b)), s, acc[g][r]);
                 }
         }
     };

@@ -1,9 +1,12 @@
 """The feed-forward operators on the GPU at the limits of their rules: the
 longest rows and the largest values."""
+import numpy as np
 import pytest
 import torch
 
 import precision_decode_amd as pd
+from ffn_util import TYPES, assert_close, rounded, weight
+from oracle import ffn
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +34,68 @@ def test_linear_longest_rows_keep_their_last_elements():
     x[n - 1, k - 1] = float("nan")
     y = pd.linear(x, codes, scales, m, out_dtype=torch.float32)
     assert bool(y[n - 1].isnan().all()) and bool((y[:n - 1] == 16.0).all())
+
+
+def one_call(rng, n, k, x, layout, gated, xv, codes, scales):
+    dc, ds = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    if layout == "packed":
+        dc, ds = pd.pack_weight(dc, ds)
+    got = pd.linear(torch.from_numpy(xv).to(TYPES[x]).cuda(), dc, ds, codes.shape[1], gated=gated,
+                    packed=layout == "packed", out_dtype=torch.float32)
+    want, err = ffn.linear(xv, codes, scales, None, None, None, "none", gated)
+    assert_close(got, want, err, "f32", f"n={n} k={k} {x} {layout} gated={gated}")
+    return got
+
+
+@pytest.mark.parametrize("layout,k", [("row", 64), ("row", 80), ("row", 320), ("packed", 64), ("packed", 320)])
+@pytest.mark.parametrize("n", [1, 2, 9])
+def test_linear_large_inputs_times_small_scales_stay_finite(n, layout, k):
+    """Inputs near the largest bf16 value and scales of 2^-9: every product is below 2^122,
+    so the sums stay finite, though those of 16 inputs times codes would not."""
+    rng = np.random.default_rng(51 + k)
+    codes, scales = weight(rng, 1, 40, k, np.array([0x01, 0x81], np.uint8))
+    xv = rounded(rng.uniform(0.3, 1.0, (n, k)) * 3.3e38 * rng.choice([-1, 1], (n, k)), "bf16")
+    scales[0, 3], codes[0, 3] = 0x01, 0x77        # 6 times 2^-9 everywhere
+    xv[0] = np.abs(xv[0]) * 2.0 ** -2             # and all products of a sign
+    assert bool(one_call(rng, n, k, "bf16", layout, False, xv, codes, scales).isfinite().all())
+
+
+@pytest.mark.parametrize("layout", ["row", "packed"])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 2, 9])
+def test_linear_small_inputs_keep_their_bits(n, x, layout):
+    """Subnormal inputs and the smallest scales: fp32 holds every product."""
+    rng = np.random.default_rng(52)
+    codes, scales = weight(rng, 1, 40, 192, np.array([0x01, 0x02, 0x09, 0x81], np.uint8))
+    tiny = torch.finfo(TYPES[x]).smallest_normal
+    xv = rounded(rng.uniform(-2.0, 2.0, (n, 192)) * tiny, x)
+    dc, ds = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    if layout == "packed":
+        dc, ds = pd.pack_weight(dc, ds)
+    up = 2.0 ** 120 if x == "bf16" else 1.0
+    got = pd.linear(torch.from_numpy(xv).to(TYPES[x]).cuda(), dc, ds, 40, packed=layout == "packed",
+                    alpha=torch.tensor([up], device="cuda"), out_dtype=torch.float32)
+    want, err = ffn.linear(xv, codes, scales, np.array([up]), None, None, "none", False)
+    # besides, an addition in fp32's subnormals is off by up to half of 2^-149
+    assert_close(got, want, err + 192 * 2.0 ** -150 * up, "f32", f"n={n} {x} {layout}")
+
+
+@pytest.mark.parametrize("layout,k", [("row", 320), ("row", 336), ("packed", 320)])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_special_values_of_one_token(x, gated, layout, k):
+    """One token has a kernel of its own: NaN scales stay in their rows, an infinite input
+    gives infinities and NaN by the weights' signs and zeros."""
+    rng = np.random.default_rng(53)
+    codes, scales = weight(rng, 2 if gated else 1, 40, k)
+    scales[0, 5, 3] = 0x7F
+    codes[0, 7], scales[0, 9] = 0, 0
+    xv = rounded(rng.standard_normal((1, k)), x)
+    got = one_call(rng, 1, k, x, layout, gated, xv, codes, scales)
+    assert bool(got[:, 5].isnan().all()) and int(got.isnan().sum()) == 1
+    xv[0, 100] = np.inf
+    got = one_call(rng, 1, k, x, layout, gated, xv, codes, scales)
+    assert bool(got[:, [5, 7, 9]].isnan().all())
+    xv[0] = 0.0
+    got = one_call(rng, 1, k, x, layout, gated, xv, codes, scales)
+    assert bool((got[0, [0, 1, 7, 9]] == 0).all())
