@@ -40,9 +40,12 @@
  *   h_j   = f( alpha13[e_j][0] * gate_{e_j} X[t] ) * ( alpha13[e_j][1] * up_{e_j} X[t] )
  *   Y[t]  = y( residual[t] + sum_j w[j] * alpha2[e_j] * down_{e_j} h_j )
  *
- * The scores are computed in fp64, so experts are chosen as the exact scores
- * say; h is kept with 16 significand bits for a 16-bit Y and with 24 for an
- * fp32 Y; all other sums are fp32.
+ * Logits and scores are computed in fp64.  Without a route_bias experts are
+ * ordered by their logits, so they are chosen as the exact scores say, also where
+ * these round to the same number; with one, keys that fp64 does not tell apart
+ * (sigmoids of logits from about 37 on are all 1) count as equal.  h is kept with
+ * 16 significand bits for a 16-bit Y and with 24 for an fp32 Y; all other sums are
+ * fp32.
  *
  * All data pointers are DEVICE pointers owned by the caller (the
  * nvfp4_moe_layer_t itself is host memory, read during the call only); the

@@ -98,7 +98,8 @@ def linear(x, codes, scales, alpha=None, bias=None, residual=None, act="none", g
 
 def route(x, router, topk, route_bias=None, scoring="softmax", renormalize=True, scale=1.0):
     """(experts (tokens, topk), weights (tokens, topk)): the lowest index first
-    among equal keys, NaN keys last."""
+    among equal keys, NaN keys last.  Without a route_bias the keys are the logits,
+    which order the experts as the exact scores do."""
     z = np.asarray(x, np.float64) @ np.asarray(router, np.float64).T
     with np.errstate(invalid="ignore", over="ignore"):
         if scoring == "softmax":
@@ -106,8 +107,8 @@ def route(x, router, topk, route_bias=None, scoring="softmax", renormalize=True,
             s = s / s.sum(axis=1, keepdims=True)
         else:
             s = 1.0 / (1.0 + np.exp(-z))
-        key = s if route_bias is None else s + np.asarray(route_bias, np.float64)
-    key = np.where(np.isnan(key), -np.inf, key)
+        key = z if route_bias is None else s + np.asarray(route_bias, np.float64)
+    key = np.where(np.isnan(key), -np.inf, np.maximum(key, -np.finfo(np.float64).max))
     order = np.argsort(-key, axis=1, kind="stable")[:, :topk]
     w = np.take_along_axis(s, order, axis=1)
     if renormalize:

@@ -6,6 +6,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cstddef>
 #include <cstdint>
 #include <type_traits>
@@ -1362,10 +1363,13 @@ __device__ __forceinline__ double logit(const RouteArgs &a, int64_t t, int e) {
     }
     return v;
 }
-// The key experts are chosen by; a NaN counts as the least.
-__device__ __forceinline__ double choice_key(const RouteArgs &a, int e, double score) {
-    const double key = score + (a.route_bias ? double(a.route_bias[e]) : 0.0);
-    return key == key ? key : -INFINITY;
+// The key experts are chosen by; a NaN counts as the least, below -infinity.
+// Without a route_bias it is the logit z: both scorings grow with it, and where
+// scores saturate (sigmoids from z of 37 on are all 1 in fp64) it still tells the
+// experts apart.
+__device__ __forceinline__ double choice_key(const RouteArgs &a, int e, double z, double score) {
+    const double key = a.route_bias ? score + double(a.route_bias[e]) : z;
+    return key == key ? fmax(key, -DBL_MAX) : -INFINITY;
 }
 __device__ __forceinline__ float routed_weight(const RouteArgs &a, double score, double chosen) {
     return static_cast<float>((a.renormalize ? score / chosen : score) * double(a.routed_scale));
@@ -1381,7 +1385,7 @@ __device__ __forceinline__ void choose_token(const RouteArgs &a, int64_t t, doub
     const bool softmax = a.scoring == NVFP4_SCORE_SOFTMAX;
     double top = -INFINITY, sum = 0.0;
     for (int e = lane; e < experts; e += kWave) {
-        score[e] = logit(a, t, e);
+        score[e] = keys[e] = logit(a, t, e);
         top = fmax(top, score[e]);
     }
     if (softmax) top = wave_max64(top);
@@ -1389,7 +1393,7 @@ __device__ __forceinline__ void choose_token(const RouteArgs &a, int64_t t, doub
     if (softmax) sum = wave_sum64(sum);
     for (int e = lane; e < experts; e += kWave) {
         score[e] = softmax ? score[e] / sum : 1.0 / (1.0 + score[e]);
-        keys[e] = choice_key(a, e, score[e]);
+        keys[e] = choice_key(a, e, keys[e], score[e]);
     }
     wave_lds_fence();
     double chosen = 0.0;
@@ -1579,6 +1583,7 @@ __device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j,
     }
     for (int e = thread; e < experts; e += THREADS) {
         if (a.splits > 0) score[e] = logit(a, t, e);
+        keys[e] = score[e];
         rank[e] = 0;
         top = fmax(top, score[e]);
     }
@@ -1600,7 +1605,7 @@ __device__ __forceinline__ int choose_slot(const RouteArgs &a, int64_t t, int j,
     }
     for (int e = thread; e < experts; e += THREADS) {
         score[e] = softmax ? score[e] / sum : 1.0 / (1.0 + score[e]);
-        keys[e] = choice_key(a, e, score[e]);
+        keys[e] = choice_key(a, e, keys[e], score[e]);
     }
     __syncthreads();
     // the waves share the comparisons
