@@ -256,6 +256,21 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _enqueue(call, args, device, stream, where):
+    """Makes the C call with the GPU that holds the tensors current, on ``stream``."""
+    import torch
+
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+        raise ValueError(f"stream is on GPU {stream.device_index}, the tensors on GPU {device}")
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == device:
+        status = call(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, handle)
+    _check(status, where)
+
+
 def _check(status: int, where: str):
     if status != NVFP4_GEMV_OK:
         raise Nvfp4GemvError(status, where)
@@ -603,22 +618,25 @@ def _named(table, name, what):
     return table[name]
 
 
+_FLOAT_TYPES = {}   # torch.dtype -> NVFP4_OUT_*, filled on first use: torch is not imported before
+
+
 def _float_type(dtype, what, f32=False):
-    import torch
+    if not _FLOAT_TYPES:
+        import torch
 
-    if dtype is torch.bfloat16:
-        return NVFP4_OUT_BF16
-    if dtype is torch.float16:
-        return NVFP4_OUT_F16
-    if f32 and dtype is torch.float32:
-        return NVFP4_OUT_F32
-    raise ValueError(f"{what} must be bfloat16{', float16 or float32' if f32 else ' or float16'}")
+        _FLOAT_TYPES.update({torch.bfloat16: NVFP4_OUT_BF16, torch.float16: NVFP4_OUT_F16,
+                             torch.float32: NVFP4_OUT_F32})
+    code = _FLOAT_TYPES.get(dtype)
+    if code is None or (code == NVFP4_OUT_F32 and not f32):
+        raise ValueError(f"{what} must be bfloat16{', float16 or float32' if f32 else ' or float16'}")
+    return code
 
 
-def _rows(t, what, shape, dtype=None):
-    """Element stride of the rows of a 2-D device tensor whose columns are contiguous."""
-    if t.shape != shape or not t.is_cuda or (dtype is not None and t.dtype is not dtype):
-        raise ValueError(f"{what} must be a device tensor of shape {shape}"
+def _rows(t, what, shape, device, dtype=None):
+    """Element stride of the rows of a 2-D tensor on that GPU whose columns are contiguous."""
+    if t.shape != shape or t.get_device() != device or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{what} must be a tensor on GPU {device} of shape {shape}"
                          f"{'' if dtype is None else f' and {dtype}'}")
     rows, cols = t.stride()
     if cols != 1 and shape[1] > 1:
@@ -630,24 +648,24 @@ def _rows(t, what, shape, dtype=None):
     return ld
 
 
-def _floats(t, count, what):
+def _floats(t, count, what, device):
     if t is None:
         return
     import torch
 
-    if t.dtype is not torch.float32 or t.numel() != count or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what} must be a contiguous float32 device tensor of {count} values")
+    if t.dtype is not torch.float32 or t.numel() != count or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous float32 tensor of {count} values on GPU {device}")
 
 
-def _weight(codes, scales, groups, rows, k, packed, what):
+def _weight(codes, scales, groups, rows, k, packed, what, device):
     """Checks codes and scales of ``groups`` matrices of rows x k in either layout."""
     import torch
 
     # packed: whole tiles of 16 rows and windows of 256 elements, as nvfp4_mma_packed_sizes says
     count = groups * (-(-rows // 16) * 16) * (-(-k // 256) * 256) if packed else groups * rows * k
     for t, want, name in ((codes, count // 2, "codes"), (scales, count // 16, "scales")):
-        if t.dtype is not torch.uint8 or t.numel() != want or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError(f"{what} {name} must be a contiguous uint8 device tensor of {want} bytes")
+        if t.dtype is not torch.uint8 or t.numel() != want or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"{what} {name} must be a contiguous uint8 tensor of {want} bytes on GPU {device}")
 
 
 def _output(out, out_dtype, n, m, x, residual, stream):
@@ -655,6 +673,7 @@ def _output(out, out_dtype, n, m, x, residual, stream):
     type code and row strides of it and of the residual."""
     import torch
 
+    device = x.get_device()
     if out is None:
         dtype = x.dtype if out_dtype is None else out_dtype
         y_type = _float_type(dtype, "out_dtype", f32=True)
@@ -668,8 +687,8 @@ def _output(out, out_dtype, n, m, x, residual, stream):
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out_dtype differs from out's type")
         y_type = _float_type(out.dtype, "out", f32=True)
-        ldy = _rows(out, "out", (n, m))
-    ldr = 0 if residual is None else _rows(residual, "residual", (n, m), out.dtype)
+        ldy = _rows(out, "out", (n, m), device)
+    ldr = 0 if residual is None else _rows(residual, "residual", (n, m), device, out.dtype)
     return out, y_type, ldy, ldr
 
 
@@ -688,30 +707,36 @@ def linear(x, codes, scales, m, alpha=None, bias=None, residual=None, activation
     :func:`pack_weight` returns for them; alpha float32 of 1 (gated 2) values,
     bias float32 of m (gated 2 m); residual (n, m) of the output's type, which
     may be ``out`` itself.  Returns (n, m) of ``out_dtype`` (default x's type).
+    All tensors are on one GPU, which need not be the current one; the default
+    stream is that GPU's current stream.
     """
     if x.dim() != 2:
         raise ValueError("x must be (n, k)")
     n, k = x.shape
     x_type = _float_type(x.dtype, "x")
-    ldx = _rows(x, "x", (n, k))
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("x must be on a GPU")
+    ldx = _rows(x, "x", (n, k), device)
     groups = 2 if gated else 1
-    _weight(codes, scales, groups, m, k, packed, "weight")
-    _floats(alpha, groups, "alpha")
-    _floats(bias, groups * m, "bias")
+    _weight(codes, scales, groups, m, k, packed, "weight", device)
+    _floats(alpha, groups, "alpha", device)
+    _floats(bias, groups * m, "bias", device)
     act = _named(_ACTIVATIONS, activation, "activation") | (NVFP4_ACT_GATED if gated else 0)
     out, y_type, ldy, ldr = _output(out, out_dtype, n, m, x, residual, stream)
     if n > 0:
-        _check(load().nvfp4_linear_launch(
+        _enqueue(load().nvfp4_linear_launch, (
             x.data_ptr(), x_type, ldx, codes.data_ptr(), scales.data_ptr(),
             NVFP4_W_PACKED if packed else NVFP4_W_ROW_MAJOR, _address(alpha), _address(bias),
-            _address(residual), ldr, out.data_ptr(), y_type, ldy, n, m, k, act, _stream(stream)),
+            _address(residual), ldr, out.data_ptr(), y_type, ldy, n, m, k, act), device, stream,
             "nvfp4_linear_launch")
     return out
 
 
 class MoeLayer:
     """What stays the same from call to call of one mixture-of-experts layer
-    (``nvfp4_moe_layer_t``); keeps the tensors it names alive.
+    (``nvfp4_moe_layer_t``); keeps the tensors it names alive, which are all on
+    one GPU.
 
     router (experts, hidden) bfloat16 or float16; codes13 / scales13 the gate
     and up matrices, (2 experts, inter, .) with expert e's gate at 2 e; codes2 /
@@ -726,11 +751,12 @@ class MoeLayer:
         if router.dim() != 2 or not router.is_cuda or not router.is_contiguous():
             raise ValueError("router must be a contiguous (experts, hidden) device tensor")
         experts, hidden = router.shape
-        _weight(codes13, scales13, 2 * experts, inter, hidden, packed, "gate and up")
-        _weight(codes2, scales2, experts, hidden, inter, packed, "down")
-        _floats(alpha13, 2 * experts, "alpha13")
-        _floats(alpha2, experts, "alpha2")
-        _floats(route_bias, experts, "route_bias")
+        self.device = router.get_device()
+        _weight(codes13, scales13, 2 * experts, inter, hidden, packed, "gate and up", self.device)
+        _weight(codes2, scales2, experts, hidden, inter, packed, "down", self.device)
+        _floats(alpha13, 2 * experts, "alpha13", self.device)
+        _floats(alpha2, experts, "alpha2", self.device)
+        _floats(route_bias, experts, "route_bias", self.device)
         self.tensors = (router, codes13, scales13, codes2, scales2, alpha13, alpha2, route_bias)
         self.dtype, self.hidden = router.dtype, hidden
         self.struct = MoeLayerStruct(
@@ -753,14 +779,15 @@ def moe_layer(x, layer, residual=None, out=None, out_dtype=None, stream=None):
     """Tensor-level mixture-of-experts layer: x (tokens, hidden) of the
     router's type with any row stride, ``layer`` a :class:`MoeLayer`, residual
     (tokens, hidden) of the output's type, which may be ``out`` itself.  Returns
-    (tokens, hidden) of ``out_dtype`` (default x's type)."""
+    (tokens, hidden) of ``out_dtype`` (default x's type).  GPU and stream as in
+    :func:`linear`."""
     if x.dim() != 2 or x.shape[1] != layer.hidden:
         raise ValueError(f"x must be (tokens, {layer.hidden})")
     n = x.shape[0]
-    ldx = _rows(x, "x", (n, layer.hidden), layer.dtype)
+    ldx = _rows(x, "x", (n, layer.hidden), layer.device, layer.dtype)
     out, y_type, ldy, ldr = _output(out, out_dtype, n, layer.hidden, x, residual, stream)
     if n > 0:
-        _check(load().nvfp4_moe_layer_launch(layer.reference, x.data_ptr(), ldx, _address(residual), ldr,
-                                             out.data_ptr(), y_type, ldy, n, _stream(stream)),
-               "nvfp4_moe_layer_launch")
+        _enqueue(load().nvfp4_moe_layer_launch,
+                 (layer.reference, x.data_ptr(), ldx, _address(residual), ldr, out.data_ptr(), y_type, ldy, n),
+                 layer.device, stream, "nvfp4_moe_layer_launch")
     return out
