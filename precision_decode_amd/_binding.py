@@ -677,11 +677,13 @@ def _output(out, out_dtype, n, m, x, residual, stream):
     if out is None:
         dtype = x.dtype if out_dtype is None else out_dtype
         y_type = _float_type(dtype, "out_dtype", f32=True)
-        if isinstance(stream, torch.cuda.Stream):
-            with torch.cuda.stream(stream):
-                out = torch.empty((n, m), dtype=dtype, device=x.device)
-        else:
+        if stream is None:
             out = torch.empty((n, m), dtype=dtype, device=x.device)
+        else:
+            # memory of another stream's tensors may still be in use by work queued there
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                   torch.cuda.ExternalStream(stream, device=device)):
+                out = torch.empty((n, m), dtype=dtype, device=x.device)
         ldy = m
     else:
         if out_dtype is not None and out.dtype != out_dtype:

@@ -45,6 +45,19 @@ class Runtime:
                     return 0
                 return call
 
+        class On:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                runtime.on.append(self.stream)
+
+            def __exit__(self, *_):
+                pass
+
+        self.on = []
+        monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
         monkeypatch.setattr(torch.cuda, "device", Current)
         monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.current, raising=False)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
@@ -104,3 +117,15 @@ def test_calls_are_made_on_the_tensors_gpu(fake, monkeypatch, gpu):
     assert pd.moe_layer(x, layer, out=fake((2, 64), BF16, gpu), stream=7).get_device() == gpu
     assert runtime.calls == [("nvfp4_linear_launch", gpu, 100 + gpu), ("nvfp4_moe_layer_launch", gpu, 7)]
     assert runtime.current == 0
+
+
+def test_outputs_are_allocated_on_a_stream_given_as_a_handle(fake, monkeypatch):
+    runtime = Runtime(monkeypatch)
+    t = linear_tensors(fake, 0)
+    del t["out"]
+    pd.linear(m=8, stream=0x7000, **t)
+    layer = pd.MoeLayer(inter=32, topk=1, **layer_tensors(fake, 0))
+    pd.moe_layer(fake((2, 64), BF16, 0), layer, stream=0x7040)
+    pd.linear(m=8, **t)
+    assert runtime.on == [(0x7000, 0), (0x7040, 0)]
+    assert [c[2] for c in runtime.calls] == [0x7000, 0x7040, 100]
