@@ -10,6 +10,7 @@ All arithmetic happens in the HIP kernels; nothing here falls back to the CPU.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -256,17 +257,24 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _enqueue(call, args, device, stream, where):
-    """Makes the C call with the GPU that holds the tensors current, on ``stream``."""
+def _current(device, stream):
+    """Context with that GPU current, for a call on ``stream``."""
     import torch
 
     if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
         raise ValueError(f"stream is on GPU {stream.device_index}, the tensors on GPU {device}")
+    return contextlib.nullcontext() if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
+
+
+def _enqueue(call, args, device, stream, where):
+    """Makes the C call with the GPU that holds the tensors current, on ``stream``."""
+    import torch
+
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if torch._C._cuda_getDevice() == device:
+    if stream is None and torch._C._cuda_getDevice() == device:
         status = call(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with _current(device, stream):
             status = call(*args, handle)
     _check(status, where)
 
@@ -503,13 +511,15 @@ def quantize_activation(x, global_scale, rule=NVFP4_ROUND_HALF_STEP, stream=None
     if x.dim() != 2 or x.element_size() != 2 or not x.is_contiguous() or not x.is_cuda:
         raise ValueError("x must be a contiguous 2-D 16-bit device tensor (bf16 bits)")
     rows, d = x.shape
-    if global_scale.dtype != torch.float32 or not global_scale.is_cuda or \
+    device = x.get_device()
+    if global_scale.dtype != torch.float32 or global_scale.get_device() != device or \
             global_scale.numel() not in (1, rows):
-        raise ValueError("global_scale must be a float32 device tensor of 1 or rows values")
+        raise ValueError(f"global_scale must be a float32 tensor of 1 or rows values on GPU {device}")
     per_row = 1 if (global_scale.numel() == rows and rows > 1) else 0
     q = torch.empty((rows, d // 2), dtype=torch.uint8, device=x.device)
     sf = torch.empty((rows, d // 16), dtype=torch.uint8, device=x.device)
-    nvfp4_quantize_activation(x, global_scale, per_row, q, sf, rows, d, rule, stream)
+    with _current(device, stream):
+        nvfp4_quantize_activation(x, global_scale, per_row, q, sf, rows, d, rule, stream)
     return q, sf
 
 
@@ -527,18 +537,22 @@ def gemv(A_packed, sfA, x_packed, sfx, alpha=None, out=None, stream=None):
     k = 2 * half
     want = {"A_packed": (A_packed, (l, m, half)), "sfA": (sfA, (l, m, k // 16)),
             "x_packed": (x_packed, (l, half)), "sfx": (sfx, (l, k // 16))}
+    device = A_packed.get_device()
     for name, (t, shape) in want.items():
         if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
             raise ValueError(f"{name} must be a contiguous uint8 device tensor of shape {shape}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} must be on GPU {device}, as A_packed")
     if alpha is not None and (alpha.dtype != torch.float32 or tuple(alpha.shape) != (l,)
-                              or not alpha.is_cuda):
-        raise ValueError("alpha must be a float32 device tensor of shape (l,)")
+                              or alpha.get_device() != device):
+        raise ValueError(f"alpha must be a float32 tensor of shape (l,) on GPU {device}")
     if out is None:
         out = torch.empty((l, m), dtype=torch.uint16, device=A_packed.device)
     elif (out.dtype not in (torch.uint16, torch.float16, torch.int16) or tuple(out.shape) != (l, m)
-          or not out.is_contiguous() or not out.is_cuda):
-        raise ValueError("out must be a contiguous 16-bit device tensor of shape (l, m)")
-    nvfp4_gemv_launch(A_packed, sfA, x_packed, sfx, alpha, out, l, m, k, stream)
+          or not out.is_contiguous() or out.get_device() != device):
+        raise ValueError(f"out must be a contiguous 16-bit tensor of shape (l, m) on GPU {device}")
+    with _current(device, stream):
+        nvfp4_gemv_launch(A_packed, sfA, x_packed, sfx, alpha, out, l, m, k, stream)
     return out
 
 
@@ -559,10 +573,14 @@ def pack_weight(W, sW, stream=None):
     for name, t, shape in (("W", W, (groups, rows, half)), ("sW", sW, (groups, rows, k // 16))):
         if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
             raise ValueError(f"{name} must be a contiguous uint8 device tensor of shape {shape}")
+    device = W.get_device()
+    if sW.get_device() != device:
+        raise ValueError(f"sW must be on GPU {device}, as W")
     cb, sb = nvfp4_mma_packed_sizes(groups, rows, k)
     codes = torch.empty(cb, dtype=torch.uint8, device=W.device)
     scales = torch.empty(sb, dtype=torch.uint8, device=W.device)
-    nvfp4_mma_pack_weight(W, sW, groups, rows, k, codes, scales, stream)
+    with _current(device, stream):
+        nvfp4_mma_pack_weight(W, sW, groups, rows, k, codes, scales, stream)
     return codes, scales
 
 
