@@ -266,6 +266,18 @@ def _current(device, stream):
     return contextlib.nullcontext() if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
 
 
+def _allocate(shape, dtype, device, stream):
+    """Tensor allocated on the stream that writes it: memory of another stream's tensors
+    may still be in use by work queued there."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                           torch.cuda.ExternalStream(stream, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _enqueue(call, args, device, stream, where):
     """Makes the C call with the GPU that holds the tensors current, on ``stream``."""
     import torch
@@ -516,8 +528,8 @@ def quantize_activation(x, global_scale, rule=NVFP4_ROUND_HALF_STEP, stream=None
             global_scale.numel() not in (1, rows):
         raise ValueError(f"global_scale must be a float32 tensor of 1 or rows values on GPU {device}")
     per_row = 1 if (global_scale.numel() == rows and rows > 1) else 0
-    q = torch.empty((rows, d // 2), dtype=torch.uint8, device=x.device)
-    sf = torch.empty((rows, d // 16), dtype=torch.uint8, device=x.device)
+    q = _allocate((rows, d // 2), torch.uint8, x.device, stream)
+    sf = _allocate((rows, d // 16), torch.uint8, x.device, stream)
     with _current(device, stream):
         nvfp4_quantize_activation(x, global_scale, per_row, q, sf, rows, d, rule, stream)
     return q, sf
@@ -547,7 +559,7 @@ def gemv(A_packed, sfA, x_packed, sfx, alpha=None, out=None, stream=None):
                               or alpha.get_device() != device):
         raise ValueError(f"alpha must be a float32 tensor of shape (l,) on GPU {device}")
     if out is None:
-        out = torch.empty((l, m), dtype=torch.uint16, device=A_packed.device)
+        out = _allocate((l, m), torch.uint16, A_packed.device, stream)
     elif (out.dtype not in (torch.uint16, torch.float16, torch.int16) or tuple(out.shape) != (l, m)
           or not out.is_contiguous() or out.get_device() != device):
         raise ValueError(f"out must be a contiguous 16-bit tensor of shape (l, m) on GPU {device}")
@@ -577,8 +589,8 @@ def pack_weight(W, sW, stream=None):
     if sW.get_device() != device:
         raise ValueError(f"sW must be on GPU {device}, as W")
     cb, sb = nvfp4_mma_packed_sizes(groups, rows, k)
-    codes = torch.empty(cb, dtype=torch.uint8, device=W.device)
-    scales = torch.empty(sb, dtype=torch.uint8, device=W.device)
+    codes = _allocate(cb, torch.uint8, W.device, stream)
+    scales = _allocate(sb, torch.uint8, W.device, stream)
     with _current(device, stream):
         nvfp4_mma_pack_weight(W, sW, groups, rows, k, codes, scales, stream)
     return codes, scales
@@ -689,19 +701,11 @@ def _weight(codes, scales, groups, rows, k, packed, what, device):
 def _output(out, out_dtype, n, m, x, residual, stream):
     """Output tensor (allocated on the stream that writes it if not given), its
     type code and row strides of it and of the residual."""
-    import torch
-
     device = x.get_device()
     if out is None:
         dtype = x.dtype if out_dtype is None else out_dtype
         y_type = _float_type(dtype, "out_dtype", f32=True)
-        if stream is None:
-            out = torch.empty((n, m), dtype=dtype, device=x.device)
-        else:
-            # memory of another stream's tensors may still be in use by work queued there
-            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                   torch.cuda.ExternalStream(stream, device=device)):
-                out = torch.empty((n, m), dtype=dtype, device=x.device)
+        out = _allocate((n, m), dtype, x.device, stream)
         ldy = m
     else:
         if out_dtype is not None and out.dtype != out_dtype:

@@ -57,7 +57,7 @@ class Runtime:
 
         self.on = []
         monkeypatch.setattr(torch.cuda, "stream", On)
-        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, torch.device(device).index))
         monkeypatch.setattr(torch.cuda, "device", Current)
         monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: self.current, raising=False)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
@@ -127,5 +127,5 @@ def test_outputs_are_allocated_on_a_stream_given_as_a_handle(fake, monkeypatch):
     layer = pd.MoeLayer(inter=32, topk=1, **layer_tensors(fake, 0))
     pd.moe_layer(fake((2, 64), BF16, 0), layer, stream=0x7040)
     pd.linear(m=8, **t)
-    assert runtime.on == [(0x7000, 0), (0x7040, 0)]
+    assert runtime.on == [(0x7000, 0), (0x7040, 0)]   # handle and GPU
     assert [c[2] for c in runtime.calls] == [0x7000, 0x7040, 100]

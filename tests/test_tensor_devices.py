@@ -49,3 +49,12 @@ def test_calls_are_made_on_the_tensors_gpu(fake, runtime, gpu):  # noqa: F811
     assert calls == [("nvfp4_gemv_launch", gpu, 100 + gpu), ("nvfp4_quantize_activation", gpu, 100 + gpu),
                      ("nvfp4_mma_pack_weight", gpu, 7)]
     assert runtime.current == 0
+
+
+def test_outputs_are_allocated_on_a_stream_given_as_a_handle(fake, runtime):  # noqa: F811
+    t = gemv_tensors(fake, 0)
+    del t["out"]
+    pd.gemv(stream=0x7000, **t)
+    pd.quantize_activation(fake((2, 64), BF16, 0), fake((1,), F32, 0), stream=0x7040)
+    pd.pack_weight(fake((8, 32), U8, 0), fake((8, 4), U8, 0), stream=0x7080)
+    assert runtime.on == [(0x7000, 0), (0x7040, 0), (0x7040, 0), (0x7080, 0), (0x7080, 0)]
