@@ -29,7 +29,10 @@
  *   bias     float [m] (gated [2 m]) or NULL (0)
  *   residual y_type, row t at residual + t * ldr elements, or NULL (0).  May be
  *            Y itself (same address and ldr == ldy): the update is in place
- *   Y        y_type, row t at Y + t * ldy elements; only its m elements are written
+ *   Y        y_type, row t at Y + t * ldy elements; only its m elements are written.
+ *            No input may share an element with it (but the residual, as above):
+ *            rows of X or the residual may lie between Y's where the strides are
+ *            the same number of bytes, as column ranges of one matrix do
  *
  * MoE layer.  For token t, with z = X[t] Wr^T over the experts:
  *

@@ -63,6 +63,24 @@ inline bool span_bytes(int64_t rows, int64_t cols, int64_t ld, int bytes, int64_
     return true;
 }
 
+// Rows of `width` bytes, `stride` bytes apart, that take `span` bytes from `at` on.
+struct RowSpan {
+    uintptr_t at;
+    int64_t span, width, stride;
+};
+
+// Whether an element of one may be an element of the other.  Rows of the same
+// stride may lie between each other: column ranges of one matrix.
+inline bool rows_overlap(const RowSpan &a, const RowSpan &b) {
+    if (a.span <= 0 || b.span <= 0 || a.at >= b.at + static_cast<uintptr_t>(b.span) ||
+        b.at >= a.at + static_cast<uintptr_t>(a.span))
+        return false;
+    if (a.stride != b.stride || a.width > a.stride || b.width > b.stride) return true;
+    const uintptr_t stride = static_cast<uintptr_t>(a.stride);
+    const uintptr_t apart = b.at >= a.at ? (b.at - a.at) % stride : (stride - (a.at - b.at) % stride) % stride;
+    return apart < static_cast<uintptr_t>(a.width) || apart + static_cast<uintptr_t>(b.width) > stride;
+}
+
 inline int check_linear_shape(int64_t n, int64_t m, int64_t k, int32_t w_layout) {
     if (n < 0 || m < 1 || !k_ok(k, w_layout) || n >= (int64_t(1) << 31) || m >= (int64_t(1) << 31))
         return NVFP4_GEMV_ERR_BAD_SHAPE;

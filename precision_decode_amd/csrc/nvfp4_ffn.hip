@@ -45,6 +45,10 @@ bool overlaps(Span a, Span b) {
     return x < y + static_cast<uintptr_t>(b.n) && y < x + static_cast<uintptr_t>(a.n);
 }
 
+RowSpan rows_at(const void *p, int64_t cols, int64_t ld, int bytes, int64_t span) {
+    return {reinterpret_cast<uintptr_t>(p), p ? span : 0, cols * bytes, ld * bytes};
+}
+
 int run(const void *fn, dim3 grid, int threads, void **args, hipStream_t stream) {
     return hipLaunchKernel(fn, grid, dim3(threads), args, 0, stream) == hipSuccess ? NVFP4_GEMV_OK
                                                                                   : NVFP4_GEMV_ERR_LAUNCH;
@@ -108,10 +112,11 @@ int check_linear(const LinearCall &c) {
         (c.residual && !span_bytes(c.n, c.m, c.ldr, yb, &rs)))
         return NVFP4_GEMV_ERR_BAD_SHAPE;
     const Span y{c.Y, ys};
+    const RowSpan yr = rows_at(c.Y, c.m, c.ldy, yb, ys);
     const bool in_place = c.residual == c.Y && c.ldr == c.ldy;
-    if (overlaps(y, {c.X, xs}) || overlaps(y, {c.W, wb}) || overlaps(y, {c.sfW, sb}) ||
+    if (rows_overlap(yr, rows_at(c.X, c.k, c.ldx, 2, xs)) || overlaps(y, {c.W, wb}) || overlaps(y, {c.sfW, sb}) ||
         overlaps(y, {c.alpha, mats * 4}) || overlaps(y, {c.bias, mats * c.m * 4}) ||
-        (!in_place && overlaps(y, {c.residual, rs})))
+        (!in_place && rows_overlap(yr, rows_at(c.residual, c.m, c.ldr, yb, rs))))
         return NVFP4_GEMV_ERR_ALIAS;
     return NVFP4_GEMV_OK;
 }
@@ -263,12 +268,13 @@ int check_moe(const MoeCall &c) {
         (c.residual && !span_bytes(c.tokens, l.hidden, c.ldr, yb, &rs)))
         return NVFP4_GEMV_ERR_BAD_SHAPE;
     const Span y{c.Y, ys};
+    const RowSpan yr = rows_at(c.Y, l.hidden, c.ldy, yb, ys);
     const bool in_place = c.residual == c.Y && c.ldr == c.ldy;
-    if (overlaps(y, {c.X, xs}) || overlaps(y, {l.router, l.experts * l.hidden * 2}) ||
+    if (rows_overlap(yr, rows_at(c.X, l.hidden, c.ldx, 2, xs)) || overlaps(y, {l.router, l.experts * l.hidden * 2}) ||
         overlaps(y, {l.route_bias, l.experts * 4}) || overlaps(y, {l.W13, w13}) ||
         overlaps(y, {l.sf13, s13}) || overlaps(y, {l.W2, w2}) || overlaps(y, {l.sf2, s2}) ||
         overlaps(y, {l.alpha13, l.experts * 8}) || overlaps(y, {l.alpha2, l.experts * 4}) ||
-        (!in_place && overlaps(y, {c.residual, rs})))
+        (!in_place && rows_overlap(yr, rows_at(c.residual, l.hidden, c.ldr, yb, rs))))
         return NVFP4_GEMV_ERR_ALIAS;
     return NVFP4_GEMV_OK;
 }

@@ -36,10 +36,41 @@ void check_reach() {
     CHECK(!p.stream && p.tile >= 0 && kTileKinds[p.tile].tokens() == 256);
 }
 
+// Rows that share no byte are not refused where their strides agree, and rows that
+// share one always are.
+void check_overlap() {
+    for (int64_t stride = 1; stride <= 9; ++stride)
+        for (int64_t other = stride; other <= stride + 1; ++other)
+            for (int64_t wa = 1; wa <= stride; ++wa)
+                for (int64_t wb = 1; wb <= other; ++wb)
+                    for (int64_t rows = 1; rows <= 4; ++rows)
+                        for (int64_t at = 0; at <= 80; ++at) {
+                            const RowSpan a = {40, (rows - 1) * stride + wa, wa, stride};
+                            const RowSpan b = {static_cast<uintptr_t>(at), (rows - 1) * other + wb, wb, other};
+                            bool share = false;
+                            for (int64_t i = 0; i < rows; ++i)
+                                for (int64_t j = 0; j < rows; ++j) {
+                                    const int64_t x = 40 + i * stride, y = at + j * other;
+                                    share |= x < y + wb && y < x + wa;
+                                }
+                            const bool said = rows_overlap(a, b);
+                            CHECK(said == rows_overlap(b, a));
+                            CHECK(said || !share);
+                            // column ranges of one matrix, b's in a row of a's or a's in a row of b's
+                            const int64_t d = ((at - 40) % stride + stride) % stride;
+                            const bool columns = d >= wa && d + wb <= stride;
+                            if (stride == other && columns) CHECK(!said);
+                            // one row each: exactly
+                            if (rows == 1 && (at >= 40 + wa || at + wb <= 40)) CHECK(!said);
+                        }
+    CHECK(!rows_overlap({40, 0, 4, 8}, {40, 12, 4, 8}));
+}
+
 }  // namespace
 
 int main() {
     check_reach();
+    check_overlap();
     if (g_failures) return 1;
     std::printf("ffn_limits_check ok\n");
     return 0;

@@ -99,3 +99,38 @@ def test_linear_special_values_of_one_token(x, gated, layout, k):
     xv[0] = 0.0
     got = one_call(rng, 1, k, x, layout, gated, xv, codes, scales)
     assert bool((got[0, [0, 1, 7, 9]] == 0).all())
+
+
+@pytest.mark.parametrize("n", [1, 3, 40, 800])
+def test_linear_between_columns_of_one_matrix(n):
+    """X, the residual and Y as column ranges of one matrix."""
+    rng = np.random.default_rng(54)
+    codes, scales = weight(rng, 1, 80, 128)
+    dc, ds = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    both = torch.from_numpy(rng.standard_normal((n, 128 + 80 + 80 + 8))).to(torch.bfloat16).cuda()
+    before = both.clone()
+    al = torch.tensor([0.01], device="cuda")
+    want = pd.linear(both[:, 88:216].contiguous(), dc, ds, 80, alpha=al, residual=both[:, 216:].contiguous()[:, :80])
+    pd.linear(both[:, 88:216], dc, ds, 80, alpha=al, residual=both[:, 216:296], out=both[:, 4:84])
+    assert torch.equal(both[:, 4:84], want)
+    before[:, 4:84] = want
+    assert torch.equal(both, before)
+    if n > 1:   # a column too far
+        with pytest.raises(pd.Nvfp4GemvError) as e:
+            pd.linear(both[:, 88:216], dc, ds, 80, out=both[:, 9:89])
+        assert e.value.status == pd.NVFP4_GEMV_ERR_ALIAS
+
+
+def test_moe_layer_between_columns_of_one_matrix():
+    rng = np.random.default_rng(55)
+    c13, s13 = weight(rng, 12, 64, 128)
+    c2, s2 = weight(rng, 6, 128, 64)
+    dev = lambda v: torch.from_numpy(v).cuda()
+    layer = pd.MoeLayer(dev(rng.standard_normal((6, 128))).to(torch.bfloat16), dev(c13), dev(s13), dev(c2), dev(s2),
+                        inter=64, topk=2, alpha13=torch.full((6, 2), 0.01, device="cuda"))
+    for n in (1, 5, 50):
+        both = dev(rng.standard_normal((n, 256))).to(torch.bfloat16)
+        x = both[:, :128].clone()
+        want = pd.moe_layer(x, layer)
+        pd.moe_layer(both[:, :128], layer, out=both[:, 128:])
+        assert torch.equal(both[:, 128:], want) and torch.equal(both[:, :128], x)
