@@ -1218,20 +1218,19 @@ __global__ void __launch_bounds__(kFinishThreads) linear_finish(FfnArgs a) {
 }
 
 // ---------------------------------------------------------------- alignment of X
-constexpr int kAlignThreads = 256;
-
 // Copies 16-bit rows with any stride and alignment to rows of k elements (a
-// multiple of 16) on 16-byte boundaries: one thread per 8 elements.
+// multiple of 16) on 16-byte boundaries: 8 elements a thread at a time.
 __global__ void __launch_bounds__(kAlignThreads) align_rows(const uint16_t *x, int64_t ldx, uint16_t *y,
                                                             int64_t rows, int64_t k) {
     const int64_t pieces = k / 8;
-    const int64_t i = int64_t(blockIdx.x) * kAlignThreads + threadIdx.x;
-    if (i >= rows * pieces) return;
-    const int64_t row = i / pieces, e = 8 * (i - row * pieces);
-    uint16_t v[8];
+    for (int64_t i = int64_t(blockIdx.x) * kAlignThreads + threadIdx.x; i < rows * pieces;
+         i += int64_t(gridDim.x) * kAlignThreads) {
+        const int64_t row = i / pieces, e = 8 * (i - row * pieces);
+        uint16_t v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = x[row * ldx + e + j];
-    __builtin_memcpy(y + row * k + e, v, 16);
+        for (int j = 0; j < 8; ++j) v[j] = x[row * ldx + e + j];
+        __builtin_memcpy(y + row * k + e, v, 16);
+    }
 }
 
 // ---------------------------------------------------------------- routing

@@ -160,6 +160,16 @@ inline float rounds_us(const float (&us)[4], int64_t count, int64_t wins) {
                static_cast<float>(wins) / 28.0f;
 }
 
+// Workgroups that copy X to aligned rows, a thread per 8 elements at a time: at
+// most 16 rounds of the 8 that a compute unit holds, so that X of any size keeps
+// the launch within 2^32 threads.
+constexpr int kAlignThreads = 256;
+constexpr int64_t kMaxAlignGroups = 128 * kComputeUnits;
+inline int64_t align_groups(int64_t n, int64_t k) {
+    const int64_t want = ceil_div(n * (k / 8), kAlignThreads);
+    return want < kMaxAlignGroups ? want : kMaxAlignGroups;
+}
+
 struct LinearPlan {
     bool stream;        // stream kernel
     int tile;           // shape of the tile kernel, or -1; neither: the simple kernel

@@ -182,7 +182,7 @@ int copy_aligned(const void *X, int64_t ldx, void *to, int64_t rows, int64_t k, 
     uint16_t *y = static_cast<uint16_t *>(to);
     void *args[] = {&x, &ldx, &y, &rows, &k};
     return run(reinterpret_cast<const void *>(align_rows),
-               dim3(static_cast<uint32_t>(ceil_div(rows * (k / 8), kAlignThreads))), kAlignThreads, args, stream);
+               dim3(static_cast<uint32_t>(align_groups(rows, k))), kAlignThreads, args, stream);
 }
 
 LinearPlan plan_of(const LinearCall &c) {

@@ -66,9 +66,20 @@ void check_overlap() {
     CHECK(!rows_overlap({40, 0, 4, 8}, {40, 12, 4, 8}));
 }
 
+// The copy of X to aligned rows: X of any size that the GPU's memory can hold.
+void check_align() {
+    const int64_t sizes[][2] = {{1, 16}, {17, 272}, {4096, 7168}, {1 << 22, 16384}, {1 << 15, kMaxK}, {1 << 27, 1024}};
+    for (const auto &s : sizes) {
+        const int64_t groups = align_groups(s[0], s[1]);
+        CHECK(groups >= 1 && groups * kAlignThreads < (int64_t(1) << 32));
+        CHECK(groups <= ceil_div(s[0] * (s[1] / 8), kAlignThreads));
+    }
+}
+
 }  // namespace
 
 int main() {
+    check_align();
     check_reach();
     check_overlap();
     if (g_failures) return 1;

@@ -134,3 +134,18 @@ def test_moe_layer_between_columns_of_one_matrix():
         want = pd.moe_layer(x, layer)
         pd.moe_layer(both[:, :128], layer, out=both[:, 128:])
         assert torch.equal(both[:, 128:], want) and torch.equal(both[:, :128], x)
+
+
+def test_linear_large_unaligned_input():
+    """More pieces of X than the copy to aligned rows has threads."""
+    n, m, k = 40000, 2050, 4096
+    rng = np.random.default_rng(56)
+    codes, scales = weight(rng, 1, m, k)
+    dc, ds = pd.pack_weight(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda())
+    x = torch.randint(-8, 9, (n, k + 1), device="cuda").to(torch.bfloat16)
+    got = pd.linear(x[:, 1:], dc, ds, m, packed=True, out_dtype=torch.float32)
+    want = pd.linear(x[:, 1:].contiguous(), dc, ds, m, packed=True, out_dtype=torch.float32)
+    assert torch.equal(got, want)
+    for t in (0, 1, 16384, n - 1):
+        w, err = ffn.linear(x[t:t + 1, 1:].double().cpu().numpy(), codes, scales)
+        assert_close(got[t:t + 1], w, err, "f32", f"token {t}")
