@@ -14,16 +14,14 @@
 #include <climits>
 #include <cstddef>
 #include <cstdint>
-#include <map>
 #include <mutex>
-#include <utility>
-#include <vector>
 
 #include "device_common.h"
 #include "gemv_kernels.h"
 #include "gemv_plan.h"
 #include "nvfp4_gemv.h"
 #include "probe_kernels.h"
+#include "workspace_table.h"
 
 namespace {
 
@@ -107,16 +105,7 @@ int run(const Plan &p, const GemvArgs &g, void *ws, hipStream_t stream) {
     return NVFP4_GEMV_OK;
 }
 
-// Library-owned split-K workspaces, one per (device, stream).  A slot only
-// grows.  Growing allocates a new buffer and retires the old one without
-// freeing it: kernels enqueued earlier on the stream may still read it, and
-// freeing it safely would need a synchronisation.  Retired buffers are kept
-// until the process ends; each growth at least doubles the slot, so they add
-// at most the slot's final size.  No allocation is made while the stream is
-// being captured into a graph (the call fails instead).
-std::mutex g_ws_mutex;
-std::map<std::pair<int, void *>, std::pair<void *, size_t>> g_ws;
-std::vector<void *> g_ws_retired;
+nvfp4ws::WorkspaceTable g_workspaces;
 
 bool stream_capturing(void *stream) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
@@ -190,20 +179,13 @@ void *scratch_address(int dev) {
 }  // namespace
 
 void *nvfp4_stream_workspace(int dev, void *stream, size_t need) {
-    std::lock_guard<std::mutex> lock(g_ws_mutex);
-    auto &slot = g_ws[std::make_pair(dev, stream)];
-    if (slot.second >= need) return slot.first;
-    if (stream_capturing(stream)) return nullptr;
-    size_t bytes = slot.second > need / 2 ? 2 * slot.second : need;
-    bytes = (bytes + 255) & ~size_t(255);
-    void *ptr = nullptr;
-    if (hipMalloc(&ptr, bytes) != hipSuccess) {
+    const auto alloc = [](size_t bytes) -> void * {
+        void *ptr = nullptr;
+        if (hipMalloc(&ptr, bytes) == hipSuccess) return ptr;
         (void)hipGetLastError();
         return nullptr;
-    }
-    if (slot.first) g_ws_retired.push_back(slot.first);
-    slot = std::make_pair(ptr, bytes);
-    return ptr;
+    };
+    return g_workspaces.get(dev, stream, need, alloc, [stream] { return stream_capturing(stream); });
 }
 
 extern "C" {
