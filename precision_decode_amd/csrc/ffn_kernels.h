@@ -596,7 +596,7 @@ __device__ __forceinline__ void stream_sums(const FfnArgs &a, int expert, int64_
 // with the sum of row i of every tile, the same for all q.  The token's elements
 // of a window go through the wave's LDS slot, every lane quarter's 128 bytes 16
 // bytes further, so that the quarters' reads hit distinct banks.
-constexpr int kDotSlot = 4 * (8 + 1);   // 16-byte pieces of a plane
+constexpr int kDotSlot = 4 * (8 + 1);   // 16-byte pieces of a window
 // A block is summed before its scale is known to make its products smaller: 16
 // products of a bf16 value and a code reach 96 times the largest fp32 value, so
 // the codes are converted to 2^-7 times their value and the scales to 2^7 times
@@ -634,9 +634,9 @@ __device__ __forceinline__ float dot8(uint32_t q, u32x4 x, float s) {
     }
 }
 
-template <bool BF16, int L, int G, int P, int MODE, int R, int U>
-__device__ __forceinline__ void dot_sums(const FfnArgs &a, int expert, int64_t row0, int split, int32_t p0,
-                                         u32x4 *slot, int wave, int waves, float (&acc)[G][R]) {
+template <bool BF16, int L, int G, int R, int U>
+__device__ __forceinline__ void dot_sums(const FfnArgs &a, int64_t row0, int split, int32_t token, u32x4 *slot, int wave,
+                                         int waves, float (&acc)[G][R]) {
     const int lane = threadIdx.x & (kWave - 1);
     const int li = lane & 15, kq = lane >> 4;
     const uint32_t k = static_cast<uint32_t>(a.k);
@@ -645,22 +645,17 @@ __device__ __forceinline__ void dot_sums(const FfnArgs &a, int expert, int64_t r
     const int nwin = static_cast<int>(int64_t(split + 1) * wins / a.splits) - win0;
     const int niter = nwin > wave ? (nwin - wave + waves - 1) / waves : 0;
 
-    const WeightTiles<L, R> w0(a, G * int64_t(expert), row0, li, kq);
-    const WeightTiles<L, R> w1(a, G * int64_t(expert) + (G - 1), row0, li, kq);
-    const int64_t row = MODE == kLinear ? p0 : x_row<MODE>(a, out_row<MODE>(a, p0));
-    __amdgpu_buffer_rsrc_t xdesc[P];
-#pragma unroll
-    for (int p = 0; p < P; ++p) xdesc[p] = buffer_of(a.X + 2 * (row * a.ldx + p * a.plane), kAnyRange);
+    const WeightTiles<L, R> w0(a, 0, row0, li, kq);
+    const WeightTiles<L, R> w1(a, G - 1, row0, li, kq);
+    const __amdgpu_buffer_rsrc_t xdesc = buffer_of(a.X + 2 * (token * a.ldx), kAnyRange);
 
-    u32x4 wq[U][G][R][2], xq[U][P];
+    u32x4 wq[U][G][R][2], xq[U];
     ScaleWord<L> ws[U][G][R];
     auto issue = [&](int i, int u) {
         const uint32_t win = static_cast<uint32_t>(win0 + wave + waves * i);
         const int left = i < niter ? static_cast<int>(k - win * kWinElems) : 0;
         const uint32_t xo = lane < 32 && 8 * lane < left ? 16 * lane : kOutOfRange;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-            xq[u][p] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xdesc[p], xo, win * 512, 0));
+        xq[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xdesc, xo, win * 512, 0));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             w0.load(r, win, left, wq[u][0][r], ws[u][0][r]);
@@ -673,26 +668,20 @@ __device__ __forceinline__ void dot_sums(const FfnArgs &a, int expert, int64_t r
         for (int r = 0; r < R; ++r) acc[g][r] = 0.0f;
     auto consume = [&](int u) {
         wave_lds_fence();
-        if (lane < 32)
-#pragma unroll
-            for (int p = 0; p < P; ++p) slot[p * kDotSlot + lane + (lane >> 3)] = xq[u][p];
+        if (lane < 32) slot[lane + (lane >> 3)] = xq[u];
         wave_lds_fence();
 #pragma unroll
         for (int b = 0; b < 4; ++b) {   // blocks of 16 elements
-            u32x4 xv[P][2];
+            u32x4 xv[2];
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) xv[p][c] = slot[p * kDotSlot + 9 * kq + 2 * b + c];
+            for (int c = 0; c < 2; ++c) xv[c] = slot[9 * kq + 2 * b + c];
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     float s = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int p = 0; p < P; ++p) s = dot8<BF16>(wq[u][g][r][b / 2][2 * (b & 1) + c], xv[p][c], s);
+                    for (int c = 0; c < 2; ++c) s = dot8<BF16>(wq[u][g][r][b / 2][2 * (b & 1) + c], xv[c], s);
                     acc[g][r] = __builtin_fmaf(dot_scale<BF16>(ws[u][g][r].value() >> (8 * b)), s, acc[g][r]);
                 }
         }
@@ -734,7 +723,7 @@ __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int li = lane & 15, kq = lane >> 4;
-    f32x4 acc[G][R];
+    static_assert(W > 1, "the waves' sums go through LDS");
     // the sums of wave w, matrix g and tile r, four rows of a token, for this lane
     const f32x4 *red = reinterpret_cast<const f32x4 *>(lds);
     auto at = [&](int w, int g, int r) {
@@ -742,7 +731,8 @@ __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_
     };
     if constexpr (NX == 0) {
         float sum[G][R];
-        dot_sums<BF16, L, G, P, MODE, R, U>(a, expert, row0, split, p0, lds + wave * (P * kDotSlot), wave, W, sum);
+        static_assert(MODE == kLinear && P == 1, "one token of the linear layer");
+        dot_sums<BF16, L, G, R, U>(a, row0, split, p0, lds + wave * kDotSlot, wave, W, sum);
         __syncthreads();
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -751,41 +741,36 @@ __device__ __forceinline__ void stream_pass(const FfnArgs &a, int expert, int64_
                 if (lane < kTile) reinterpret_cast<float *>(lds)[((wave * G + g) * R + r) * kTile + lane] = sum[g][r];
         __syncthreads();
     } else {
+        f32x4 acc[G][R];
         stream_sums<BF16, L, G, P, MODE, R, U, NX>(a, expert, row0, split, p0, end, lds + wave * (P * 2 * NX * 32), wave,
                                                    W, acc);
-        if (W > 1) {
-            __syncthreads();
+        __syncthreads();
 #pragma unroll
-            for (int g = 0; g < G; ++g)
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int r = 0; r < R; ++r) reinterpret_cast<f32x4 *>(lds)[at(wave, g, r)] = acc[g][r];
-            __syncthreads();
-        }
+            for (int r = 0; r < R; ++r) reinterpret_cast<f32x4 *>(lds)[at(wave, g, r)] = acc[g][r];
+        __syncthreads();
     }
     // wave r % W finishes row tile r
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if (W > 1 && r % W != wave) continue;
+        if (r % W != wave) continue;
         f32x4 sum[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            if (NX > 0 && W == 1) {
-                sum[g] = acc[g][r];
-                continue;
-            }
             sum[g] = red[at(0, g, r)];
             for (int w = 1; w < W; ++w) sum[g] += red[at(w, g, r)];
         }
         if (p0 + li < end && li < (NX == 0 ? 1 : 2 * NX))
             finish4<MODE, G>(a, expert, split, out_row<MODE>(a, p0 + li), row0 + r * kTile + 4 * kq, sum);
     }
-    if (MODE != kLinear && W > 1) __syncthreads();   // before the next pass writes LDS
+    if (MODE != kLinear) __syncthreads();   // before the next pass writes LDS
 }
 
 // LDS of a stream workgroup in 16-byte pieces: the waves' slots, later their sums.
 template <int G, int P, int R, int W, int NX>
 constexpr int stream_lds() {
-    return NX == 0 ? W * (P * kDotSlot > G * R * 4 ? P * kDotSlot : G * R * 4)
+    return NX == 0 ? W * (kDotSlot > G * R * 4 ? kDotSlot : G * R * 4)
                    : W * kWave * (P * NX > G * R ? P * NX : G * R);
 }
 
@@ -883,22 +868,22 @@ template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
-template <int G, int Q, int NT, int WM, int WN, int WK>
+template <int G, int Q, int NT, int WM, int WK>
 struct TileShape {
-    static constexpr int waves = WM * WN * WK;
+    static constexpr int waves = WM * WK;
     static constexpr int rows = kTile * Q * WM;       // of each matrix
-    static constexpr int tokens = kTile * NT * WN;
+    static constexpr int tokens = kTile * NT;
     static constexpr int stage = tokens * kStageElems / 8;             // 16-byte pieces
     static constexpr int stride = kTile * Q * G * 4 + 16;              // bytes of a token in the epilogue
     static constexpr int out_tiles = Q == 1 ? 2 : 1;                   // token tiles a wave's epilogue takes at a time
     static constexpr int wave_out = out_tiles * kTile * stride;        // bytes of them
-    static constexpr int out_waves = WM * WN * (WK < NT / out_tiles ? WK : NT / out_tiles);   // waves that have any
+    static constexpr int out_waves = WM * (WK < NT / out_tiles ? WK : NT / out_tiles);   // waves that have any
 };
 
 // More than 16 tokens.  A workgroup owns 16 Q WM rows of each of G matrices and
-// 16 NT WN tokens; WK groups of WM x WN waves take the windows of K in turn and
-// add their sums through LDS at the end.  A wave holds the sums of G Q row tiles
-// by NT token tiles.
+// 16 NT tokens; WK groups of WM waves take the windows of K in turn and add their
+// sums through LDS at the end.  A wave holds the sums of G Q row tiles by NT token
+// tiles.
 //
 // Weights go from memory straight into the registers of the wave that owns their
 // rows, in 1 KiB instructions (packed), and are decoded there, once for all NT
@@ -918,9 +903,9 @@ struct TileShape {
 // cores do not sustain their nominal rate on such operands; the tokens' copies
 // add 20 us, the weights' loads 15 and the decode 12 (fp16) or 25.  Waves of 64
 // rows by 128 tokens decode as little, but spill or leave one wave per SIMD.
-template <bool BF16, int L, int G, int Q, int NT, int WM, int WN, int WK>
+template <bool BF16, int L, int G, int Q, int NT, int WM, int WK>
 __device__ __forceinline__ void tile_product(const FfnArgs &a) {
-    using S = TileShape<G, Q, NT, WM, WN, WK>;
+    using S = TileShape<G, Q, NT, WM, WK>;
     constexpr int RT = G * Q;
     static_assert(S::out_waves * S::wave_out <= 2 * 16 * S::stage * WK && S::out_waves % 2 == 0, "the epilogue fits");
     static_assert(WK == 1 || (S::waves * NT * kWave <= S::stage * WK && RT <= 2), "the groups' sums fit");
@@ -928,8 +913,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int li = lane & 15, kq = lane >> 4;
-    const int wm = wave % WM, wn = wave / WM % WN, kg = wave / (WM * WN);
-    const int gwave = wave % (WM * WN);   // wave of its group
+    const int wm = wave % WM, kg = wave / WM;   // wave of its group, group
     const uint32_t k = static_cast<uint32_t>(a.k);
 
     // Workgroup -> (split, strip of rows, block of tokens): every die takes a
@@ -956,15 +940,15 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     // staging: copy i of 4 tokens: lane l fills position l % 16 of token t = 4 i + l / 16
     // with piece (l % 16) ^ (t & 15); piece 4 q + c holds elements 64 q + 32 h + 8 c
     // of the window
-    constexpr int kCopies = S::tokens / 4 / (WM * WN);
-    static_assert(S::tokens % (4 * WM * WN) == 0, "whole copies per wave");
+    constexpr int kCopies = S::tokens / 4 / WM;
+    static_assert(S::tokens % (4 * WM) == 0, "whole copies per wave");
     const __amdgpu_buffer_rsrc_t xdesc = buffer_of(a.X + 2 * (tok0 * a.ldx), kAnyRange);
     const int tlast = a.n - tok0 < S::tokens ? static_cast<int>(a.n - tok0) - 1 : S::tokens - 1;
-    const int piece = li ^ ((4 * kCopies * gwave + kq) & 15);
+    const int piece = li ^ ((4 * kCopies * wm + kq) & 15);
     uint32_t xo[kCopies];   // rows past the last repeat it and are not stored
 #pragma unroll
     for (int j = 0; j < kCopies; ++j) {
-        const int t = 4 * (kCopies * gwave + j) + kq;
+        const int t = 4 * (kCopies * wm + j) + kq;
         xo[j] = 2 * ((t < tlast ? t : tlast) * static_cast<uint32_t>(a.ldx) +
                      64 * ((piece >> 2) ^ (j & 3)) + 8 * (piece & 3));
     }
@@ -983,7 +967,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
 #pragma unroll
         for (int j = 0; j < kCopies; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                xdesc, to + 16 * S::stage * kg + 1024 * (kCopies * gwave + j), 16,
+                xdesc, to + 16 * S::stage * kg + 1024 * (kCopies * wm + j), 16,
                 xo[j] | (64 * ((piece >> 2) ^ (j & 3)) + (L == kRows16 ? 32 * h + 8 * (piece & 3) : 0) < left ? 0u
                                                                                                        : kOutOfRange),
                 2 * (win * kWinElems + 32 * h), 0, 0);
@@ -1010,7 +994,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
         constexpr int kPairs = NT / 2;
         u32x4 xv[2][2];
         auto read = [&](int c, int t, u32x4 &to) {
-            to = (h == 0 ? lds0 : lds1)[S::stage * kg + 16 * (16 * (wn * NT + t) + li) + ((4 * kq + c) ^ li)];
+            to = (h == 0 ? lds0 : lds1)[S::stage * kg + 16 * (16 * t + li) + ((4 * kq + c) ^ li)];
         };
         read(0, 0, xv[0][0]);
         read(0, 1, xv[0][1]);
@@ -1086,10 +1070,10 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (t / S::out_tiles % WK != kg) continue;
-                const f32x4 *from = reinterpret_cast<const f32x4 *>(r == 0 ? lds0 : lds1) + (gwave * NT + t) * kWave + lane;
+                const f32x4 *from = reinterpret_cast<const f32x4 *>(r == 0 ? lds0 : lds1) + (wm * NT + t) * kWave + lane;
                 f32x4 sum = from[0];
 #pragma unroll
-                for (int i = 1; i < WK; ++i) sum += from[i * WM * WN * NT * kWave];
+                for (int i = 1; i < WK; ++i) sum += from[i * WM * NT * kWave];
                 acc[r][t] = sum;
             }
         lds_barrier();
@@ -1104,7 +1088,7 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     constexpr int kStep = kWave / kGroups;               // tokens per iteration
     constexpr int kIters = S::out_tiles * kTile / kStep;
     const int64_t r = row0 + 8 * (lane % kGroups);
-    const int64_t first = tok0 + kTile * NT * wn + lane / kGroups;   // the lane's first token
+    const int64_t first = tok0 + lane / kGroups;   // the lane's first token
     const int rows = a.m - r < 8 ? static_cast<int>(a.m - r) : 8;    // of the lane's 8, those that exist
     const bool whole = rows == 8;
     const float al = a.alpha ? a.alpha[0] : 1.0f, au = G == 2 && a.alpha ? a.alpha[1] : 1.0f;
@@ -1182,9 +1166,9 @@ __device__ __forceinline__ void tile_product(const FfnArgs &a) {
     }
 }
 
-template <bool BF16, int L, int G, int Q, int NT, int WM, int WN, int WK>
-__global__ void __launch_bounds__(WM *WN *WK *kWave, 2) ffn_tile(const FfnArgs a) {
-    tile_product<BF16, L, G, Q, NT, WM, WN, WK>(a);
+template <bool BF16, int L, int G, int Q, int NT, int WM, int WK>
+__global__ void __launch_bounds__(WM *WK *kWave, 2) ffn_tile(const FfnArgs a) {
+    tile_product<BF16, L, G, Q, NT, WM, WK>(a);
 }
 
 // ---------------------------------------------------------------- split sums

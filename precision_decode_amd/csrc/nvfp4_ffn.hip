@@ -133,7 +133,7 @@ int launch_linear_stream(const FfnArgs &a, const LinearPlan &p, hipStream_t stre
 template <bool BF16, int L, int G, int KIND>
 int launch_tile(const FfnArgs &a, const LinearPlan &p, hipStream_t stream) {
     constexpr TileKind t = G == 2 ? kGatedTileKinds[KIND % kNumGatedTileKinds] : kTileKinds[KIND];
-    return run(ffn_tile<BF16, L, G, t.q, t.nt, t.wm, 1, t.wk>,
+    return run(ffn_tile<BF16, L, G, t.q, t.nt, t.wm, t.wk>,
                dim3(static_cast<uint32_t>(p.strips * p.blocks * p.splits)), t.waves() * kWave, a, stream);
 }
 
