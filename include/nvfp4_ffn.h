@@ -4,8 +4,9 @@
  * epilogue, and a whole mixture-of-experts (MoE) layer for a few tokens.
  *
  * Both take 16-bit floating-point activations (bf16 or fp16) as they are: a
- * weight element times its block scale, e2m1 * e4m3, has at most 5
- * significant bits and lies in 2^-10 .. 2688, so it is exact in either type,
+ * weight element times its block scale, e2m1 * e4m3, has at most 6
+ * significant bits and, unless it is 0, lies in 2^-10 .. 2688, so it is exact in
+ * either type,
  * the products are exact in fp32 and the sums are fp32 (their order is fixed
  * for a given shape, type, layout and alignment).
  *

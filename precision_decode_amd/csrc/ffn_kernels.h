@@ -64,10 +64,12 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // The normal distribution function: with a = |z| / sqrt 2 its smaller side is
-// erfc(a) / 2 = exp(-z^2 / 2) (exp(a^2) erfc(a)) / 2, and exp(a^2) erfc(a) is, to
-// 2e-8 of itself up to a = 4 and as far as exp(-a^2) lets it matter beyond, a
-// polynomial of degree 9 in t = 1 / (1 + 0.4 a) without a constant term: a
-// weighted least-squares fit, reweighted until the error is level.
+// erfc(a) / 2 = exp(-z^2 / 2) (exp(a^2) erfc(a)) / 2, and exp(a^2) erfc(a) is a
+// polynomial of degree 9 in t = 1 / (1 + 0.4 a) without a constant term, a weighted
+// least-squares fit, reweighted until the error is level: to 3.2e-8 of itself up to
+// a = 4, 1e-7 up to 6 and 1.2e-5 up to 9.5, where exp(-a^2) is 1e-39.  With the fp32
+// operations around it GELU is off by at most 4.1e-7 of itself for bf16 z from -4 on
+// and 1.6e-6 from -8 on, most of it from the exponential.
 __device__ __forceinline__ float normal_cdf(float z) {
     const float t = fast_rcp(__builtin_fmaf(0.4f * 0.70710678f, __builtin_fabsf(z), 1.0f));
     constexpr float c[9] = {0.22539076f, 0.23008046f, 0.17877823f, 0.27498057f, -0.09545095f,
@@ -423,7 +425,7 @@ struct WeightTiles {
     __device__ __forceinline__ uint32_t past(int left, int block) const {
         return first + 16 * block < left ? 0u : kOutOfRange;
     }
-    // POLICY: kNonTemporal for weights that are read once.
+    // POLICY: kNonTemporal for weights that a workgroup reads once.
     template <int POLICY>
     __device__ __forceinline__ void load_half(int r, uint32_t window, int left, int h, u32x4 &q) const {
         if constexpr (L == kRows16) {
@@ -451,6 +453,8 @@ struct WeightTiles {
                                                              window * (L == kPackedTiles ? kWinScaleBytes : 16), POLICY);
         }
     }
+    // For the stream kernels: non-temporal also where another block of tokens, pass or
+    // slot reads the same weights again.
     __device__ __forceinline__ void load(int r, uint32_t window, int left, u32x4 (&q)[2], ScaleWord<L> &s) const {
         load_half<kNonTemporal>(r, window, left, 0, q[0]);
         load_half<kNonTemporal>(r, window, left, 1, q[1]);
@@ -468,8 +472,9 @@ __device__ __forceinline__ void wave_lds_fence() {
 // The sums of R tiles of 16 rows of each of G matrices for up to 2 NX tokens: a
 // wave takes every `waves`-th window of 256 elements of K of its part of K from
 // window `wave` on, U in flight.  This is the shape for few tokens, where the
-// weights' bytes are the bound: every weight byte is read once, in 1 KiB
-// instructions (packed), and decoded once for all tokens.
+// weights' bytes are the bound: every weight byte is read in 1 KiB instructions
+// (packed) and decoded, once for up to 2 NX tokens; more tokens (blocks of the
+// linear layer, passes over an expert's slots) read and decode it again.
 //
 // The tokens' elements of a window (512 bytes each) are read row by row, two
 // tokens per instruction, as far ahead as the weights, and go through a slot
@@ -895,12 +900,13 @@ struct TileShape {
 // the same piece of 16 tokens hit distinct banks.  Two buffers are two variables:
 // in one, every read would wait for the copies into the other half.
 //
-// 4096 tokens x (4096 x 7168) in 256 x 256 tiles: bf16 210 us, 1.15 PFLOP/s,
-// fp16 191 us, where a library's bf16 product reaches 1.54.  256 x 128 tiles,
-// which decode every weight for half as many tokens, take 230-260 and 205 us.  Of
-// those, without the loads and the decode, so with matrix instructions and LDS
-// reads alone, the same loop takes 180 us, without the LDS reads 167: the matrix
-// cores do not sustain their nominal rate on such operands; the tokens' copies
+// 4096 tokens x (4096 x 7168) in 256 x 256 tiles: bf16 192-196 us, 1.24 PFLOP/s,
+// fp16 192, where a library's bf16 product reaches 1.54; with SiLU, bias and
+// residual 206-209 us (up to 230 on other GPUs).  256 x 128 tiles, which decode every
+// weight for half as many tokens, take 214 and 203 us, 128 x 128 tiles 274 and 266.
+// In 256 x 128 tiles the loop without the loads and the decode, so with matrix
+// instructions and LDS reads alone, takes 180 us, without the LDS reads 167: the
+// matrix cores do not sustain their nominal rate on such operands; the tokens' copies
 // add 20 us, the weights' loads 15 and the decode 12 (fp16) or 25.  Waves of 64
 // rows by 128 tokens decode as little, but spill or leave one wave per SIMD.
 template <bool BF16, int L, int G, int Q, int NT, int WM, int WK>

@@ -189,8 +189,8 @@ struct LinearPlan {
 // workgroups, and the shapes of the tile kernel, which read and decode the less
 // per product the larger they are.  Measured, in us, for 256 x 256, 256 x 128,
 // 128 x 128, 128 x 64, 64 x 64 tiles on 4096 x 7168: 256 tokens -, 96, 60, 37, 32;
-// 512 tokens -, 96, 61, 41, 50; 1024 tokens -, 98, 70, 72, 93; 4096 tokens 204,
-// 240, 264, -, -.  K whole and split: 64 tokens 20.7 and 17.8 (in two); 32 tokens,
+// 512 tokens -, 96, 61, 41, 50; 1024 tokens -, 98, 70, 72, 93; 4096 tokens 194,
+// 214, 274, -, -.  K whole and split: 64 tokens 20.7 and 17.8 (in two); 32 tokens,
 // 7168 x 2048, 9.4 and 12.4.
 inline LinearPlan plan_linear(int64_t n, int64_t m, int64_t k, bool gated, bool fast, bool x_aligned) {
     LinearPlan p = {};

@@ -2,9 +2,9 @@
 // layer with bias, activation and residual in its epilogue, and a whole
 // mixture-of-experts layer for a few tokens.
 //
-// A weight element times its block scale, e2m1 * e4m3, has at most 5
-// significant bits and lies in 2^-10 .. 2688, so it is exact as bf16 and as
-// fp16.  The 16-bit activations therefore meet the 4-bit weights on the
+// A weight element times its block scale, e2m1 * e4m3, has at most 6
+// significant bits (2 times 4, 15 * 3 = 45) and, unless it is 0, lies in 2^-10 ..
+// 2688, so it is exact as bf16 and as fp16.  The 16-bit activations therefore meet the 4-bit weights on the
 // 16x16x32 matrix-core instructions of their own type without being
 // quantised: the VALU decodes weight tiles into operands, the products are
 // exact in fp32 and summed there.  The weight tile is the A operand and the

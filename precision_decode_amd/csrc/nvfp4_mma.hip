@@ -11,8 +11,8 @@
 // still those of a GEMV: weights are read once and dominate the traffic.  So
 // the products go to the matrix cores and the VALU only decodes:
 //
-//  * a weight element times its block scale, e2m1 * e4m3, has at most 5
-//    significant bits and lies in 2^-10 .. 2688, so it is exact in fp16; the
+//  * a weight element times its block scale, e2m1 * e4m3, has at most 6
+//    significant bits and, unless 0, lies in 2^-10 .. 2688, so it is exact in fp16; the
 //    same holds for the vectors.  Each lane decodes 32 codes (16 bytes) and
 //    their two block scales into four 8-element fp16 operands with the gfx950
 //    packed FP4 -> fp16 conversion and one packed fp16 multiply per pair;
