@@ -7,6 +7,7 @@ import torch
 import precision_decode_amd as pd
 from ffn_util import TYPES, assert_close, rounded, weight
 from oracle import ffn
+from test_gpu_ffn import linear_case, moe_case
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +150,92 @@ def test_linear_large_unaligned_input():
     for t in (0, 1, 16384, n - 1):
         w, err = ffn.linear(x[t:t + 1, 1:].double().cpu().numpy(), codes, scales)
         assert_close(got[t:t + 1], w, err, "f32", f"token {t}")
+
+
+@pytest.mark.parametrize("n,m,k,gated", [(1, 40, 65536, False), (2, 40, 65536, False), (5, 41, 65536, True),
+                                         (16, 40, 65536, False), (1, 100, 16400, False), (8, 100, 16400, True)])
+def test_linear_few_tokens_with_k_split(n, m, k, gated):
+    """Long rows and few of them: the stream kernel's workgroups share K."""
+    for layout in (("row",) if k % 64 else ("row", "packed")):
+        for x in ("bf16", "f16"):
+            linear_case(np.random.default_rng(57 + n), n, m, k, x=x, y="f32", gated=gated, act="silu", bias=True,
+                        residual="apart", layout=layout, ws=True, ldy=m + 1)
+
+
+def test_linear_more_outputs_than_31_bits():
+    """n m of 4 10^9: the first and last tokens against a call of their own."""
+    n, m, k = 262000, 16000, 64
+    rng = np.random.default_rng(58)
+    codes, scales = weight(rng, 1, m, k)
+    dc, ds = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    x = torch.randint(-8, 9, (n, k), device="cuda").to(torch.float16)
+    al = torch.tensor([0.01], device="cuda")
+    y = pd.linear(x, dc, ds, m, alpha=al, activation="relu")
+    for first in (0, 134200, n - 300):    # the second: around element 2^31
+        part = pd.linear(x[first:first + 300], dc, ds, m, alpha=al, activation="relu")
+        assert torch.equal(y[first:first + 300], part)
+    want, err = ffn.linear(x[n - 1:].double().cpu().numpy(), codes, scales, al.cpu().numpy(), act="relu")
+    assert_close(y[n - 1:], want, err, "f16")
+    del y
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_moe_layer_weights_past_4_gb(packed):
+    """300 experts of 7168 x 2048, 6.6 GB of gate and up codes: the last experts' outputs
+    against a layer of these alone."""
+    experts, hidden, inter, last = 300, 7168, 2048, 6
+    g = torch.Generator(device="cuda").manual_seed(59)
+    byte = lambda *s: torch.randint(0, 256, s, dtype=torch.uint8, device="cuda", generator=g)
+    scale = lambda *s: torch.randint(0x20, 0x48, s, dtype=torch.uint8, device="cuda", generator=g)
+    c13, s13 = byte(2 * experts, inter, hidden // 2), scale(2 * experts, inter, hidden // 16)
+    c2, s2 = byte(experts, hidden, inter // 2), scale(experts, hidden, inter // 16)
+    a13, a2 = torch.full((experts, 2), 0.01, device="cuda"), torch.full((experts,), 0.01, device="cuda")
+    bias = torch.zeros(experts, device="cuda")
+    bias[:experts - last] = -float("inf")
+    router = torch.randn((experts, hidden), device="cuda", generator=g).to(torch.bfloat16)
+    pack = pd.pack_weight if packed else lambda c, s: (c.contiguous(), s.contiguous())
+    whole = pd.MoeLayer(router, *pack(c13, s13), *pack(c2, s2), inter=inter, topk=3, alpha13=a13, alpha2=a2,
+                        route_bias=bias, scoring="sigmoid", packed=packed)
+    f = experts - last
+    alone = pd.MoeLayer(router[f:].contiguous(), *pack(c13[2 * f:], s13[2 * f:]), *pack(c2[f:], s2[f:]), inter=inter,
+                        topk=3, alpha13=a13[f:], alpha2=a2[f:], route_bias=bias[f:], scoring="sigmoid", packed=packed)
+    for tokens in (1, 24):
+        x = torch.randn((tokens, hidden), device="cuda", generator=g).to(torch.bfloat16)
+        got, want = (pd.moe_layer(x, v, out_dtype=torch.float32) for v in (whole, alone))
+        # sums of other workgroup shapes may round in another order
+        assert float((got - want).abs().max()) <= 1e-5 * float(want.abs().max())
+        assert bool(got.isfinite().all()) and float(want.abs().max()) > 0
+
+
+@pytest.mark.parametrize("experts,topk,hidden,inter", [(1024, 64, 16, 16), (70, 33, 128, 64), (100, 16, 128, 64),
+                                                       (9, 9, 64, 64)])
+def test_moe_layer_few_tokens_many_experts_each(experts, topk, hidden, inter):
+    """More experts a token than the down product's workgroup has waves."""
+    rng = np.random.default_rng(60 + topk)
+    for tokens in (1, 2):
+        moe_case(rng, tokens, experts, topk, hidden, inter, residual="apart")
+        moe_case(rng, tokens, experts, topk, hidden, inter, x="f16", y="f32", scoring="sigmoid", route_bias=True)
+
+
+def test_moe_layer_slots_past_2_gb():
+    """h of more than 2^31 bytes a plane, past the stream kernel's offsets: against calls of
+    fewer tokens."""
+    tokens, experts, topk, hidden, inter = 65535, 16, 8, 64, 2064
+    rng = np.random.default_rng(61)
+    c13, s13 = weight(rng, 2 * experts, inter, hidden)
+    c2, s2 = weight(rng, experts, hidden, inter)
+    dev = lambda v: torch.from_numpy(v).cuda()
+    layer = pd.MoeLayer(dev(rng.standard_normal((experts, hidden))).to(torch.bfloat16), dev(c13), dev(s13), dev(c2), dev(s2),
+                        inter=inter, topk=topk, alpha13=torch.full((experts, 2), 0.01, device="cuda"),
+                        alpha2=torch.full((experts,), 0.01, device="cuda"))
+    assert tokens * topk * inter * 2 > 1 << 31
+    x = dev(rng.standard_normal((tokens, hidden))).to(torch.bfloat16)
+    got = torch.empty((tokens, hidden), dtype=torch.float32, device="cuda")
+    need = pd.nvfp4_moe_layer_workspace_size(layer, tokens)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")    # not the library's, which would keep it
+    pd.nvfp4_moe_layer_launch_ws(layer, x, hidden, None, hidden, got, pd.NVFP4_OUT_F32, hidden, tokens, ws, need)
+    for first in range(0, tokens, 16384):
+        want = pd.moe_layer(x[first:first + 16384], layer, out_dtype=torch.float32)
+        part = got[first:first + 16384]
+        assert float((part - want).abs().max()) <= 1e-5 * float(want.abs().max()), first
+    del ws
