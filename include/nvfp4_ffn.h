@@ -131,7 +131,8 @@ int nvfp4_linear_launch_ws(const void *X, int32_t x_type, int64_t ldx,
  * The same with the library-owned per-(device, stream) workspace of
  * nvfp4_gemv_launch (grown on first need without synchronising; a call that
  * must grow it while `stream` is being captured returns WORKSPACE: see
- * nvfp4_workspace_reserve).
+ * nvfp4_workspace_reserve; what nvfp4_gemv_launch says of graphs that run at the
+ * same time holds here).
  */
 int nvfp4_linear_launch(const void *X, int32_t x_type, int64_t ldx,
                         const uint8_t *W, const uint8_t *sfW, int32_t w_layout,

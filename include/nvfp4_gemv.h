@@ -82,7 +82,11 @@ const char *nvfp4_gemv_status_string(int status);
  * nothing.  Calls that need no more than the workspace holds allocate nothing
  * and are capture-safe; nvfp4_workspace_reserve sizes the workspace before a
  * capture.  Callers that must never allocate use nvfp4_gemv_launch_ws.
- * Concurrent calls on different streams never share a workspace.
+ * Concurrent calls on different streams never share a workspace.  Work captured
+ * into a graph keeps that of the stream it was captured on, wherever the graph is
+ * launched: it must not run at the same time as other graphs captured on that
+ * stream or calls made on it (with nvfp4_gemv_launch_ws each graph can have a
+ * workspace of its own).
  *
  * Returns NVFP4_GEMV_OK or a negative status.
  */
@@ -116,9 +120,11 @@ int nvfp4_gemv_launch_ws(const uint8_t *A_packed, const uint8_t *sfA,
  * Grows the library-owned workspace of (current device, `stream`) to at least
  * `bytes` bytes, so that later calls on `stream` needing no more than that
  * allocate nothing (for instance under graph capture).  The workspace serves
- * nvfp4_gemv_launch, nvfp4_gemm_smalln_launch(_packed), nvfp4_quantize_weight
- * and nvfp4_gemv_bf16x_launch on that stream; take `bytes` from
- * nvfp4_gemv_workspace_size or the plan calls.  Not capture-safe itself.
+ * nvfp4_gemv_launch, nvfp4_gemm_smalln_launch(_packed), nvfp4_quantize_weight,
+ * nvfp4_gemv_bf16x_launch, nvfp4_linear_launch and nvfp4_moe_layer_launch on that
+ * stream; take `bytes` from nvfp4_gemv_workspace_size, the plan calls,
+ * nvfp4_linear_workspace_size or nvfp4_moe_layer_workspace_size.  Not capture-safe
+ * itself.
  * Returns NVFP4_GEMV_OK, NVFP4_GEMV_ERR_DEVICE (no current device) or
  * NVFP4_GEMV_ERR_WORKSPACE (allocation failed, or `stream` is capturing).
  */
