@@ -1,8 +1,8 @@
 """ctypes binding of ``libnvfp4_gemv.so`` (argument marshalling only).
 
 Each C entry point of ``include/nvfp4_gemv.h``, ``include/nvfp4_quantize.h``,
-``include/nvfp4_mma.h`` and ``include/nvfp4_ffn.h`` has a Python function of
-the same name.  Pointer arguments accept a torch tensor (its ``data_ptr()``), a raw
+``include/nvfp4_mma.h``, ``include/nvfp4_ffn.h`` and ``include/nvfp4_attn.h`` has a
+Python function of the same name.  Pointer arguments accept a torch tensor (its ``data_ptr()``), a raw
 integer device address, or None where the C side allows NULL; ``stream``
 accepts None (torch's current stream), a ``torch.cuda.Stream`` or a raw
 ``hipStream_t`` integer.  A negative status raises :class:`Nvfp4GemvError`.
@@ -96,6 +96,12 @@ EXPORTED = (
     "nvfp4_moe_layer_workspace_size",
     "nvfp4_moe_layer_launch_ws",
     "nvfp4_moe_layer_launch",
+    "nvfp4_kv_write_launch",
+    "nvfp4_kv_read_launch",
+    "nvfp4_qk_norm_rope_launch",
+    "nvfp4_kv_attention_workspace_size",
+    "nvfp4_kv_attention_launch_ws",
+    "nvfp4_kv_attention_launch",
 )
 
 
@@ -134,6 +140,15 @@ class MoeLayerStruct(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("scoring", ctypes.c_int32),
                 ("renormalize", ctypes.c_int32), ("routed_scale", ctypes.c_float),
                 ("reserved", ctypes.c_int32)]
+
+
+class KvCacheStruct(ctypes.Structure):
+    """Mirror of ``nvfp4_kv_cache_t``."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("k_global", ctypes.c_void_p), ("v_global", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
 
 
 _lib = None
@@ -231,6 +246,23 @@ def load():
     lib.nvfp4_moe_layer_launch_ws.argtypes = moe_args + [_P, ctypes.c_size_t, _P]
     lib.nvfp4_moe_layer_launch.restype = ctypes.c_int
     lib.nvfp4_moe_layer_launch.argtypes = moe_args + [_P]
+    cache = ctypes.POINTER(KvCacheStruct)
+    lib.nvfp4_kv_write_launch.restype = ctypes.c_int
+    lib.nvfp4_kv_write_launch.argtypes = [cache, _P, _I64, _I64, _P, _I64, _I64, I32, _P, _I64, I32, _P]
+    lib.nvfp4_kv_read_launch.restype = ctypes.c_int
+    lib.nvfp4_kv_read_launch.argtypes = [cache, _P, _I64, _P, _P, I32, _P]
+    lib.nvfp4_qk_norm_rope_launch.restype = ctypes.c_int
+    lib.nvfp4_qk_norm_rope_launch.argtypes = [
+        _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, I32, _P, _P,
+        _I64, _I64, I32, ctypes.c_float, _I64, cache, _P, _I64, _I64, _P, I32, _P]
+    lib.nvfp4_kv_attention_workspace_size.restype = ctypes.c_size_t
+    lib.nvfp4_kv_attention_workspace_size.argtypes = [cache, _I64, _I64, _I64, _I64, _I64]
+    attention_args = [cache, _P, _I64, _I64, _P, _I64, _I64, _I64, I32, _P, _I64, _I64, _P, _P, _I64, _I64, _I64,
+                      ctypes.c_float, _I64, _I64]
+    lib.nvfp4_kv_attention_launch_ws.restype = ctypes.c_int
+    lib.nvfp4_kv_attention_launch_ws.argtypes = attention_args + [_P, ctypes.c_size_t, _P]
+    lib.nvfp4_kv_attention_launch.restype = ctypes.c_int
+    lib.nvfp4_kv_attention_launch.argtypes = attention_args + [_P]
     _lib = lib
     return lib
 
@@ -814,4 +846,284 @@ def moe_layer(x, layer, residual=None, out=None, out_dtype=None, stream=None):
         _enqueue(load().nvfp4_moe_layer_launch,
                  (layer.reference, x.data_ptr(), ldx, _address(residual), ldr, out.data_ptr(), y_type, ldy, n),
                  layer.device, stream, "nvfp4_moe_layer_launch")
+    return out
+
+
+# ---- attention operators on an NVFP4 cache (include/nvfp4_attn.h)
+
+def _cache_struct(cache):
+    return None if cache is None else ctypes.byref(cache.struct if isinstance(cache, KvCache) else cache)
+
+
+def nvfp4_kv_write_launch(cache, K, k_token_stride, k_head_stride, V, v_token_stride, v_head_stride, x_type,
+                          slots, tokens, rule, stream=None):
+    """``cache`` is a :class:`KvCacheStruct` or a :class:`KvCache`, here and below."""
+    _check(load().nvfp4_kv_write_launch(_cache_struct(cache), _ptr(K), k_token_stride, k_head_stride, _ptr(V),
+                                        v_token_stride, v_head_stride, x_type, _ptr(slots), tokens, int(rule),
+                                        _stream(stream)), "nvfp4_kv_write_launch")
+
+
+def nvfp4_kv_read_launch(cache, slots, tokens, K, V, y_type, stream=None):
+    _check(load().nvfp4_kv_read_launch(_cache_struct(cache), _ptr(slots), tokens, _ptr(K), _ptr(V), y_type,
+                                       _stream(stream)), "nvfp4_kv_read_launch")
+
+
+def nvfp4_qk_norm_rope_launch(Q, q_token_stride, q_head_stride, q_weight, Q_out, qo_token_stride, qo_head_stride,
+                              heads, K, k_token_stride, k_head_stride, k_weight, K_out, ko_token_stride,
+                              ko_head_stride, kv_heads, head_dim, x_type, positions, cos_sin, table_rows, rot_dim,
+                              interleaved, eps, tokens, cache=None, V=None, v_token_stride=0, v_head_stride=0,
+                              slots=None, rule=NVFP4_ROUND_NEAREST_EVEN, stream=None):
+    _check(load().nvfp4_qk_norm_rope_launch(
+        _ptr(Q), q_token_stride, q_head_stride, _ptr(q_weight), _ptr(Q_out), qo_token_stride, qo_head_stride, heads,
+        _ptr(K), k_token_stride, k_head_stride, _ptr(k_weight), _ptr(K_out), ko_token_stride, ko_head_stride,
+        kv_heads, head_dim, x_type, _ptr(positions), _ptr(cos_sin), table_rows, rot_dim, int(interleaved), eps,
+        tokens, _cache_struct(cache), _ptr(V), v_token_stride, v_head_stride, _ptr(slots), int(rule),
+        _stream(stream)), "nvfp4_qk_norm_rope_launch")
+
+
+def nvfp4_kv_attention_workspace_size(cache, heads, batch, tokens, max_query, table_width) -> int:
+    return int(load().nvfp4_kv_attention_workspace_size(_cache_struct(cache), heads, batch, tokens, max_query,
+                                                        table_width))
+
+
+def nvfp4_kv_attention_launch_ws(cache, Q, q_token_stride, q_head_stride, out, o_token_stride, o_head_stride, heads,
+                                 x_type, block_table, table_stride, table_width, lengths, query_starts, batch,
+                                 tokens, max_query, scale, window, sinks, workspace, workspace_bytes, stream=None):
+    _check(load().nvfp4_kv_attention_launch_ws(
+        _cache_struct(cache), _ptr(Q), q_token_stride, q_head_stride, _ptr(out), o_token_stride, o_head_stride,
+        heads, x_type, _ptr(block_table), table_stride, table_width, _ptr(lengths), _ptr(query_starts), batch,
+        tokens, max_query, scale, window, sinks, _ptr(workspace), int(workspace_bytes), _stream(stream)),
+        "nvfp4_kv_attention_launch_ws")
+
+
+def nvfp4_kv_attention_launch(cache, Q, q_token_stride, q_head_stride, out, o_token_stride, o_head_stride, heads,
+                              x_type, block_table, table_stride, table_width, lengths, query_starts, batch, tokens,
+                              max_query, scale, window, sinks, stream=None):
+    _check(load().nvfp4_kv_attention_launch(
+        _cache_struct(cache), _ptr(Q), q_token_stride, q_head_stride, _ptr(out), o_token_stride, o_head_stride,
+        heads, x_type, _ptr(block_table), table_stride, table_width, _ptr(lengths), _ptr(query_starts), batch,
+        tokens, max_query, scale, window, sinks, _stream(stream)), "nvfp4_kv_attention_launch")
+
+
+class KvCache:
+    """A paged key/value cache held in NVFP4 (``nvfp4_kv_cache_t``); keeps the
+    tensors it names alive, which are all on one GPU.
+
+    Codes uint8 (pages, kv_heads, page_size, dp / 2) and scales uint8 (pages,
+    kv_heads, dp / 16, page_size), dp = head_dim rounded up to 64; k_global and
+    v_global float32 (kv_heads,), optional.  :meth:`empty` allocates them.
+    """
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, head_dim, k_global=None, v_global=None):
+        import torch
+
+        if k_codes.dim() != 4 or not k_codes.is_cuda:
+            raise ValueError("k_codes must be a (pages, kv_heads, page_size, dp / 2) device tensor")
+        pages, kv_heads, page_size, half = k_codes.shape
+        if half != -(-head_dim // 64) * 32:
+            raise ValueError(f"codes of head_dim {head_dim} have {-(-head_dim // 64) * 32} bytes a token")
+        self.device = k_codes.get_device()
+        for name, t, shape in (("k_codes", k_codes, k_codes.shape), ("v_codes", v_codes, k_codes.shape),
+                               ("k_scales", k_scales, (pages, kv_heads, half // 8, page_size)),
+                               ("v_scales", v_scales, (pages, kv_heads, half // 8, page_size))):
+            if t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device:
+                raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {tuple(shape)} on GPU {self.device}")
+        _floats(k_global, kv_heads, "k_global", self.device)
+        _floats(v_global, kv_heads, "v_global", self.device)
+        self.tensors = (k_codes, k_scales, v_codes, v_scales, k_global, v_global)
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, kv_heads, page_size, head_dim
+        self.struct = KvCacheStruct(
+            k_codes=_ptr(k_codes), k_scales=_ptr(k_scales), v_codes=_ptr(v_codes), v_scales=_ptr(v_scales),
+            k_global=_ptr(k_global), v_global=_ptr(v_global), pages=pages, page_size=page_size, kv_heads=kv_heads,
+            head_dim=head_dim)
+        self.reference = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page_size, head_dim, device="cuda", k_global=None, v_global=None):
+        """A cache of that shape whose slots hold zeros."""
+        import torch
+
+        dp = -(-head_dim // 64) * 64
+        codes = (pages, kv_heads, page_size, dp // 2)
+        scales = (pages, kv_heads, dp // 16, page_size)
+        return cls(*(torch.zeros(s, dtype=torch.uint8, device=device) for s in (codes, scales, codes, scales)),
+                   head_dim=head_dim, k_global=k_global, v_global=v_global)
+
+
+def _head_rows(t, what, tokens, heads, dim, dtype, device):
+    """Token and head strides of a (tokens, heads, dim) tensor on that GPU with contiguous rows."""
+    if t.shape != (tokens, heads, dim) or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{what} must be a tensor on GPU {device} of shape {(tokens, heads, dim)} and {dtype}")
+    token, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    # the stride of a dimension of one is free; torch reports anything there
+    return (token if tokens > 1 else heads * dim), (head if heads > 1 else dim)
+
+
+def _integers(t, what, shape, dtype, device):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape} on GPU {device}")
+
+
+def _heads_of(t, what):
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be (tokens, heads, head_dim)")
+    if t.get_device() < 0:
+        raise ValueError(f"{what} must be on a GPU")
+
+
+def kv_cache_write(k, v, cache, slots, rule=NVFP4_ROUND_NEAREST_EVEN, stream=None):
+    """Quantises k and v, (tokens, kv_heads, head_dim) bfloat16 or float16 with any
+    token and head strides, into ``slots`` (int64, page * page_size + offset; a
+    negative one leaves its token out; each at most once) of a :class:`KvCache`.
+    GPU and stream as in :func:`linear`."""
+    import torch
+
+    _heads_of(k, "k")
+    n = k.shape[0]
+    x_type = _float_type(k.dtype, "k")
+    kt, kh = _head_rows(k, "k", n, cache.kv_heads, cache.head_dim, k.dtype, cache.device)
+    vt, vh = _head_rows(v, "v", n, cache.kv_heads, cache.head_dim, k.dtype, cache.device)
+    _integers(slots, "slots", (n,), torch.int64, cache.device)
+    if n > 0:
+        _enqueue(load().nvfp4_kv_write_launch, (cache.reference, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, x_type,
+                                                slots.data_ptr(), n, rule), cache.device, stream,
+                 "nvfp4_kv_write_launch")
+
+
+def kv_cache_read(cache, slots, out_dtype=None, stream=None):
+    """Values of the slots (int64; one outside the cache gives zeros) of a
+    :class:`KvCache`: k and v, (n, kv_heads, head_dim) of ``out_dtype`` (bfloat16,
+    float16 or float32; default bfloat16).  GPU and stream as in :func:`linear`."""
+    import torch
+
+    dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    y_type = _float_type(dtype, "out_dtype", f32=True)
+    if slots.dim() != 1:
+        raise ValueError("slots must be one-dimensional")
+    n = slots.shape[0]
+    _integers(slots, "slots", (n,), torch.int64, cache.device)
+    shape = (n, cache.kv_heads, cache.head_dim)
+    k = _allocate(shape, dtype, slots.device, stream)
+    v = _allocate(shape, dtype, slots.device, stream)
+    if n > 0:
+        _enqueue(load().nvfp4_kv_read_launch, (cache.reference, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), y_type),
+                 cache.device, stream, "nvfp4_kv_read_launch")
+    return k, v
+
+
+def qk_norm_rope(q, k, positions=None, cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None, v=None, cache=None, slots=None, rule=NVFP4_ROUND_NEAREST_EVEN, stream=None):
+    """Head norms and position rotation of queries and keys in one pass.
+
+    q (tokens, heads, head_dim) and k (tokens, kv_heads, head_dim) bfloat16 or
+    float16 with any token and head strides; positions int64 (tokens,); cos_sin
+    float32 (table rows, rot_dim), rot_dim / 2 cosines, then as many sines, rot_dim
+    a multiple of 16 up to head_dim, neither where nothing is rotated; q_weight,
+    k_weight float32 (head_dim,), rows without one are not normalised.  The
+    outputs may be q and k themselves.  With ``cache`` (a :class:`KvCache`), v and
+    slots as in :func:`kv_cache_write`, k and v go into the cache instead.  Returns
+    (q, k), with a cache (q, None).  GPU and stream as in :func:`linear`.
+    """
+    import torch
+
+    _heads_of(q, "q")
+    n, heads, dim = q.shape
+    device = q.get_device()
+    x_type = _float_type(q.dtype, "q")
+    if k.dim() != 3:
+        raise ValueError("k must be (tokens, kv_heads, head_dim)")
+    kv_heads = k.shape[1]
+    qt, qh = _head_rows(q, "q", n, heads, dim, q.dtype, device)
+    kt, kh = _head_rows(k, "k", n, kv_heads, dim, q.dtype, device)
+    _floats(q_weight, dim, "q_weight", device)
+    _floats(k_weight, dim, "k_weight", device)
+    rows = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or \
+                cos_sin.get_device() != device:
+            raise ValueError(f"cos_sin must be a contiguous float32 (table rows, rot_dim) tensor on GPU {device}")
+        rows, rot = cos_sin.shape
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+    if positions is not None:
+        _integers(positions, "positions", (n,), torch.int64, device)
+    if (cache is None) != (v is None) or (cache is None) != (slots is None):
+        raise ValueError("cache, v and slots go together")
+    vt = vh = kot = koh = 0
+    if cache is not None:
+        if cache.device != device:
+            raise ValueError(f"cache must be on GPU {device}, as q")
+        if (cache.kv_heads, cache.head_dim) != (kv_heads, dim):
+            raise ValueError(f"cache has {cache.kv_heads} heads of {cache.head_dim}, k has {kv_heads} of {dim}")
+        if k_out is not None:
+            raise ValueError("k goes into the cache: k_out must be left out")
+        vt, vh = _head_rows(v, "v", n, kv_heads, dim, q.dtype, device)
+        _integers(slots, "slots", (n,), torch.int64, device)
+    elif k_out is None:
+        k_out = _allocate((n, kv_heads, dim), q.dtype, q.device, stream)
+        kot, koh = kv_heads * dim, dim
+    else:
+        kot, koh = _head_rows(k_out, "k_out", n, kv_heads, dim, q.dtype, device)
+    if q_out is None:
+        q_out = _allocate((n, heads, dim), q.dtype, q.device, stream)
+        qot, qoh = heads * dim, dim
+    else:
+        qot, qoh = _head_rows(q_out, "q_out", n, heads, dim, q.dtype, device)
+    if n > 0:
+        _enqueue(load().nvfp4_qk_norm_rope_launch, (
+            q.data_ptr(), qt, qh, _address(q_weight), q_out.data_ptr(), qot, qoh, heads, k.data_ptr(), kt, kh,
+            _address(k_weight), _address(k_out), kot, koh, kv_heads, dim, x_type, _address(positions),
+            _address(cos_sin), rows, rot, int(bool(interleaved)), eps, n, None if cache is None else cache.reference,
+            _address(v), vt, vh, _address(slots), rule), device, stream, "nvfp4_qk_norm_rope_launch")
+    return q_out, k_out
+
+
+def kv_attention(q, cache, block_table, lengths, query_starts=None, max_query=None, scale=None, window=0, sinks=0,
+                 out=None, stream=None):
+    """Causal attention of q over a :class:`KvCache`.
+
+    q (tokens, heads, head_dim) bfloat16 or float16 with any token and head
+    strides; block_table int32 (batch, pages of a sequence) with any row stride;
+    lengths int32 (batch,), tokens in the cache, those of the queries included;
+    query_starts int32 (batch + 1,), the first query of each sequence and the end
+    of the last, or None for tokens / batch queries each; max_query a bound on a
+    sequence's queries (default: tokens / batch, with query_starts all tokens);
+    scale defaults to head_dim ** -0.5; window the number of tokens that a query
+    sees (0: all), sinks the first tokens that stay visible.  Returns
+    (tokens, heads, head_dim) of q's type; rows that belong to no sequence are
+    left as they were.  GPU and stream as in :func:`linear`.
+    """
+    import torch
+
+    _heads_of(q, "q")
+    n, heads, dim = q.shape
+    device = q.get_device()
+    x_type = _float_type(q.dtype, "q")
+    if cache.device != device or cache.head_dim != dim:
+        raise ValueError(f"cache must be on GPU {device} and have heads of {dim}, as q")
+    qt, qh = _head_rows(q, "q", n, heads, dim, q.dtype, device)
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32 or block_table.get_device() != device or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be an int32 (batch, pages) tensor on GPU {device} with contiguous rows")
+    batch, width = block_table.shape
+    _integers(lengths, "lengths", (batch,), torch.int32, device)
+    if query_starts is not None:
+        _integers(query_starts, "query_starts", (batch + 1,), torch.int32, device)
+    elif batch < 1 or n % batch != 0:
+        raise ValueError(f"{n} queries of {batch} sequences: query_starts is needed")
+    if max_query is None:
+        max_query = max(1, n if query_starts is not None else n // batch)
+    if out is None:
+        out = _allocate((n, heads, dim), q.dtype, q.device, stream)
+        ot, oh = heads * dim, dim
+    else:
+        ot, oh = _head_rows(out, "out", n, heads, dim, q.dtype, device)
+    if n > 0:
+        _enqueue(load().nvfp4_kv_attention_launch, (
+            cache.reference, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh, heads, x_type, block_table.data_ptr(),
+            block_table.stride(0) if batch > 1 else width, width, lengths.data_ptr(), _address(query_starts), batch, n,
+            max_query, dim ** -0.5 if scale is None else scale, window, sinks), device, stream,
+            "nvfp4_kv_attention_launch")
     return out

@@ -1,0 +1,148 @@
+// Host-side plan of the attention operators on an NVFP4 cache: argument checks,
+// kernel choice, grids and workspace layout.
+//
+// Plain C++17 with no HIP types, so that the same code is compiled into the
+// library (nvfp4_attn.hip) and into a host-only check built with g++ and the
+// address and undefined-behaviour sanitizers.  Not part of the C ABI.
+#ifndef NVFP4_ATTN_PLAN_H
+#define NVFP4_ATTN_PLAN_H
+
+#include <climits>
+#include <cstddef>
+#include <cstdint>
+
+#include "nvfp4_attn.h"
+
+namespace nvfp4attnplan {
+
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxTokens = (int64_t(1) << 24) - 1;
+constexpr int64_t kMaxHeads = 16384, kMaxKvHeads = 1024, kMaxBatch = 65535;
+constexpr int64_t kStepTokens = 64;                // cache tokens of one step of the attention kernels
+constexpr int64_t kComputeUnits = 256;             // CUs of an MI355X (8 XCDs x 32)
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t padded_dim(int64_t d) { return ceil_div(d, 64) * 64; }
+inline bool mul_fits(int64_t a, int64_t b) { return a == 0 || b <= INT64_MAX / a; }
+
+inline int log2_of(int64_t v) {
+    int n = 0;
+    while ((int64_t(1) << n) < v) ++n;
+    return n;
+}
+
+inline int check_dims(int64_t kv_heads, int64_t head_dim) {
+    return kv_heads < 1 || kv_heads > kMaxKvHeads || head_dim < 16 || head_dim > 256 || head_dim % 16 != 0
+               ? NVFP4_GEMV_ERR_BAD_SHAPE
+               : NVFP4_GEMV_OK;
+}
+
+inline int check_cache_shape(const nvfp4_kv_cache_t &c) {
+    if (check_dims(c.kv_heads, c.head_dim) != NVFP4_GEMV_OK || c.page_size < 16 || c.page_size > 1024 ||
+        (c.page_size & (c.page_size - 1)) != 0 || c.pages < 1 || c.pages > ((int64_t(1) << 31) - 1) / c.page_size)
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    return NVFP4_GEMV_OK;
+}
+
+// Bytes of each code and scale buffer of a cache whose shape has been checked
+// (below 2^31 * 2^10 * 2^7).
+inline int64_t code_bytes(const nvfp4_kv_cache_t &c) {
+    return c.pages * c.page_size * c.kv_heads * (padded_dim(c.head_dim) / 2);
+}
+inline int64_t scale_bytes(const nvfp4_kv_cache_t &c) { return code_bytes(c) / 8; }
+
+// tokens x heads rows of `dim` elements.
+struct Grid {
+    const void *p;
+    int64_t token, head;          // strides in elements
+    int64_t tokens, heads, dim;
+    int bytes;                    // of an element
+};
+
+inline int64_t extent(const Grid &g) {   // elements from the first to past the last
+    return g.tokens == 0 ? 0 : (g.tokens - 1) * g.token + (g.heads - 1) * g.head + g.dim;
+}
+inline int check_strides(const Grid &g) {
+    if (g.token < 0 || g.head < 0 || g.token > kMaxStride || g.head > kMaxStride) return NVFP4_GEMV_ERR_BAD_SHAPE;
+    if (g.tokens > 1 && !mul_fits(g.tokens - 1, g.token)) return NVFP4_GEMV_ERR_BAD_SHAPE;
+    const int64_t e = g.tokens > 1 ? (g.tokens - 1) * g.token : 0;
+    const int64_t h = (g.heads - 1) * g.head + g.dim;   // at most 2^14 * 2^40
+    return e > INT64_MAX / 8 - h ? NVFP4_GEMV_ERR_BAD_SHAPE : NVFP4_GEMV_OK;
+}
+// Whether no two rows of the grid share an element: heads within a token's stride
+// or tokens within a head's.
+inline bool rows_apart(const Grid &g) {
+    const bool heads_apart = g.heads == 1 || g.head >= g.dim, tokens_apart = g.tokens <= 1 || g.token >= g.dim;
+    if (!heads_apart || !tokens_apart) return false;
+    return g.heads == 1 || g.tokens <= 1 || g.token >= (g.heads - 1) * g.head + g.dim ||
+           g.head >= (g.tokens - 1) * g.token + g.dim;
+}
+// Whether a row of one may share an element with a row of the other.  Grids of
+// the same token stride, each token's rows within it, may lie between each
+// other: the parts of one projection's output.
+inline bool grids_overlap(const Grid &a, const Grid &b) {
+    const int64_t as = extent(a) * a.bytes, bs = extent(b) * b.bytes;
+    if (!a.p || !b.p || as <= 0 || bs <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    if (x >= y + static_cast<uintptr_t>(bs) || y >= x + static_cast<uintptr_t>(as)) return false;
+    const int64_t aw = ((a.heads - 1) * a.head + a.dim) * a.bytes, bw = ((b.heads - 1) * b.head + b.dim) * b.bytes;
+    const int64_t at = a.token * a.bytes, bt = b.token * b.bytes;
+    if (at != bt || aw > at || bw > bt) return true;
+    const uintptr_t stride = static_cast<uintptr_t>(at);
+    const uintptr_t apart = y >= x ? (y - x) % stride : (stride - (x - y) % stride) % stride;
+    return apart < static_cast<uintptr_t>(aw) || apart + static_cast<uintptr_t>(bw) > stride;
+}
+
+inline int64_t span_of(const Grid &g) { return extent(g) * g.bytes; }
+
+// ---------------------------------------------------------------- attention
+// Query rows (tokens times heads of one kv head) that a workgroup of the stream
+// kernel holds: 16, 32 or 64, the last where its sums fit the registers.
+inline int64_t stream_rows(int64_t dp) { return dp <= 128 ? 64 : 32; }
+
+constexpr int64_t kStreamGroups = 3 * kComputeUnits;   // workgroups that share the cache's steps
+
+struct AttnPlan {
+    bool shared;          // the steps of all sequences are dealt out evenly over the workgroups
+    int64_t rows;         // query rows of a workgroup
+    int64_t groups;       // workgroups
+    size_t part_bytes, ml_bytes, prefix_bytes;
+    size_t ws_bytes() const { return part_bytes + ml_bytes + prefix_bytes; }
+};
+
+// max_query: bound on a sequence's queries; steps: bound on its steps of the cache.
+inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t batch, int64_t tokens,
+                          int64_t max_query, int64_t max_context) {
+    AttnPlan p = {};
+    const int64_t dp = padded_dim(head_dim), group = heads / kv_heads, rows = max_query * group;
+    const int64_t steps = ceil_div(max_context, kStepTokens);
+    const int64_t most = stream_rows(dp);
+    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : most;
+    if (rows <= most && steps > 8) {
+        p.shared = true;
+        p.groups = kStreamGroups;
+        p.part_bytes = static_cast<size_t>(2 * p.groups * p.rows * dp) * 4;
+        p.ml_bytes = static_cast<size_t>(2 * p.groups * p.rows * 2) * 4;
+        p.prefix_bytes = static_cast<size_t>(batch + 1) * 8;
+    } else {
+        // tiles of a sequence: ceil(queries * group / rows), over all sequences at most
+        const int64_t tiles = rows <= most ? batch : tokens * group / p.rows + batch;
+        p.groups = tiles * kv_heads;
+    }
+    return p;
+}
+
+inline int check_attn_shape(const nvfp4_kv_cache_t &c, int64_t heads, int64_t batch, int64_t tokens,
+                            int64_t max_query, int64_t table_width) {
+    if (check_cache_shape(c) != NVFP4_GEMV_OK || heads < c.kv_heads || heads > kMaxHeads ||
+        heads % c.kv_heads != 0 || tokens < 0 || tokens > kMaxTokens || tokens * heads >= (int64_t(1) << 31) ||
+        batch < 1 || batch > kMaxBatch || batch * c.kv_heads >= (int64_t(1) << 24) || max_query < 1 ||
+        (tokens > 0 && max_query > tokens) || table_width < 1 ||
+        table_width > ((int64_t(1) << 31) - 1) / c.page_size)
+        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    return NVFP4_GEMV_OK;
+}
+
+}  // namespace nvfp4attnplan
+
+#endif  // NVFP4_ATTN_PLAN_H
