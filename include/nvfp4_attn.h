@@ -147,7 +147,7 @@ int nvfp4_qk_norm_rope_launch(const void *Q, int64_t q_token_stride, int64_t q_h
  * power of two of its row to fit fp16, where e2m1 * e4m3 is exact), softmax
  * statistics and sums are fp32, and the weights meet v rounded to fp16 after
  * scaling, 2^-11 relative; results do not depend on other sequences' values.
- * table_width * page_size < 2^31, batch from 1 to 65535, batch * kv_heads < 2^24,
+ * table_width * page_size < 2^31, batch from 1 to 65535, batch * kv_heads < 2^22,
  * batch and strides of block_table non-negative, scale finite.
  */
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache_t *cache, int64_t heads, int64_t batch,

@@ -19,6 +19,7 @@
 #include <cstdint>
 #include <utility>
 
+#include "attn_plan.h"
 #include "cache_kernels.h"
 #include "device_common.h"
 
@@ -27,6 +28,7 @@ namespace nvfp4attn {
 using nvfp4dev::f16x8;
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * kWave;
@@ -55,7 +57,11 @@ struct Sequence {
     int len, first, n, computed;   // cache tokens, first query's row of Q, queries, queries that are computed
 };
 
-__device__ __forceinline__ int steps_of(int tokens) { return (tokens >> 6) + ((tokens & 63) != 0 ? 1 : 0); }
+// Steps of 2^LOG tokens that hold `tokens` of them.
+template <int LOG>
+__device__ __forceinline__ int steps_of(int tokens) {
+    return (tokens >> LOG) + ((tokens & ((1 << LOG) - 1)) != 0 ? 1 : 0);
+}
 
 __device__ __forceinline__ Sequence sequence_of(const AttnArgs &a, int b) {
     Sequence s;
@@ -84,6 +90,7 @@ struct Steps {
     __device__ __forceinline__ int at(int i) const { return i < sinks ? i : from + (i - sinks); }
 };
 
+template <int LOG>
 __device__ __forceinline__ Steps steps_for(const AttnArgs &a, const Sequence &s, int row0, int rows) {
     Steps w = {};
     const int last_row = s.computed * a.group - 1;
@@ -98,10 +105,10 @@ __device__ __forceinline__ Steps steps_for(const AttnArgs &a, const Sequence &s,
         lo = (w.p_first > 0 ? w.p_first : 0) - a.window + 1;
         lo = lo > 0 ? lo : 0;
     }
-    w.from = lo >> 6;
-    const int sinks = steps_of(a.sinks < hi ? a.sinks : hi);
+    w.from = lo >> LOG;
+    const int sinks = steps_of<LOG>(a.sinks < hi ? a.sinks : hi);
     w.sinks = sinks < w.from ? sinks : w.from;
-    w.count = w.sinks + steps_of(hi) - w.from;
+    w.count = w.sinks + steps_of<LOG>(hi) - w.from;
     return w;
 }
 
@@ -123,6 +130,32 @@ __device__ __forceinline__ float xor32(float v, bool take_max) {
 __device__ __forceinline__ float rows_max(float v) { return xor32(xor16(v, true), true); }
 __device__ __forceinline__ float rows_sum(float v) { return xor32(xor16(v, false), false); }
 
+// A power of two that brings magnitude `top` (its pattern; infinities and NaN sort
+// above the numbers) to [2^14, 2^15), and its inverse.
+__device__ __forceinline__ void row_power(uint32_t top, float *up, float *down) {
+    int e = static_cast<int>(top >> 23) - 127;         // -127 (zero, subnormal) .. 128
+    e = e < -100 ? -100 : e > 127 ? 127 : e;
+    *up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+    *down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+}
+
+// Whether a query at position p (-1: none) sees token j.
+__device__ __forceinline__ bool visible(const AttnArgs &a, int p, int j) {
+    return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+}
+
+__device__ __forceinline__ void store4(uint16_t *p, f32x4 v, bool bf16, bool wide) {
+    const uint32_t lo = to16(v[0], bf16) | to16(v[1], bf16) << 16, hi = to16(v[2], bf16) | to16(v[3], bf16) << 16;
+    if (wide) {
+        *reinterpret_cast<u32x2 *>(p) = u32x2{lo, hi};
+    } else {
+        p[0] = static_cast<uint16_t>(lo);
+        p[1] = static_cast<uint16_t>(lo >> 16);
+        p[2] = static_cast<uint16_t>(hi);
+        p[3] = static_cast<uint16_t>(hi >> 16);
+    }
+}
+
 // Lane N of each 16-lane row, to the whole row.
 template <int N>
 __device__ __forceinline__ f16x2 row_bcast(f16x2 v) {
@@ -139,6 +172,19 @@ __device__ __forceinline__ f16x8 decode8(uint32_t w, f16x2 s0, f16x2 s1, f16x2 s
     const f16x2 a = nvfp4dev::e2m1x2_f16<0>(w) * s0, b = nvfp4dev::e2m1x2_f16<1>(w) * s1,
                 c = nvfp4dev::e2m1x2_f16<2>(w) * s2, d = nvfp4dev::e2m1x2_f16<3>(w) * s3;
     return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The lane's number and its 16-lane row.  Not known to be the same from use to use,
+// so that the many addresses of a step are computed in it and not kept in
+// registers through the loop, which has none to spare.
+struct Lane {
+    uint32_t id, r16, h;
+};
+__device__ __forceinline__ Lane this_lane() {
+    uint32_t x = threadIdx.x;
+    __asm__ volatile("" : "+v"(x));
+    x &= kWave - 1;
+    return {x, x & 15, x >> 4};
 }
 
 __device__ __forceinline__ void wave_fence() {
@@ -174,29 +220,36 @@ struct Stream {
     static constexpr int kLaneBlocks = NB / 4;     // scale blocks of a lane's slice of K
     static constexpr int kStage = kStep * kDp / 2; // a wave's V codes in LDS
 
+    // 16 rows times up to 8 blocks of outputs are joined at a time
+    static constexpr int kJoinBlocks = NB < 8 ? NB : NB % 8 == 0 ? 8 : 6;
+    static constexpr int kJoinRow = 16 * kJoinBlocks + 4;
+
     struct Buffers {
-        __attribute__((aligned(16))) uint8_t v[kAttnWaves][kStage];
-        __attribute__((aligned(16))) float o[kAttnWaves][kRows][20];   // one block of 16 outputs, rows padded
+        union {
+            __attribute__((aligned(16))) uint8_t v[kAttnWaves][kStage];
+            __attribute__((aligned(16))) float o[kAttnWaves][16][kJoinRow];
+        };
         float m[kAttnWaves][kRows], l[kAttnWaves][kRows];
     };
 
-    struct Loads {                                 // a step on its way
-        uint32_t k[4][kK];
-        uint32_t ks[kLaneBlocks];
-        u32x4 v[kChunks];
-        u32x4 vs;
-        int page[4];                               // of each run, -1 where nothing is visible
-    };
+    // A step on its way: K's registers are free for the next step once its scores are
+    // there, V's once its codes are in LDS, so that both loads run ahead without a
+    // second set of registers.
+    uint32_t kw[4][kK];
+    uint32_t ks[kLaneBlocks];
+    u32x4 vw[kChunks];
+    u32x4 vsw;
 
-    int lane, wave, r16, h;                        // r16 = lane % 16, h = lane / 16
+    int wave;
     f16x8 q[R][kK];
     float c[R];                                    // scores to log2 units
     int pos[R];
     f32x4 acc[R][NB];
     float m[R], l[R];
 
-    // The pages of step s as lane r16 / 4 sees them (its run's), -1 without one.
+    // The page of step s that lane r16's run r16 / 4 lies in, -1 without one.
     __device__ __forceinline__ int entry(const AttnArgs &a, const int32_t *row, int len, int s) const {
+        const int r16 = this_lane().r16;
         const int token = s * kStep + kRun * (r16 >> 2);
         int i = token >> a.c.page_log2;
         i = i < a.table_width ? i : a.table_width - 1;
@@ -204,74 +257,83 @@ struct Stream {
         return token < len && p >= 0 && p < a.pages ? p : -1;
     }
 
-    __device__ __forceinline__ void load(const AttnArgs &a, int kvh, int s, int e, Loads &x) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x.page[i] = __builtin_amdgcn_readlane(e, 4 * i);
+    // Tokens of all heads before (page, kvh), page 0 for what is not there.
+    static __device__ __forceinline__ uint64_t tokens_before(const AttnArgs &a, int page, int kvh) {
+        return static_cast<uint64_t>(static_cast<uint32_t>(page < 0 ? 0 : page)) *
+                   (static_cast<uint32_t>(a.c.kv_heads) << a.c.page_log2) +
+               (static_cast<uint32_t>(kvh) << a.c.page_log2);
+    }
+    // Lane entry of run i, of all lanes.
+    static __device__ __forceinline__ int page_of(int e, int i) { return __builtin_amdgcn_readlane(e, 4 * i); }
+
+    __device__ __forceinline__ void load_k(const AttnArgs &a, int kvh, int s, int e) {
+        const auto [lane, r16, h] = this_lane();
         const int ps = 1 << a.c.page_log2;
-        const uint32_t page_codes = static_cast<uint32_t>(a.c.kv_heads) << a.c.page_log2;   // tokens of all heads
-        const int tok0 = s * kStep;
-        const int own = e < 0 ? 0 : e;
-        // K: this lane's four tokens
-        {
-            const int off = ((tok0 + kRun * (r16 >> 2)) & (ps - 1)) + 4 * (r16 & 3);
-            const uint64_t at = static_cast<uint64_t>(own) * page_codes + (static_cast<uint32_t>(kvh) << a.c.page_log2);
-            const uint8_t *p = a.c.k_codes + (at + off) * (kDp / 2) + h * (kDp / 8);
+        const uint32_t off = ((s * kStep + kRun * (r16 >> 2)) & (ps - 1)) + 4 * (r16 & 3);
+        const uint64_t at = tokens_before(a, e, kvh);
+        const uint8_t *p = a.c.k_codes + (at + off) * (kDp / 2) + h * (kDp / 8);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if constexpr (kK % 4 == 0) {
+        for (int t = 0; t < 4; ++t) {
+            if constexpr (kK % 4 == 0) {
 #pragma unroll
-                    for (int j = 0; j < kK; j += 4) {
-                        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + t * (kDp / 2) + 4 * j));
-                        x.k[t][j] = w[0]; x.k[t][j + 1] = w[1]; x.k[t][j + 2] = w[2]; x.k[t][j + 3] = w[3];
-                    }
-                } else {
+                for (int j = 0; j < kK; j += 4) {
+                    const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + t * (kDp / 2) + 4 * j));
+                    kw[t][j] = w[0]; kw[t][j + 1] = w[1]; kw[t][j + 2] = w[2]; kw[t][j + 3] = w[3];
+                }
+            } else {
 #pragma unroll
-                    for (int j = 0; j < kK; j += 2) {
-                        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p + t * (kDp / 2) + 4 * j));
-                        x.k[t][j] = w[0]; x.k[t][j + 1] = w[1];
-                    }
+                for (int j = 0; j < kK; j += 2) {
+                    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p + t * (kDp / 2) + 4 * j));
+                    kw[t][j] = w[0]; kw[t][j + 1] = w[1];
                 }
             }
-            const uint8_t *sp = a.c.k_scales + at * NB + off;
+        }
+        const uint8_t *sp = a.c.k_scales + at * NB + off;
 #pragma unroll
-            for (int j = 0; j < kLaneBlocks; ++j)
-                x.ks[j] = *reinterpret_cast<const uint32_t *>(sp + ((h * kLaneBlocks + j) << a.c.page_log2));
-        }
-        // V: pieces of 16 bytes in memory order
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int at = i * kWave + lane, token = at / kChunks, piece = at % kChunks;
-            const int run = token >> 4;
-            int p = run == 0 ? x.page[0] : run == 1 ? x.page[1] : run == 2 ? x.page[2] : x.page[3];
-            p = p < 0 ? 0 : p;
-            const uint64_t base = static_cast<uint64_t>(p) * page_codes + (static_cast<uint32_t>(kvh) << a.c.page_log2);
-            const uint8_t *vp = a.c.v_codes + (base + ((tok0 + token) & (ps - 1))) * (kDp / 2) + 16 * piece;
-            x.v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(vp));
-        }
-        // V's scales: lane r16 of run h takes block r16, 16 tokens
-        {
-            int p = h == 0 ? x.page[0] : h == 1 ? x.page[1] : h == 2 ? x.page[2] : x.page[3];
-            p = p < 0 ? 0 : p;
-            const uint64_t base = static_cast<uint64_t>(p) * page_codes + (static_cast<uint32_t>(kvh) << a.c.page_log2);
-            const int b = r16 < NB ? r16 : NB - 1;
-            x.vs = *reinterpret_cast<const u32x4 *>(a.c.v_scales + base * NB + (b << a.c.page_log2) +
-                                                    ((tok0 + kRun * h) & (ps - 1)));
-        }
+        for (int j = 0; j < kLaneBlocks; ++j)
+            ks[j] = *reinterpret_cast<const uint32_t *>(sp + ((h * kLaneBlocks + j) << a.c.page_log2));
     }
 
-    static __device__ __forceinline__ int piece_at(int token, int piece) {
+    __device__ __forceinline__ void load_v(const AttnArgs &a, int kvh, int s, int e) {
+        const auto [lane, r16, h] = this_lane();
+        const int ps = 1 << a.c.page_log2, tok0 = s * kStep;
+        // pieces of 16 bytes in memory order
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const uint32_t at = i * kWave + lane, token = at / kChunks, piece = at % kChunks;
+            uint64_t base;
+            uint32_t off;
+            if constexpr (kWave / kChunks == kRun) {          // the lanes share a run
+                base = tokens_before(a, page_of(e, i), kvh) + ((tok0 + kRun * i) & (ps - 1));
+                off = (token & (kRun - 1)) * (kDp / 2) + 16 * piece;
+            } else {
+                const uint32_t run = token >> 4;
+                const int p = run == 0 ? page_of(e, 0) : run == 1 ? page_of(e, 1) : run == 2 ? page_of(e, 2) : page_of(e, 3);
+                base = tokens_before(a, p, kvh) + ((tok0 + token) & (ps - 1));
+                off = 16 * piece;
+            }
+            vw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.c.v_codes + base * (kDp / 2) + off));
+        }
+        // scales: lane r16 of run h takes block r16, 16 tokens
+        const int p = h == 0 ? page_of(e, 0) : h == 1 ? page_of(e, 1) : h == 2 ? page_of(e, 2) : page_of(e, 3);
+        const uint32_t b = r16 < NB ? r16 : NB - 1;
+        vsw = *reinterpret_cast<const u32x4 *>(a.c.v_scales + tokens_before(a, p, kvh) * NB + (b << a.c.page_log2) +
+                                               ((tok0 + kRun * h) & (ps - 1)));
+    }
+
+    static __device__ __forceinline__ uint32_t piece_at(uint32_t token, uint32_t piece) {
         // pieces change places so that 16 tokens' reads of one block fall on all banks
-        const int f = kChunks == 2 ? (token >> 3) & 1 : kChunks == 4 ? (token >> 2) & 3
+        const uint32_t f = kChunks == 2 ? (token >> 3) & 1 : kChunks == 4 ? (token >> 2) & 3
                       : kChunks == 6 ? (token >> 3) & 1 : (token >> 1) & 7;
         return token * (kDp / 2) + 16 * (piece ^ f);
     }
 
     template <int B>
-    __device__ __forceinline__ void block(const uint8_t *stage, const f16x2 (&vs)[8], const f16x8 (&p)[R][2]) {
+    __device__ __forceinline__ void block(const uint8_t *stage, uint32_t token, const f16x2 (&vs)[8], const f16x8 (&p)[R][2]) {
         typedef __attribute__((address_space(3))) i32x2 lds2;
-        const int token = kRun * h + 4 * (r16 & 3) + (r16 >> 2);
         const uint8_t *at = stage + piece_at(token, B / 2) + 8 * (B % 2);
         const i32x2 w = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds2 *)at);
+        if constexpr (B % 2 == 0) nvfp4dev::phase_fence();
         f16x2 s[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = row_bcast<B>(vs[i]);
@@ -285,7 +347,9 @@ struct Stream {
     template <int... B>
     __device__ __forceinline__ void blocks(std::integer_sequence<int, B...>, const uint8_t *stage, const f16x2 (&vs)[8],
                                            const f16x8 (&p)[R][2]) {
-        (block<B>(stage, vs, p), ...);
+        const Lane n = this_lane();
+        const uint32_t token = kRun * n.h + 4 * (n.r16 & 3) + (n.r16 >> 2);
+        (block<B>(stage, token, vs, p), ...);
     }
 
     // Rows that see a token whose block of V is NaN: NaN there.  `bad` holds the
@@ -308,58 +372,105 @@ struct Stream {
         (poison_block<B>(a, tok0, bad), ...);
     }
 
-    static __device__ __forceinline__ bool visible(const AttnArgs &a, int p, int j) {
-        return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+    // Minus infinity for what row tile r does not see; `there`: which runs' pages are.
+    __device__ __forceinline__ void hide(const AttnArgs &a, int r, int tok0, uint64_t there, f32x4 (&sc)[4]) const {
+        const uint32_t h = this_lane().h;
+        const bool page = (there >> (4 * h)) & 1u;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!page || !visible(a, pos[r], tok0 + kRun * static_cast<int>(h) + 4 * i + t)) sc[t][i] = -__builtin_inff();
     }
 
-    __device__ __forceinline__ void step(const AttnArgs &a, const Steps &w, int s, Loads &x, uint8_t *stage) {
+    // Softmax of row tile r: its running maximum and sum, the step's weights as B
+    // operands.
+    __device__ __forceinline__ void weigh(int r, const f32x4 (&sc)[4], f16x8 (&p)[2]) {
+        float top = sc[0][0];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][i]);
+        top = rows_max(top);
+        top = top == -__builtin_inff() ? top : top * c[r];
+        const bool grown = top > m[r] + kRescaleAt || (m[r] == -__builtin_inff() && top > m[r]);
+        if (__any(grown)) {
+            const float to = grown ? top : m[r];
+            const float f = grown ? __builtin_amdgcn_exp2f(m[r] - to) : 1.0f;
+            m[r] = to;
+            l[r] *= f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) acc[r][b] *= f;
+        }
+        const float shift = kWeightShift - (m[r] == -__builtin_inff() ? 0.0f : m[r]);
+        float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], c[r], shift));
+                sum[i] += e;
+                p[t / 2][4 * (t % 2) + i] = static_cast<_Float16>(e);
+            }
+        l[r] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+
+    // Step s, whose pages e holds, on what is loaded; loads step `next` (pages e_next)
+    // on the way unless it is negative.
+    __device__ __forceinline__ void step(const AttnArgs &a, const Steps &w, int kvh, int s, int e, int next, int e_next,
+                                         uint8_t *stage) {
+        const uint32_t lane = this_lane().id;
         const int tok0 = s * kStep;
-        const bool pages = (x.page[0] | x.page[1] | x.page[2] | x.page[3]) >= 0;
+        const uint64_t there = __ballot(e >= 0);       // lanes 4 i: run i
+        const bool pages = there == ~uint64_t(0);
         const bool whole = pages && tok0 + kStep - 1 <= w.p_first &&
                            (a.window == 0 || tok0 > w.p_last - a.window || tok0 + kStep - 1 < a.sinks);
         // V's codes to LDS
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int at = i * kWave + lane;
-            *reinterpret_cast<u32x4 *>(stage + piece_at(at / kChunks, at % kChunks)) = x.v[i];
+            const uint32_t at = i * kWave + lane;
+            *reinterpret_cast<u32x4 *>(stage + piece_at(at / kChunks, at % kChunks)) = vw[i];
         }
-        wave_fence();
-
-        // scores
-        f32x4 sc[R][4];
-        f16x2 ks[kLaneBlocks][2];
-#pragma unroll
-        for (int j = 0; j < kLaneBlocks; ++j) {
-            ks[j][0] = nvfp4dev::e4m3x2_f16(x.ks[j]);
-            ks[j][1] = e4m3_high_f16(x.ks[j]);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) sc[r][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < kK; ++j) {
-                const _Float16 sv = ks[j / 2][t / 2][t % 2];
-                const f16x2 ss = {sv, sv};
-                const f16x8 k = decode8(x.k[t][j], ss, ss, ss, ss);
-#pragma unroll
-                for (int r = 0; r < R; ++r) sc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], sc[r][t], 0, 0, 0);
-            }
-        }
-
         // V's scales, and which of its blocks are NaN
         uint32_t bad = 0;
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t nan = ((x.vs[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                const uint32_t nan = ((vsw[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                 // one bit a byte, to bits 4 i .. 4 i + 3
                 bad |= ((nan >> 7) * 0x10204080u >> 28) << (4 * i);
-                x.vs[i] &= ~((nan >> 7) * 0xFFu);
+                vsw[i] &= ~((nan >> 7) * 0xFFu);
             }
         }
         uint32_t turned[4];
-        turn_bytes(x.vs, turned);
+        turn_bytes(vsw, turned);
+        if (next >= 0) load_v(a, kvh, next, e_next);
+        wave_fence();
+
+        // scores
+        f32x4 sc[R][4];
+        f16x2 kf[kLaneBlocks][2];
+#pragma unroll
+        for (int j = 0; j < kLaneBlocks; ++j) {
+            kf[j][0] = nvfp4dev::e4m3x2_f16(ks[j]);
+            kf[j][1] = e4m3_high_f16(ks[j]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) sc[r][t] = f32x4{0, 0, 0, 0};
+            nvfp4dev::phase_fence();                   // else the scheduler decodes all tiles first and spills
+#pragma unroll
+            for (int j = 0; j < kK; ++j) {
+                const _Float16 sv = kf[j / 2][t / 2][t % 2];
+                const f16x2 ss = {sv, sv};
+                const f16x8 k = decode8(kw[t][j], ss, ss, ss, ss);
+#pragma unroll
+                for (int r = 0; r < R; ++r) sc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], sc[r][t], 0, 0, 0);
+            }
+        }
+        if (next >= 0) load_k(a, kvh, next, e_next);
+
         f16x2 vs[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -367,52 +478,13 @@ struct Stream {
             vs[2 * t + 1] = e4m3_high_f16(turned[t]);
         }
 
-        // softmax: the row's maximum, weights, their sum
         f16x8 p[R][2];
+        if (!whole) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            uint32_t seen = 0xFFFFu;
-            if (!whole) {
-                seen = 0;
-                const bool page = (h == 0 ? x.page[0] : h == 1 ? x.page[1] : h == 2 ? x.page[2] : x.page[3]) >= 0;
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool v = page && visible(a, pos[r], tok0 + kRun * h + 4 * i + t);
-                        seen |= (v ? 1u : 0u) << (4 * t + i);
-                        sc[r][t][i] = v ? sc[r][t][i] : -__builtin_inff();
-                    }
-            }
-            float top = sc[r][0][0];
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[r][t][i]);
-            top = rows_max(top);
-            top = top == -__builtin_inff() ? top : top * c[r];
-            const bool grown = top > m[r] + kRescaleAt || (m[r] == -__builtin_inff() && top > m[r]);
-            if (__any(grown)) {
-                const float to = grown ? top : m[r];
-                const float f = grown ? __builtin_amdgcn_exp2f(m[r] - to) : 1.0f;
-                m[r] = to;
-                l[r] *= f;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) acc[r][b] *= f;
-            }
-            const float shift = kWeightShift - (m[r] == -__builtin_inff() ? 0.0f : m[r]);
-            float sum = 0.0f;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r][t][i], c[r], shift));
-                    if (!whole) e = (seen >> (4 * t + i)) & 1u ? e : 0.0f;
-                    sum += e;
-                    p[r][t / 2][4 * (t % 2) + i] = static_cast<_Float16>(e);
-                }
-            l[r] += sum;
+            for (int r = 0; r < R; ++r) hide(a, r, tok0, there, sc[r]);
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r) weigh(r, sc[r], p[r]);
 
         blocks(std::make_integer_sequence<int, NB>{}, stage, vs, p);
         if (!whole && __any(bad != 0)) poison(std::make_integer_sequence<int, NB>{}, a, tok0, bad);
@@ -421,6 +493,7 @@ struct Stream {
 
     // Query rows row0 .. of sequence s as B operands.
     __device__ __forceinline__ void load_queries(const AttnArgs &a, const Sequence &s, int kvh, int row0) {
+        const auto [lane, r16, h] = this_lane();
         const int rows = s.computed * a.group;
         const float g = a.scale * (a.c.k_global != nullptr ? a.c.k_global[kvh] : 1.0f);
         const bool bf16 = a.bf16 != 0;
@@ -456,19 +529,14 @@ struct Stream {
             // a power of two that brings the row's largest element to [2^14, 2^15), bf16 only
             float up = 1.0f, down = 1.0f;
             if (bf16) {
-                // magnitudes as floats, infinities and NaN included, sort as their patterns do
-                uint32_t all = top;
-                const uint32_t t16 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), 16, kWave));
-                all = t16 > all ? t16 : all;
-                const uint32_t t32 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), 32, kWave));
-                all = t32 > all ? t32 : all;
-                int e = static_cast<int>(all >> 23) - 127;          // -127 (zero, subnormal) .. 128
-                e = e < -100 ? -100 : e > 127 ? 127 : e;
-                up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-                down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+                const uint32_t t16 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, kWave));
+                top = t16 > top ? t16 : top;
+                const uint32_t t32 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave));
+                row_power(t32 > top ? t32 : top, &up, &down);
             }
             const float sign = g < 0.0f ? -up : up;
             c[r] = __builtin_fabsf(g) * kLog2e * down;
+            c[r] = c[r] == 0.0f ? 0x1p-126f : c[r];      // hidden scores stay minus infinity, others about 0
 #pragma unroll
             for (int j = 0; j < kK; ++j)
 #pragma unroll
@@ -480,10 +548,7 @@ struct Stream {
     // waves and written: to `out`, or where `slot` >= 0 as a partial result.
     __device__ __forceinline__ void run(const AttnArgs &a, Buffers &buf, const Sequence &s, const Steps &w, int b, int kvh,
                                         int row0, int i0, int i1, int64_t slot) {
-        lane = threadIdx.x & (kWave - 1);
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-        r16 = lane & 15;
-        h = lane >> 4;
         const int32_t *row = a.table + static_cast<int64_t>(b) * a.table_stride;
         load_queries(a, s, kvh, row0);
 #pragma unroll
@@ -496,24 +561,22 @@ struct Stream {
         uint8_t *stage = buf.v[wave];
         int i = i0 + wave;
         if (i < i1) {
-            Loads x;
-            load(a, kvh, w.at(i), entry(a, row, s.len, w.at(i)), x);
-            int next = i + kAttnWaves;
-            int e = next < i1 ? entry(a, row, s.len, w.at(next)) : -1;
+            int at = w.at(i);
+            int e = entry(a, row, s.len, at);
+            load_v(a, kvh, at, e);
+            load_k(a, kvh, at, e);
+            int next = i + kAttnWaves < i1 ? w.at(i + kAttnWaves) : -1;
+            int e_next = next >= 0 ? entry(a, row, s.len, next) : -1;
             for (;;) {
-                Loads y;
-                const bool more = next < i1;
-                int after = -1;
-                if (more) {
-                    load(a, kvh, w.at(next), e, y);
-                    if (next + kAttnWaves < i1) after = entry(a, row, s.len, w.at(next + kAttnWaves));
-                }
-                step(a, w, w.at(i), x, stage);
-                if (!more) break;
-                x = y;
-                e = after;
-                i = next;
-                next += kAttnWaves;
+                const int after = i + 2 * kAttnWaves < i1 ? w.at(i + 2 * kAttnWaves) : -1;
+                const int e_after = after >= 0 ? entry(a, row, s.len, after) : -1;
+                step(a, w, kvh, at, e, next, e_next, stage);
+                if (next < 0) break;
+                i += kAttnWaves;
+                at = next;
+                e = e_next;
+                next = after;
+                e_next = e_after;
             }
         }
         join(a, buf, s, kvh, row0, slot);
@@ -521,6 +584,8 @@ struct Stream {
 
     __device__ __forceinline__ void join(const AttnArgs &a, Buffers &buf, const Sequence &s, int kvh, int row0,
                                          int64_t slot) {
+        const auto [lane, r16, h] = this_lane();
+        const int left = s.computed * a.group - row0, rows = left < kRows ? left : kRows;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float sum = rows_sum(l[r]);
@@ -529,134 +594,114 @@ struct Stream {
                 buf.l[wave][16 * r + r16] = sum;
             }
         }
-        __syncthreads();
-        float f[R];
+        __syncthreads();                               // the waves are done with V's codes, too
+        const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
+        const bool bf16 = a.bf16 != 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            if (16 * r >= rows) break;
             float top = buf.m[0][16 * r + r16];
 #pragma unroll
             for (int k = 1; k < kAttnWaves; ++k) top = __builtin_fmaxf(top, buf.m[k][16 * r + r16]);
-            f[r] = m[r] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[r] - top);
-        }
-        const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
-        const bool bf16 = a.bf16 != 0;
-        const int rows = s.computed * a.group;
-        // this thread's row and four outputs of each block
-        constexpr int kEach = kRows * 4;           // threads of a block of outputs
-        const int my_row = threadIdx.x / 4 % kRows, my = threadIdx.x % 4;
-        const bool busy = threadIdx.x < kEach;
-        float top = -__builtin_inff(), total = 0.0f;
-        if (busy) {
+            const float f = m[r] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[r] - top);
 #pragma unroll
-            for (int k = 0; k < kAttnWaves; ++k) top = __builtin_fmaxf(top, buf.m[k][my_row]);
+            for (int b0 = 0; b0 < NB; b0 += kJoinBlocks) {
+                if (static_cast<int>(16 * r + r16) < rows) {
 #pragma unroll
-            for (int k = 0; k < kAttnWaves; ++k) {
-                const float mk = buf.m[k][my_row];
-                total += buf.l[k][my_row] * (mk == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mk - top));
-            }
-            if (slot >= 0 && my == 0) {
-                a.ml[(slot * kRows + my_row) * 2] = top;
-                a.ml[(slot * kRows + my_row) * 2 + 1] = total;
-            }
-        }
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        const int global_row = row0 + my_row;
-        const int i = global_row / a.group, head = kvh * a.group + (global_row - i * a.group);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const f32x4 v = acc[r][b] * f[r];
-                *reinterpret_cast<f32x4 *>(&buf.o[wave][16 * r + r16][4 * h]) = v;
-            }
-            __syncthreads();
-            if (busy) {
-                f32x4 v = *reinterpret_cast<const f32x4 *>(&buf.o[0][my_row][4 * my]);
-#pragma unroll
-                for (int k = 1; k < kAttnWaves; ++k) v += *reinterpret_cast<const f32x4 *>(&buf.o[k][my_row][4 * my]);
-                if (slot >= 0) {
-                    *reinterpret_cast<f32x4 *>(a.part + (slot * kRows + my_row) * kDp + 16 * b + 4 * my) = v;
-                } else if (global_row < rows && 16 * b < a.c.head_dim) {
-                    store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 16 * b + 4 * my,
-                           total == 0.0f ? f32x4{0, 0, 0, 0} : v * inv * g, bf16, a.o_wide);
+                    for (int b = 0; b < kJoinBlocks; ++b)
+                        *reinterpret_cast<f32x4 *>(&buf.o[wave][r16][16 * b + 4 * h]) = acc[r][b0 + b] * f;
                 }
+                __syncthreads();
+                const int n = rows - 16 * r < 16 ? rows - 16 * r : 16;
+                for (int j = threadIdx.x; j < n * 4 * kJoinBlocks; j += kAttnThreads) {
+                    const int row = 16 * r + j / (4 * kJoinBlocks), col = 4 * (j % (4 * kJoinBlocks));
+                    f32x4 v = *reinterpret_cast<const f32x4 *>(&buf.o[0][row - 16 * r][col]);
+#pragma unroll
+                    for (int k = 1; k < kAttnWaves; ++k) v += *reinterpret_cast<const f32x4 *>(&buf.o[k][row - 16 * r][col]);
+                    float best = buf.m[0][row], total = 0.0f;
+#pragma unroll
+                    for (int k = 1; k < kAttnWaves; ++k) best = __builtin_fmaxf(best, buf.m[k][row]);
+#pragma unroll
+                    for (int k = 0; k < kAttnWaves; ++k) {
+                        const float mk = buf.m[k][row];
+                        total += buf.l[k][row] * (mk == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mk - best));
+                    }
+                    if (slot >= 0) {
+                        *reinterpret_cast<f32x4 *>(a.part + (slot * kRows + row) * kDp + 16 * b0 + col) = v;
+                        if (b0 == 0 && col == 0) {
+                            a.ml[(slot * kRows + row) * 2] = best;
+                            a.ml[(slot * kRows + row) * 2 + 1] = total;
+                        }
+                    } else if (16 * b0 + col < a.c.head_dim) {
+                        const int i = (row0 + row) / a.group, head = kvh * a.group + (row0 + row - i * a.group);
+                        store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 16 * b0 + col,
+                               total == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / total) * g, bf16, a.o_wide);
+                    }
+                }
+                __syncthreads();
             }
-            __syncthreads();
         }
-    }
-
-    static __device__ __forceinline__ void store4(uint16_t *p, f32x4 v, bool bf16, bool wide) {
-        const uint32_t lo = to16(v[0], bf16) | to16(v[1], bf16) << 16, hi = to16(v[2], bf16) | to16(v[3], bf16) << 16;
-        if (wide) {
-            *reinterpret_cast<u32x2 *>(p) = u32x2{lo, hi};
-        } else {
-            p[0] = static_cast<uint16_t>(lo);
-            p[1] = static_cast<uint16_t>(lo >> 16);
-            p[2] = static_cast<uint16_t>(hi);
-            p[3] = static_cast<uint16_t>(hi >> 16);
-        }
+        // the last round's barrier also frees m and l; without a round nothing reads them
+        if (rows <= 0) __syncthreads();
     }
 };
 
-// Sums of count(b) over the sequences before each thread's share of them, and over
-// all (`scan` of kAttnThreads values).
-struct Share {
-    int from, to;          // this thread's sequences
-    int64_t before, total;
-};
-template <typename Count>
-__device__ __forceinline__ Share share_of(int batch, int64_t *scan, Count count) {
-    Share s;
-    const int each = (batch + kAttnThreads - 1) / kAttnThreads;
-    s.from = static_cast<int>(threadIdx.x) * each;
-    s.from = s.from < batch ? s.from : batch;
-    s.to = s.from + each < batch ? s.from + each : batch;
-    int64_t own = 0;
-    for (int b = s.from; b < s.to; ++b) own += count(b);
-    scan[threadIdx.x] = own;
-    __syncthreads();
-    for (int o = 1; o < kAttnThreads; o <<= 1) {
-        const int64_t add = static_cast<int>(threadIdx.x) >= o ? scan[threadIdx.x - o] : 0;
-        __syncthreads();
-        scan[threadIdx.x] += add;
-        __syncthreads();
-    }
-    s.before = scan[threadIdx.x] - own;
-    s.total = scan[kAttnThreads - 1];
-    return s;
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v)),
+                   hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// One workgroup a tile of query rows and kv head; the whole list of steps.
+// count(b) of up to 64 sequences from b0 on, one a lane, and their sum over the lanes
+// up to and with each (below 64 * 2^25).
+struct Counts {
+    uint32_t own, upto;
+    __device__ __forceinline__ uint32_t all() const {
+        return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto), kWave - 1));
+    }
+};
+template <typename Count>
+__device__ __forceinline__ Counts counts_from(int b0, int batch, Count count) {
+    const int lane = threadIdx.x & (kWave - 1);
+    Counts c;
+    c.own = b0 + lane < batch ? static_cast<uint32_t>(count(b0 + lane)) : 0u;
+    c.upto = c.own;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const uint32_t x = static_cast<uint32_t>(__shfl_up(static_cast<int>(c.upto), o, kWave));
+        c.upto += lane >= o ? x : 0u;
+    }
+    return c;
+}
+// The sequence that holds `at` where each counts count(b) * times, and where its
+// counts begin; batch if none does.  Every wave finds it by itself.
+template <typename Count>
+__device__ __forceinline__ int sequence_with(int64_t at, int64_t times, int batch, Count count, int64_t *before) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < batch; b0 += kWave) {
+        const Counts c = counts_from(b0, batch, count);
+        const int64_t end = base + static_cast<int64_t>(c.upto) * times;
+        const uint64_t past = __ballot(end > at);
+        if (past != 0) {
+            const int n = __builtin_ctzll(past);
+            *before = uniform64(base + static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<int>(c.upto - c.own), n)) * times);
+            return b0 + n;
+        }
+        base += static_cast<int64_t>(c.all()) * times;
+    }
+    return batch;
+}
+
+// One workgroup a sequence and kv head, all of its steps: short caches.
 template <int NB, int R>
-__global__ __launch_bounds__(kAttnThreads) void attn_tiles(const AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * NB, 16 * R)) void attn_whole(const AttnArgs a) {
     using S = Stream<NB, R>;
     __shared__ typename S::Buffers buf;
-    __shared__ int64_t scan[kAttnThreads];
-    __shared__ int found[2];
-    const int kvh = blockIdx.x % a.c.kv_heads;
-    const int tile = blockIdx.x / a.c.kv_heads;
-    const auto tiles = [&](int b) -> int64_t {
-        return (static_cast<int64_t>(sequence_of(a, b).computed) * a.group + S::kRows - 1) / S::kRows;
-    };
-    if (threadIdx.x == 0) found[0] = -1;
-    const Share mine = share_of(a.batch, scan, tiles);
-    int64_t at = mine.before;
-    for (int b = mine.from; b < mine.to; ++b) {
-        const int64_t n = tiles(b);
-        if (tile >= at && tile < at + n) {
-            found[0] = b;
-            found[1] = static_cast<int>(tile - at);
-        }
-        at += n;
-    }
-    __syncthreads();
-    const int b = __builtin_amdgcn_readfirstlane(found[0]);
-    if (b < 0) return;
-    const int row0 = __builtin_amdgcn_readfirstlane(found[1]) * S::kRows;
+    const int b = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x - b * a.c.kv_heads;
     const Sequence s = sequence_of(a, b);
-    const Steps w = steps_for(a, s, row0, S::kRows);
+    const Steps w = steps_for<6>(a, s, 0, S::kRows);
     S job;
-    job.run(a, buf, s, w, b, kvh, row0, 0, w.count, -1);
+    job.run(a, buf, s, w, b, kvh, 0, 0, w.count, -1);
 }
 
 // First step of workgroup g of n that share `total` steps.
@@ -670,69 +715,57 @@ __device__ __forceinline__ int64_t sharing(int64_t groups, int64_t total) {
 // workgroup's share may begin and end within a sequence, whose results it then
 // leaves as partial ones for attn_join.
 template <int NB, int R>
-__global__ __launch_bounds__(kAttnThreads) void attn_shared(const AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * NB, 16 * R)) void attn_shared(const AttnArgs a) {
     using S = Stream<NB, R>;
     __shared__ typename S::Buffers buf;
-    __shared__ int64_t scan[kAttnThreads];
-    __shared__ int64_t found[2];
-    const auto count = [&](int b) -> int64_t { return steps_for(a, sequence_of(a, b), 0, S::kRows).count; };
-    const Share mine = share_of(a.batch, scan, count);
-    const int64_t heads = a.c.kv_heads, total = mine.total * heads, n = sharing(a.groups, total);
-    if (blockIdx.x == 0) {
-        int64_t at = mine.before;
-        for (int b = mine.from; b < mine.to; ++b) {
-            a.prefix[b] = at;
-            at += count(b);
-        }
-        if (threadIdx.x == 0) a.prefix[a.batch] = mine.total;
+    const auto count = [&](int b) { return steps_for<6>(a, sequence_of(a, b), 0, S::kRows).count; };
+    const int64_t heads = a.c.kv_heads;
+    int64_t total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+        const Counts c = counts_from(b0, a.batch, count);
+        if (blockIdx.x == 0 && threadIdx.x < kWave && b0 + static_cast<int>(threadIdx.x) < a.batch)
+            a.prefix[b0 + threadIdx.x] = total + (c.upto - c.own);
+        total += c.all();
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.batch] = total;
+    total = uniform64(total) * heads;
+    const int64_t n = sharing(a.groups, total);
     if (static_cast<int64_t>(blockIdx.x) >= n || total == 0) return;
     int64_t at = first_of(blockIdx.x, n, total);
     const int64_t end = first_of(static_cast<int64_t>(blockIdx.x) + 1, n, total);
-    {
-        int64_t x = mine.before * heads;
-        for (int b = mine.from; b < mine.to; ++b) {
-            const int64_t c = count(b) * heads;
-            if (at >= x && at < x + c) {
-                found[0] = b;
-                found[1] = at - x;
-            }
-            x += c;
-        }
-    }
-    __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0]));
-    int64_t offset = found[1];
+    int64_t before = 0;
+    int b = __builtin_amdgcn_readfirstlane(sequence_with(at, heads, a.batch, count, &before));
+    int64_t offset = at - before;
+    int left = static_cast<int>(end - at);             // below 2^31: a sequence's steps times kv heads over n
     bool first = true;
-    while (at < end) {
+    while (left > 0) {
         const Sequence s = sequence_of(a, b);
-        const Steps w = steps_for(a, s, 0, S::kRows);
-        if (w.count == 0) {
+        const Steps w = steps_for<6>(a, s, 0, S::kRows);
+        const int64_t steps = static_cast<int64_t>(w.count) * heads;
+        if (offset >= steps) {
+            offset -= steps;
             ++b;
             continue;
         }
-        int kvh = __builtin_amdgcn_readfirstlane(static_cast<int>(offset / w.count));
-        int i0 = __builtin_amdgcn_readfirstlane(static_cast<int>(offset - static_cast<int64_t>(kvh) * w.count));
-        for (; kvh < a.c.kv_heads && at < end; ++kvh, i0 = 0) {
-            const int left = static_cast<int>(end - at < w.count ? end - at : w.count);
-            const int i1 = i0 + left < w.count ? i0 + left : w.count;
-            const bool complete = i0 == 0 && i1 == w.count;
-            S job;
-            job.run(a, buf, s, w, b, kvh, 0, i0, i1, complete ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1));
-            first = false;
-            at += i1 - i0;
-        }
-        offset = 0;
-        ++b;
+        const int kvh = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint64_t>(offset) / static_cast<uint32_t>(w.count)));
+        const int i0 = static_cast<int>(offset - static_cast<int64_t>(kvh) * w.count);
+        const int i1 = left < w.count - i0 ? i0 + left : w.count;
+        const bool complete = i0 == 0 && i1 == w.count;
+        S job;
+        job.run(a, buf, s, w, b, kvh, 0, i0, i1, complete ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1));
+        first = false;
+        left -= i1 - i0;
+        offset += i1 - i0;
     }
 }
 
-// One workgroup a query row: its partial results joined, or zeros where there are none.
+// One workgroup a query row (`used` of the `rows` that a partial result holds): its
+// partial results joined, or zeros where there are none.
 template <int NB>
-__global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int rows) {
+__global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int rows, int used) {
     constexpr int kDp = 16 * NB, kWide = kDp / 4, kSlices = kAttnThreads / kWide;
     __shared__ f32x4 sums[kSlices][kWide];
-    const int row = blockIdx.x % rows, item = blockIdx.x / rows;
+    const int row = blockIdx.x % used, item = blockIdx.x / used;
     const int b = item / a.c.kv_heads, kvh = item - b * a.c.kv_heads;
     const Sequence s = sequence_of(a, b);
     if (row >= s.computed * a.group) return;
@@ -779,8 +812,481 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int 
     if (4 * col >= a.c.head_dim) return;
     const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
     const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
-    Stream<NB, 1>::store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 4 * col,
+    store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 4 * col,
                           sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum) * g, a.bf16 != 0, a.o_wide);
+}
+
+// ---------------------------------------------------------------- the tile kernel
+//
+// Many query rows: a workgroup holds 32 of them a wave and walks the cache in steps
+// of T tokens, which its waves decode once into LDS, as fp16, for all of them: K as
+// [token][element], V turned, as [element][token].  Products run on the 32 x 32
+// matrix instructions.  Codes are loaded two steps ahead into registers and decoded
+// one step ahead into the other of two buffers, so that one barrier a step is
+// enough; half of the waves decode before their products and half after them, so
+// that the two waves of a SIMD need the VALU and the matrix cores at different
+// times.
+template <int NB, int WAVES>
+struct Tile {
+    static constexpr int kDp = 16 * NB;
+    static constexpr int kLog = NB <= 8 ? 6 : 5;   // more tokens' scores do not fit the registers
+    static constexpr int kT = 1 << kLog;
+    static constexpr int kRuns = kT / kRun;
+    static constexpr int kRows = 32 * WAVES;
+    static constexpr int kUnits = 2 * kRuns;       // runs of K, then of V, that are decoded by a wave each
+    static constexpr int kOwn = (kUnits + WAVES - 1) / WAVES;
+    static constexpr int kPieces = (kDp / 2 + kWave - 1) / kWave;   // 16-byte pieces of a run's codes a lane has
+    static constexpr int kSlices = kDp / 16;       // k steps of the first product
+    static constexpr int kOuts = kDp / 32;         // output tiles of 32 elements
+    static constexpr int kRead = NB / 4;           // transposed reads of a lane: blocks of 16 over four lane groups
+
+    struct Buffers {
+        __attribute__((aligned(16))) _Float16 k[2][kT * kDp];
+        __attribute__((aligned(16))) _Float16 v[2][kT * kDp];
+        __attribute__((aligned(16))) uint8_t raw[kRuns][kRun * kDp / 2];
+        uint32_t bad[2][kRuns];                    // whether a run of V holds NaN, and which tokens of which block
+        uint16_t nan[2][kRuns][NB];
+    };
+
+    // a unit's codes and scales on their way
+    u32x4 code[kOwn][kPieces];
+    u32x4 scale[kOwn][kPieces > kRead ? kPieces : kRead];   // of K one word of two bytes each
+
+    int wave;
+    f16x8 q[kSlices];
+    float c;
+    int pos;
+    f32x16 acc[kOuts];
+    float m, l;
+
+    static __device__ __forceinline__ uint32_t k_at(uint32_t token, uint32_t chunk) {   // chunks of 8 elements
+        const uint32_t f = NB == 8 || NB == 16 ? token & 15 : (token >> 1) & 7;
+        return token * kDp + 8 * (chunk ^ f);
+    }
+    static __device__ __forceinline__ uint32_t v_at(uint32_t element, uint32_t chunk) {   // chunks of 8 tokens
+        const uint32_t f = kT == 64 ? element & 7 : (element >> 2) & 3;
+        return element * kT + 8 * (chunk ^ f);
+    }
+    static __device__ __forceinline__ uint32_t raw_at(uint32_t token, uint32_t piece) {
+        constexpr int kEach = kDp / 32;
+        const uint32_t f = kEach == 2 ? (token >> 3) & 1 : kEach == 4 ? (token >> 2) & 3
+                           : kEach == 6 ? (token >> 3) & 1 : (token >> 1) & 7;
+        return token * (kDp / 2) + 16 * (piece ^ f);
+    }
+
+    // The page of step s that run lane % kRuns lies in, -1 without one.
+    __device__ __forceinline__ int entry(const AttnArgs &a, const int32_t *row, int len, int s) const {
+        const int token = s * kT + kRun * static_cast<int>(this_lane().id % kRuns);
+        int i = token >> a.c.page_log2;
+        i = i < a.table_width ? i : a.table_width - 1;
+        const int p = row[i];
+        return token < len && p >= 0 && p < a.pages ? p : -1;
+    }
+
+    __device__ __forceinline__ void load(const AttnArgs &a, int kvh, int s, int e) {
+        const Lane n = this_lane();
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int unit = wave + o * WAVES;
+            if (unit >= kUnits) break;
+            const bool is_v = unit >= kRuns;
+            const int run = is_v ? unit - kRuns : unit;
+            int page = __builtin_amdgcn_readlane(e, run);
+            page = page < 0 ? 0 : page;
+            const uint64_t head = static_cast<uint64_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(a.c.kv_heads) +
+                                  static_cast<uint32_t>(kvh);
+            const uint64_t tokens = head << a.c.page_log2;
+            const uint32_t off = (s * kT + kRun * run) & ((1 << a.c.page_log2) - 1);
+            const uint8_t *codes = (is_v ? a.c.v_codes : a.c.k_codes) + (tokens + off) * (kDp / 2);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const uint32_t at = i * kWave + n.id;
+                if ((i + 1) * kWave <= kDp / 2 || at < kDp / 2)
+                    code[o][i] = *reinterpret_cast<const u32x4 *>(codes + 16 * at);
+            }
+            if (is_v) {
+                const uint8_t *scales = a.c.v_scales + tokens * NB + off;
+#pragma unroll
+                for (int i = 0; i < kRead; ++i)
+                    scale[o][i] = *reinterpret_cast<const u32x4 *>(scales + ((4 * i + n.h) << a.c.page_log2));
+            } else {
+                const uint8_t *scales = a.c.k_scales + tokens * NB + off;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const uint32_t at = i * kWave + n.id, token = at / (kDp / 32), piece = at % (kDp / 32);
+                    if ((i + 1) * kWave <= kDp / 2 || at < kDp / 2) {
+                        scale[o][i][0] = scales[((2 * piece) << a.c.page_log2) + token];
+                        scale[o][i][1] = scales[((2 * piece + 1) << a.c.page_log2) + token];
+                    }
+                }
+            }
+        }
+    }
+
+    // Decodes the loaded units into buffer `to`.
+    __device__ __forceinline__ void decode(Buffers &buf, int to) {
+        typedef __attribute__((address_space(3))) i32x2 lds2;
+        const Lane n = this_lane();
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int unit = wave + o * WAVES;
+            if (unit >= kUnits) break;
+            if (unit < kRuns) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const uint32_t at = i * kWave + n.id, token = at / (kDp / 32), piece = at % (kDp / 32);
+                    if ((i + 1) * kWave <= kDp / 2 || at < kDp / 2) {
+                        const _Float16 s0 = nvfp4dev::e4m3x2_f16(scale[o][i][0])[0], s1 = nvfp4dev::e4m3x2_f16(scale[o][i][1])[0];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const f16x2 ss = j < 2 ? f16x2{s0, s0} : f16x2{s1, s1};
+                            *reinterpret_cast<f16x8 *>(&buf.k[to][k_at(kRun * unit + token, 4 * piece + j)]) =
+                                decode8(code[o][i][j], ss, ss, ss, ss);
+                        }
+                    }
+                }
+            } else {
+                const int run = unit - kRuns;
+                uint8_t *raw = buf.raw[run];
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const uint32_t at = i * kWave + n.id;
+                    if ((i + 1) * kWave <= kDp / 2 || at < kDp / 2)
+                        *reinterpret_cast<u32x4 *>(raw + raw_at(at / (kDp / 32), at % (kDp / 32))) = code[o][i];
+                }
+                wave_fence();
+                // tokens in the order in which the scores leave the first product: 0-3, 8-11, 4-7, 12-15
+                const uint32_t token = (n.r16 & 3) | (n.r16 & 4) << 1 | (n.r16 & 8) >> 1;
+                uint32_t any = 0;
+#pragma unroll
+                for (int i = 0; i < kRead; ++i) {
+                    const uint32_t block = 4 * i + n.h;
+                    const i32x2 w = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds2 *)(raw + raw_at(token, block / 2) + 8 * (block % 2)));
+                    // a NaN block counts as 0 here; who sees it is told by its flags
+                    u32x4 x = scale[o][i];
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t nan = ((x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                        any |= nan;
+                        bad |= nan >> (7 - k);         // bits k, 8 + k, 16 + k, 24 + k: tokens 4 k ..
+                        x[k] &= ~(nan | (nan - (nan >> 7)));
+                    }
+                    if (n.r16 == 0) {
+                        uint32_t bits = 0;
+                        if (bad != 0) {
+                            for (int k = 0; k < 4; ++k)
+                                for (int j = 0; j < 4; ++j) bits |= (bad >> (8 * j + k) & 1u) << (4 * k + j);
+                        }
+                        buf.nan[to][run][block] = static_cast<uint16_t>(bits);
+                    }
+                    const f16x8 lo = decode8(static_cast<uint32_t>(w[0]), nvfp4dev::e4m3x2_f16(x[0]), e4m3_high_f16(x[0]),
+                                             nvfp4dev::e4m3x2_f16(x[2]), e4m3_high_f16(x[2]));
+                    const f16x8 hi = decode8(static_cast<uint32_t>(w[1]), nvfp4dev::e4m3x2_f16(x[1]), e4m3_high_f16(x[1]),
+                                             nvfp4dev::e4m3x2_f16(x[3]), e4m3_high_f16(x[3]));
+                    const uint32_t element = 16 * block + n.r16;
+                    *reinterpret_cast<f16x8 *>(&buf.v[to][v_at(element, 2 * run)]) = lo;
+                    *reinterpret_cast<f16x8 *>(&buf.v[to][v_at(element, 2 * run + 1)]) = hi;
+                }
+                const bool some = __any(any != 0);
+                if (n.id == 0) buf.bad[to][run] = some ? 1u : 0u;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load_query(const AttnArgs &a, const Sequence &s, int kvh, int row) {
+        const Lane n = this_lane();
+        const uint32_t h = n.id >> 5;
+        const float g = a.scale * (a.c.k_global != nullptr ? a.c.k_global[kvh] : 1.0f);
+        const bool bf16 = a.bf16 != 0;
+        const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
+        pos = -1;
+        u32x4 raw[kSlices];
+#pragma unroll
+        for (int j = 0; j < kSlices; ++j) raw[j] = u32x4{0, 0, 0, 0};
+        if (row < s.computed * a.group) {
+            const int at = s.len - s.n + i;
+            pos = at < 0 ? -1 : at;
+            const uint16_t *p = a.q + static_cast<int64_t>(s.first + i) * a.q_token + head * a.q_head;
+#pragma unroll
+            for (int j = 0; j < kSlices; ++j)
+                if (16 * j < a.c.head_dim) raw[j] = load8(p + 16 * j + 8 * h, a.q_wide);
+        }
+        uint32_t top = 0;
+        float x[8];
+        float up = 1.0f, down = 1.0f;
+        if (bf16) {
+#pragma unroll
+            for (int j = 0; j < kSlices; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t lo = raw[j][k] << 16 & 0x7FFFFFFFu, hi = raw[j][k] & 0x7FFF0000u;
+                    top = lo > top ? lo : top;
+                    top = hi > top ? hi : top;
+                }
+            const uint32_t other = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave));
+            row_power(other > top ? other : top, &up, &down);
+        }
+        const float sign = g < 0.0f ? -up : up;
+        c = __builtin_fabsf(g) * kLog2e * down;
+        c = c == 0.0f ? 0x1p-126f : c;                 // as in the stream kernel
+#pragma unroll
+        for (int j = 0; j < kSlices; ++j) {
+            widen(raw[j], bf16, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) q[j][k] = static_cast<_Float16>(x[k] * sign);
+        }
+    }
+
+    // Step s from buffer `from`; `there`: bit r where run r's page is.
+    __device__ __forceinline__ void step(const AttnArgs &a, const Buffers &buf, int from, int s, uint64_t there, int p_first,
+                                         int p_last) {
+        const int tok0 = s * kT;
+        const Lane n = this_lane();
+        const uint32_t r32 = n.id & 31, h = n.id >> 5;
+        f32x16 sc[kT / 32];
+#pragma unroll
+        for (int u = 0; u < kT / 32; ++u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kSlices; ++j) {
+                const f16x8 k = *reinterpret_cast<const f16x8 *>(&buf.k[from][k_at(32 * u + r32, 2 * j + h)]);
+                sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[j], sc[u], 0, 0, 0);
+            }
+        }
+        const uint64_t all = (uint64_t(1) << kRuns) - 1;
+        const bool whole = (there & all) == all && tok0 + kT - 1 <= p_first &&
+                           (a.window == 0 || tok0 > p_last - a.window || tok0 + kT - 1 < a.sinks);
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < kT / 32; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int token = 32 * u + 8 * (i / 4) + 4 * static_cast<int>(h) + i % 4;
+                    if (!((there >> (token / kRun)) & 1u) || !visible(a, pos, tok0 + token)) sc[u][i] = -__builtin_inff();
+                }
+        }
+        float top = sc[0][0];
+#pragma unroll
+        for (int u = 0; u < kT / 32; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, sc[u][i]);
+        top = xor32(top, true);
+        top = top == -__builtin_inff() ? top : top * c;
+        const bool grown = top > m + kRescaleAt || (m == -__builtin_inff() && top > m);
+        if (__any(grown)) {
+            const float to = grown ? top : m;
+            const float f = grown ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int o = 0; o < kOuts; ++o)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[o][i] *= f;
+        }
+        const float shift = kWeightShift - (m == -__builtin_inff() ? 0.0f : m);
+        f16x8 p[kT / 16];
+        float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < kT / 32; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][i], c, shift));
+                sum[i % 4] += e;
+                p[2 * u + i / 8][i % 8] = static_cast<_Float16>(e);
+            }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+        for (int k = 0; k < kT / 16; ++k)
+#pragma unroll
+            for (int o = 0; o < kOuts; ++o) {
+                const f16x8 v = *reinterpret_cast<const f16x8 *>(&buf.v[from][v_at(32 * o + r32, 2 * k + h)]);
+                acc[o] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[k], acc[o], 0, 0, 0);
+            }
+        uint32_t bad = 0;
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) bad |= buf.bad[from][r];
+        if (__builtin_amdgcn_readfirstlane(static_cast<int>(bad)) != 0) poison(a, buf, from, tok0, there);
+    }
+
+    // Rows that see a token whose block of V is NaN: NaN there.
+    __device__ __forceinline__ void poison(const AttnArgs &a, const Buffers &buf, int from, int tok0, uint64_t there) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            for (int run = 0; run < kRuns; ++run) {
+                uint32_t bits = __builtin_amdgcn_readfirstlane(static_cast<int>(buf.nan[from][run][b]));
+                if (!((there >> run) & 1u)) bits = 0;
+                while (bits != 0) {
+                    const int j = tok0 + kRun * run + __builtin_ctz(bits);
+                    bits &= bits - 1;
+                    if (visible(a, pos, j)) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[b / 2][8 * (b % 2) + i] = __uint_as_float(0x7FC00000u);
+                    }
+                }
+            }
+    }
+
+    // Steps i0 .. i1 of the list for the rows from row0 on; results to `out`, or where
+    // `part` is not NULL there ([kRows][dp] sums, then [kRows][2] maximum and sum).
+    __device__ __forceinline__ void run(const AttnArgs &a, Buffers &buf, const Sequence &s, const Steps &w, int b, int kvh,
+                                        int row0, int i0, int i1, float *part) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        const int32_t *table = a.table + static_cast<int64_t>(b) * a.table_stride;
+        const Lane n = this_lane();
+        const int first = row0 + 32 * wave, row = first + static_cast<int>(n.id & 31);
+        load_query(a, s, kvh, row);
+        // positions of this wave's first and last query
+        const int last_row = s.computed * a.group - 1;
+        const int end = first + 31 < last_row ? first + 31 : last_row;
+        const int p_first = s.len - s.n + first / a.group;
+        const int p_last = first <= last_row ? s.len - s.n + end / a.group : -1;
+        m = -__builtin_inff();
+        l = 0.0f;
+#pragma unroll
+        for (int o = 0; o < kOuts; ++o)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[o][i] = 0.0f;
+        if (i0 < i1) {
+            uint64_t there, there_next = 0;
+            {
+                const int e = entry(a, table, s.len, w.at(i0));
+                there = __ballot(e >= 0);
+                load(a, kvh, w.at(i0), e);
+                decode(buf, 0);
+            }
+            if (i0 + 1 < i1) {
+                const int e = entry(a, table, s.len, w.at(i0 + 1));
+                there_next = __ballot(e >= 0);
+                load(a, kvh, w.at(i0 + 1), e);
+            }
+            int e_after = i0 + 2 < i1 ? entry(a, table, s.len, w.at(i0 + 2)) : -1;
+            __syncthreads();
+            for (int i = i0; i < i1; ++i) {
+                const int from = (i - i0) & 1;
+                const bool early = wave >= WAVES / 2;
+                const auto ahead = [&]() {
+                    if (i + 1 < i1) decode(buf, from ^ 1);
+                    if (i + 2 < i1) load(a, kvh, w.at(i + 2), e_after);
+                };
+                if (early) ahead();
+                const int tok0 = w.at(i) * kT;
+                if (tok0 <= p_last) step(a, buf, from, w.at(i), there, p_first, p_last);
+                if (!early) ahead();
+                there = there_next;
+                there_next = __ballot(e_after >= 0);
+                if (i + 3 < i1) e_after = entry(a, table, s.len, w.at(i + 3));
+                __syncthreads();
+            }
+        }
+        // this lane's row: elements 32 o + 8 j + 4 h ..
+        const uint32_t h = this_lane().id >> 5;
+        const float total = xor32(l, false);
+        if (part != nullptr) {
+            const int at = 32 * wave + static_cast<int>(n.id & 31);
+            float *ml = part + kRows * kDp;
+            if (h == 0) {
+                ml[2 * at] = m;
+                ml[2 * at + 1] = total;
+            }
+#pragma unroll
+            for (int o = 0; o < kOuts; ++o)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<f32x4 *>(part + at * kDp + 32 * o + 8 * j + 4 * h) =
+                        f32x4{acc[o][4 * j], acc[o][4 * j + 1], acc[o][4 * j + 2], acc[o][4 * j + 3]};
+            return;
+        }
+        if (row > last_row) return;
+        const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
+        const float inv = 1.0f / total;
+        const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
+        uint16_t *out = a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head;
+#pragma unroll
+        for (int o = 0; o < kOuts; ++o)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = 32 * o + 8 * j + 4 * static_cast<int>(h);
+                if (e < a.c.head_dim)
+                    store4(out + e,
+                           total == 0.0f ? f32x4{0, 0, 0, 0}
+                                         : f32x4{acc[o][4 * j], acc[o][4 * j + 1], acc[o][4 * j + 2], acc[o][4 * j + 3]} * inv * g,
+                           a.bf16 != 0, a.o_wide);
+            }
+    }
+};
+
+// Floats of a partial result of the tile kernel.
+constexpr int64_t tile_part(int64_t rows, int64_t dp) { return rows * (dp + 2); }
+
+// The sequence, first row and kv head of a workgroup of the tile kernel, b = batch
+// past the last.  Tiles are numbered from the last, so that those that see the most
+// of a prompt come first; workgroups next to each other take the kv heads.
+struct TileJob {
+    int b, kvh, row0;
+};
+__device__ __forceinline__ TileJob tile_job(const AttnArgs &a, int item, int tiles, int rows) {
+    TileJob j;
+    j.kvh = item % a.c.kv_heads;
+    const int tile = tiles - 1 - item / a.c.kv_heads;
+    const auto count = [&](int b) {
+        return static_cast<int>((static_cast<int64_t>(sequence_of(a, b).computed) * a.group + rows - 1) / rows);
+    };
+    int64_t before = 0;
+    j.b = __builtin_amdgcn_readfirstlane(sequence_with(tile, 1, a.batch, count, &before));
+    j.row0 = (tile - static_cast<int>(before)) * rows;
+    return j;
+}
+
+// `tiles` bounds the tiles of all sequences; `splits` workgroups share a tile's steps.
+template <int NB, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave, 2) void attn_tiles(const AttnArgs a, int tiles, int splits) {
+    using T = Tile<NB, WAVES>;
+    __shared__ typename T::Buffers buf;
+    const int item = blockIdx.x / splits, split = blockIdx.x - item * splits;
+    const TileJob j = tile_job(a, item, tiles, T::kRows);
+    if (j.b >= a.batch) return;
+    const Sequence s = sequence_of(a, j.b);
+    const Steps w = steps_for<T::kLog>(a, s, j.row0, T::kRows);
+    const int i0 = static_cast<int>(static_cast<int64_t>(w.count) * split / splits);
+    const int i1 = static_cast<int>(static_cast<int64_t>(w.count) * (split + 1) / splits);
+    T job;
+    job.run(a, buf, s, w, j.b, j.kvh, j.row0, i0, i1,
+            splits > 1 ? a.part + static_cast<int64_t>(blockIdx.x) * tile_part(T::kRows, T::kDp) : nullptr);
+}
+
+// One workgroup a row of a tile whose steps were shared: its partial results joined.
+template <int NB>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_tiles(const AttnArgs a, int tiles, int splits, int rows) {
+    constexpr int kDp = 16 * NB, kWide = kDp / 4, kSlices = kAttnThreads / kWide;
+    __shared__ f32x4 sums[kSlices][kWide];
+    const int item = blockIdx.x / rows, row = blockIdx.x - item * rows;
+    const TileJob j = tile_job(a, item, tiles, rows);
+    if (j.b >= a.batch) return;
+    const Sequence s = sequence_of(a, j.b);
+    if (j.row0 + row >= s.computed * a.group) return;
+    const int slice = threadIdx.x / kWide, col = threadIdx.x % kWide;
+    const float *part = a.part + static_cast<int64_t>(item) * splits * tile_part(rows, kDp);
+    const auto ml = [&](int k) { return part + k * tile_part(rows, kDp) + rows * kDp + 2 * row; };
+    float top = -__builtin_inff();
+    for (int k = 0; k < splits; ++k) top = __builtin_fmaxf(top, ml(k)[0]);
+    f32x4 v = {0, 0, 0, 0};
+    float sum = 0.0f;
+    for (int k = 0; k < splits; ++k) {
+        const float mk = ml(k)[0], f = mk == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mk - top);
+        sum += ml(k)[1] * f;
+        if (k % kSlices == slice) v += *reinterpret_cast<const f32x4 *>(part + k * tile_part(rows, kDp) + row * kDp + 4 * col) * f;
+    }
+    if (slice < kSlices) sums[slice][col] = v;
+    __syncthreads();
+    if (slice > 0 || 4 * col >= a.c.head_dim) return;
+#pragma unroll
+    for (int k = 1; k < kSlices; ++k) v += sums[k][col];
+    const int global_row = j.row0 + row, i = global_row / a.group, head = j.kvh * a.group + (global_row - i * a.group);
+    const float g = a.c.v_global != nullptr ? a.c.v_global[j.kvh] : 1.0f;
+    store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 4 * col,
+           sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum) * g, a.bf16 != 0, a.o_wide);
 }
 
 }  // namespace nvfp4attn

@@ -97,38 +97,70 @@ inline int64_t span_of(const Grid &g) { return extent(g) * g.bytes; }
 
 // ---------------------------------------------------------------- attention
 // Query rows (tokens times heads of one kv head) that a workgroup of the stream
-// kernel holds: 16, 32 or 64, the last where its sums fit the registers.
-inline int64_t stream_rows(int64_t dp) { return dp <= 128 ? 64 : 32; }
+// kernel holds: 16, or 32 where their sums fit the registers of two waves a SIMD.
+inline int64_t stream_rows(int64_t dp) { return dp <= 128 ? 32 : 16; }
+// Steps of the cache up to which one workgroup takes a sequence and kv head alone.
+constexpr int64_t kWholeSteps = 8;
 
-constexpr int64_t kStreamGroups = 3 * kComputeUnits;   // workgroups that share the cache's steps
+// Workgroups of four waves that a compute unit holds: what the stream kernel's
+// registers are kept to (512 a lane of a SIMD; no variant needs accumulation
+// registers, which the loads in flight must not end up in).
+constexpr int groups_per_unit(int64_t dp, int64_t rows) {
+    return rows <= 16 ? (dp <= 64 ? 4 : dp <= 128 ? 3 : 2) : 2;
+}
+
+// Rows of a workgroup of the tile kernel, 32 a wave: 8 waves decode a step of the cache
+// half as often as 4, which fill the chip with half as many rows.
+constexpr int64_t kTileRows = 256, kTileRowsFew = 128;
+constexpr int64_t kMaxSplits = 64;
+
+enum AttnKind { kWhole, kShared, kTiled };
 
 struct AttnPlan {
-    bool shared;          // the steps of all sequences are dealt out evenly over the workgroups
+    AttnKind kind;
     int64_t rows;         // query rows of a workgroup
     int64_t groups;       // workgroups
+    int64_t tiles;        // kTiled: bound on the row tiles of all sequences
+    int64_t splits;       // kTiled: workgroups that share a tile's steps
     size_t part_bytes, ml_bytes, prefix_bytes;
     size_t ws_bytes() const { return part_bytes + ml_bytes + prefix_bytes; }
 };
 
-// max_query: bound on a sequence's queries; steps: bound on its steps of the cache.
+// max_query: bound on a sequence's queries, max_context on its tokens in the cache.
 inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t batch, int64_t tokens,
                           int64_t max_query, int64_t max_context) {
     AttnPlan p = {};
     const int64_t dp = padded_dim(head_dim), group = heads / kv_heads, rows = max_query * group;
     const int64_t steps = ceil_div(max_context, kStepTokens);
-    const int64_t most = stream_rows(dp);
-    p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : most;
-    if (rows <= most && steps > 8) {
-        p.shared = true;
-        p.groups = kStreamGroups;
-        p.part_bytes = static_cast<size_t>(2 * p.groups * p.rows * dp) * 4;
-        p.ml_bytes = static_cast<size_t>(2 * p.groups * p.rows * 2) * 4;
-        p.prefix_bytes = static_cast<size_t>(batch + 1) * 8;
-    } else {
-        // tiles of a sequence: ceil(queries * group / rows), over all sequences at most
-        const int64_t tiles = rows <= most ? batch : tokens * group / p.rows + batch;
-        p.groups = tiles * kv_heads;
+    p.splits = 1;
+    if (rows <= stream_rows(dp)) {
+        p.rows = rows <= 16 ? 16 : 32;
+        p.kind = steps <= kWholeSteps ? kWhole : kShared;
+        p.groups = batch * kv_heads;
+        if (p.kind == kShared) {
+            p.groups = groups_per_unit(dp, p.rows) * kComputeUnits;
+            p.part_bytes = static_cast<size_t>(2 * p.groups * p.rows * dp) * 4;
+            p.ml_bytes = static_cast<size_t>(2 * p.groups * p.rows * 2) * 4;
+            p.prefix_bytes = static_cast<size_t>(batch + 1) * 8;
+        }
+        return p;
     }
+    p.kind = kTiled;
+    // tiles of a sequence: ceil(queries * group / rows); over all sequences at most
+    const auto bound = [&](int64_t r) {
+        const int64_t some = tokens * group / r + batch, each = batch * ceil_div(rows, r);
+        return some < each ? some : each;
+    };
+    p.rows = rows > kTileRowsFew && bound(kTileRows) * kv_heads >= kComputeUnits ? kTileRows : kTileRowsFew;
+    p.tiles = bound(p.rows);
+    const int64_t items = p.tiles * kv_heads, fill = 2 * kComputeUnits * kTileRowsFew / p.rows;
+    if (items < fill && steps > kWholeSteps) {
+        p.splits = ceil_div(fill, items);
+        if (p.splits > ceil_div(steps, kWholeSteps)) p.splits = ceil_div(steps, kWholeSteps);
+        if (p.splits > kMaxSplits) p.splits = kMaxSplits;
+    }
+    p.groups = items * p.splits;
+    if (p.splits > 1) p.part_bytes = static_cast<size_t>(p.groups * p.rows * (dp + 2)) * 4;
     return p;
 }
 
@@ -136,7 +168,7 @@ inline int check_attn_shape(const nvfp4_kv_cache_t &c, int64_t heads, int64_t ba
                             int64_t max_query, int64_t table_width) {
     if (check_cache_shape(c) != NVFP4_GEMV_OK || heads < c.kv_heads || heads > kMaxHeads ||
         heads % c.kv_heads != 0 || tokens < 0 || tokens > kMaxTokens || tokens * heads >= (int64_t(1) << 31) ||
-        batch < 1 || batch > kMaxBatch || batch * c.kv_heads >= (int64_t(1) << 24) || max_query < 1 ||
+        batch < 1 || batch > kMaxBatch || batch * c.kv_heads >= (int64_t(1) << 22) || max_query < 1 ||
         (tokens > 0 && max_query > tokens) || table_width < 1 ||
         table_width > ((int64_t(1) << 31) - 1) / c.page_size)
         return NVFP4_GEMV_ERR_BAD_SHAPE;
