@@ -48,9 +48,9 @@ struct AttnArgs {
     int32_t pages, table_width, batch, group, tokens, max_query, window, sinks, bf16;
     bool q_wide, o_wide;
     float scale;
-    float *part, *ml;      // per workgroup two partial results: [rows][dp] sums, [rows][2] maximum and sum
-    int64_t *prefix;       // [batch + 1] steps of the sequences before each
-    int32_t groups;        // workgroups among which the steps are dealt out
+    float *part, *ml;      // partial results: [rows][dp] sums, [rows][2] maximum and sum
+    int64_t *prefix;       // [batch + 1] pieces of one kv head of the sequences before each
+    int32_t groups;        // pieces into which the steps are dealt
 };
 
 struct Sequence {
@@ -491,35 +491,41 @@ struct Stream {
         wave_fence();
     }
 
-    // Query rows row0 .. of sequence s as B operands.
-    __device__ __forceinline__ void load_queries(const AttnArgs &a, const Sequence &s, int kvh, int row0) {
+    // Query rows row0 .. of sequence s, and their positions.
+    __device__ __forceinline__ void fetch_queries(const AttnArgs &a, const Sequence &s, int kvh, int row0, u32x4 (&raw)[R][kK]) {
         const auto [lane, r16, h] = this_lane();
         const int rows = s.computed * a.group;
-        const float g = a.scale * (a.c.k_global != nullptr ? a.c.k_global[kvh] : 1.0f);
-        const bool bf16 = a.bf16 != 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = row0 + 16 * r + r16;
+            const int row = row0 + 16 * r + static_cast<int>(r16);
             const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
             pos[r] = -1;
-            u32x4 raw[kK];
 #pragma unroll
-            for (int j = 0; j < kK; ++j) raw[j] = u32x4{0, 0, 0, 0};
+            for (int j = 0; j < kK; ++j) raw[r][j] = u32x4{0, 0, 0, 0};
             if (row < rows) {
                 const int at = s.len - s.n + i;
                 pos[r] = at < 0 ? -1 : at;
                 const uint16_t *p = a.q + static_cast<int64_t>(s.first + i) * a.q_token + head * a.q_head;
 #pragma unroll
                 for (int j = 0; j < kK; ++j) {
-                    const int e0 = h * (kDp / 4) + 8 * j;
-                    if (e0 < a.c.head_dim) raw[j] = load8(p + e0, a.q_wide);
+                    const int e0 = static_cast<int>(h) * (kDp / 4) + 8 * j;
+                    if (e0 < a.c.head_dim) raw[r][j] = load8(p + e0, a.q_wide);
                 }
             }
+        }
+    }
+
+    // As B operands.
+    __device__ __forceinline__ void take_queries(const AttnArgs &a, int kvh, const u32x4 (&raw)[R][kK]) {
+        const float g = a.scale * (a.c.k_global != nullptr ? a.c.k_global[kvh] : 1.0f);
+        const bool bf16 = a.bf16 != 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
             float x[kK][8];
             uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < kK; ++j) {
-                widen(raw[j], bf16, x[j]);
+                widen(raw[r][j], bf16, x[j]);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const uint32_t b = __float_as_uint(x[j][k]) & 0x7FFFFFFFu;
@@ -550,7 +556,17 @@ struct Stream {
                                         int row0, int i0, int i1, int64_t slot) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         const int32_t *row = a.table + static_cast<int64_t>(b) * a.table_stride;
-        load_queries(a, s, kvh, row0);
+        uint8_t *stage = buf.v[wave];
+        int i = i0 + wave;
+        const int at0 = i < i1 ? w.at(i) : -1;
+        const int e0 = at0 >= 0 ? entry(a, row, s.len, at0) : -1;
+        u32x4 raw[R][kK];
+        fetch_queries(a, s, kvh, row0, raw);
+        if (at0 >= 0) {
+            load_v(a, kvh, at0, e0);
+            load_k(a, kvh, at0, e0);
+        }
+        take_queries(a, kvh, raw);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m[r] = -__builtin_inff();
@@ -558,13 +574,8 @@ struct Stream {
 #pragma unroll
             for (int k = 0; k < NB; ++k) acc[r][k] = f32x4{0, 0, 0, 0};
         }
-        uint8_t *stage = buf.v[wave];
-        int i = i0 + wave;
-        if (i < i1) {
-            int at = w.at(i);
-            int e = entry(a, row, s.len, at);
-            load_v(a, kvh, at, e);
-            load_k(a, kvh, at, e);
+        if (at0 >= 0) {
+            int at = at0, e = e0;
             int next = i + kAttnWaves < i1 ? w.at(i + kAttnWaves) : -1;
             int e_next = next >= 0 ? entry(a, row, s.len, next) : -1;
             for (;;) {
@@ -652,6 +663,23 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// Sums over the lanes, and over the lanes up to and with each.
+__device__ __forceinline__ uint32_t wave_upto(uint32_t v) {
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const uint32_t x = static_cast<uint32_t>(__shfl_up(static_cast<int>(v), o, kWave));
+        v += lane >= o ? x : 0u;
+    }
+    return v;
+}
+__device__ __forceinline__ int64_t wave_total(int v) {   // 64 values below 2^25
+    uint32_t x = static_cast<uint32_t>(v);
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) x += static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), o, kWave));
+    return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(x)));
+}
+
 // count(b) of up to 64 sequences from b0 on, one a lane, and their sum over the lanes
 // up to and with each (below 64 * 2^25).
 struct Counts {
@@ -665,12 +693,7 @@ __device__ __forceinline__ Counts counts_from(int b0, int batch, Count count) {
     const int lane = threadIdx.x & (kWave - 1);
     Counts c;
     c.own = b0 + lane < batch ? static_cast<uint32_t>(count(b0 + lane)) : 0u;
-    c.upto = c.own;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const uint32_t x = static_cast<uint32_t>(__shfl_up(static_cast<int>(c.upto), o, kWave));
-        c.upto += lane >= o ? x : 0u;
-    }
+    c.upto = wave_upto(c.own);
     return c;
 }
 // The sequence that holds `at` where each counts count(b) * times, and where its
@@ -704,116 +727,186 @@ __global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * N
     job.run(a, buf, s, w, b, kvh, 0, 0, w.count, -1);
 }
 
-// First step of workgroup g of n that share `total` steps.
-__device__ __forceinline__ int64_t first_of(int64_t g, int64_t n, int64_t total) { return g * total / n; }
-__device__ __forceinline__ int64_t sharing(int64_t groups, int64_t total) {
-    const int64_t n = (total + kAttnWaves - 1) / kAttnWaves;
-    return n < groups ? (n > 0 ? n : 1) : groups;
+// Steps of a piece: the steps of all sequences and kv heads over the pieces wanted, a
+// step for each wave at least.
+__device__ __forceinline__ int piece_steps(int64_t total, int pieces) {
+    const int64_t each = total >> 31 == 0 ? static_cast<uint32_t>(total + pieces - 1) / static_cast<uint32_t>(pieces)
+                                          : (total + pieces - 1) / pieces;
+    // a sequence has less than 2^26 steps
+    return each < kAttnWaves ? kAttnWaves : each < (1 << 26) ? static_cast<int>(each) : 1 << 26;
 }
 
-// The steps of all sequences and kv heads, one after the other, in equal shares: a
-// workgroup's share may begin and end within a sequence, whose results it then
-// leaves as partial ones for attn_join.
+// Every sequence and kv head in pieces of nearly equal length, one a workgroup: more
+// pieces than fit the chip at once, so that one's beginning and end run beside
+// others' loads.  A sequence in one piece is finished by it, those in several leave
+// partial results for attn_join.  The pieces follow from the lengths on the device.
 template <int NB, int R>
-__global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * NB, 16 * R)) void attn_shared(const AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * NB, 16 * R)) void attn_pieces(const AttnArgs a) {
     using S = Stream<NB, R>;
     __shared__ typename S::Buffers buf;
+    const int lane = threadIdx.x & (kWave - 1);
+    // the first 64 sequences stay in registers, one a lane
+    Sequence own = {};
+    int steps = 0;
+    if (lane < a.batch) {
+        own = sequence_of(a, lane);
+        steps = steps_for<6>(a, own, 0, S::kRows).count;
+    }
     const auto count = [&](int b) { return steps_for<6>(a, sequence_of(a, b), 0, S::kRows).count; };
-    const int64_t heads = a.c.kv_heads;
-    int64_t total = 0;
+    int64_t total = wave_total(steps);
+    for (int b = kWave + lane; b - lane < a.batch; b += kWave) total += wave_total(b < a.batch ? count(b) : 0);
+    const int each = piece_steps(total * a.c.kv_heads, a.groups);
+
+    int64_t before = 0;                                // pieces of one kv head of the sequences before
+    int found = -1, part = 0, kvh = 0, pieces = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-        const Counts c = counts_from(b0, a.batch, count);
-        if (blockIdx.x == 0 && threadIdx.x < kWave && b0 + static_cast<int>(threadIdx.x) < a.batch)
-            a.prefix[b0 + threadIdx.x] = total + (c.upto - c.own);
-        total += c.all();
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.batch] = total;
-    total = uniform64(total) * heads;
-    const int64_t n = sharing(a.groups, total);
-    if (static_cast<int64_t>(blockIdx.x) >= n || total == 0) return;
-    int64_t at = first_of(blockIdx.x, n, total);
-    const int64_t end = first_of(static_cast<int64_t>(blockIdx.x) + 1, n, total);
-    int64_t before = 0;
-    int b = __builtin_amdgcn_readfirstlane(sequence_with(at, heads, a.batch, count, &before));
-    int64_t offset = at - before;
-    int left = static_cast<int>(end - at);             // below 2^31: a sequence's steps times kv heads over n
-    bool first = true;
-    while (left > 0) {
-        const Sequence s = sequence_of(a, b);
-        const Steps w = steps_for<6>(a, s, 0, S::kRows);
-        const int64_t steps = static_cast<int64_t>(w.count) * heads;
-        if (offset >= steps) {
-            offset -= steps;
-            ++b;
-            continue;
+        const int n = b0 == 0 ? steps : b0 + lane < a.batch ? count(b0 + lane) : 0;
+        const uint32_t mine = static_cast<uint32_t>(n + each - 1) / static_cast<uint32_t>(each);   // n < 2^25
+        const uint32_t upto = wave_upto(mine);
+        const int64_t end = (before + upto) * a.c.kv_heads;
+        if (blockIdx.x == 0 && threadIdx.x < kWave && b0 + lane < a.batch) a.prefix[b0 + lane] = before + upto - mine;
+        const uint64_t past = __ballot(end > static_cast<int64_t>(blockIdx.x));
+        if (past != 0 && found < 0) {
+            const int k = __builtin_ctzll(past);
+            found = b0 + k;
+            pieces = __builtin_amdgcn_readlane(static_cast<int>(mine), k);
+            const int64_t start = (before + static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto - mine), k))) * a.c.kv_heads;
+            const uint32_t at = static_cast<uint32_t>(static_cast<int64_t>(blockIdx.x) - start);
+            kvh = static_cast<int>(at / static_cast<uint32_t>(pieces));
+            part = static_cast<int>(at) - kvh * pieces;
+            if (blockIdx.x != 0) break;                // the first workgroup goes on with the prefix
         }
-        const int kvh = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint64_t>(offset) / static_cast<uint32_t>(w.count)));
-        const int i0 = static_cast<int>(offset - static_cast<int64_t>(kvh) * w.count);
-        const int i1 = left < w.count - i0 ? i0 + left : w.count;
-        const bool complete = i0 == 0 && i1 == w.count;
-        S job;
-        job.run(a, buf, s, w, b, kvh, 0, i0, i1, complete ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1));
-        first = false;
-        left -= i1 - i0;
-        offset += i1 - i0;
+        before += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto), kWave - 1));
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.batch] = before;
+    if (found < 0) return;
+    Sequence s;
+    if (found < kWave) {
+        s.len = __builtin_amdgcn_readlane(own.len, found);
+        s.first = __builtin_amdgcn_readlane(own.first, found);
+        s.n = __builtin_amdgcn_readlane(own.n, found);
+        s.computed = __builtin_amdgcn_readlane(own.computed, found);
+    } else {
+        s = sequence_of(a, found);
+    }
+    const Steps w = steps_for<6>(a, s, 0, S::kRows);
+    // pieces of a sequence differ by a step at most
+    const int base = w.count / pieces, longer = w.count - base * pieces;
+    const int i0 = part * base + (part < longer ? part : longer), i1 = i0 + base + (part < longer ? 1 : 0);
+    S job;
+    job.run(a, buf, s, w, found, kvh, 0, i0, i1, pieces == 1 ? -1 : static_cast<int64_t>(blockIdx.x));
 }
 
-// One workgroup a query row (`used` of the `rows` that a partial result holds): its
-// partial results joined, or zeros where there are none.
+// Weighted sum of `n` partial results (sums from `part` on, `stride` floats apart, and
+// maximum and sum at `ml`, `ml_stride` apart) of one row, by a workgroup: four
+// elements a thread, slices of the partial results.  Every thread of slice 0 gets the
+// sums and the weights' total.  All loads of a round are on their way together.
+template <int NB>
+struct Joiner {
+    static constexpr int kDp = 16 * NB, kWide = kDp / 4, kSlices = kAttnThreads / kWide;
+    static constexpr int kAhead = 8;
+    struct Buffers {
+        f32x4 sums[kSlices][kWide];
+        float weight[kAttnThreads];
+        float best[kAttnWaves], total[kAttnWaves];
+    };
+    f32x4 v;
+    float total;
+
+    __device__ __forceinline__ void run(Buffers &buf, const float *part, int64_t stride, const float *ml, int64_t ml_stride,
+                                        int n) {
+        const int slice = threadIdx.x / kWide, col = threadIdx.x % kWide;
+        const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+        v = f32x4{0, 0, 0, 0};
+        total = 0.0f;
+        float best = -__builtin_inff();                // of the rounds before
+        for (int k0 = 0; k0 < n; k0 += kAttnThreads) {
+            const int here = n - k0 < kAttnThreads ? n - k0 : kAttnThreads;
+            f32x4 ahead[kAhead];
+            const auto fetch = [&](int base) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int k = base + slice + i * kSlices;
+                    ahead[i] = f32x4{0, 0, 0, 0};
+                    if (slice < kSlices && k < here)
+                        ahead[i] = *reinterpret_cast<const f32x4 *>(part + (k0 + k) * stride + 4 * col);
+                }
+            };
+            fetch(0);
+            const int mine = threadIdx.x;
+            float m = -__builtin_inff(), l = 0.0f;
+            if (mine < here) {
+                m = ml[(k0 + mine) * ml_stride];
+                l = ml[(k0 + mine) * ml_stride + 1];
+            }
+            float top = m;
+#pragma unroll
+            for (int o = 1; o < kWave; o <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, kWave));
+            if (lane == 0) buf.best[wave] = top;
+            __syncthreads();
+            top = best;
+#pragma unroll
+            for (int k = 0; k < kAttnWaves; ++k) top = __builtin_fmaxf(top, buf.best[k]);
+            const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+            buf.weight[mine] = f;
+            const float sum = nvfp4dev::wave_sum(mine < here ? l * f : 0.0f);
+            if (lane == 0) buf.total[wave] = sum;
+            const float old = best == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(best - top);
+            best = top;
+            __syncthreads();
+            v *= old;
+            total *= old;
+#pragma unroll
+            for (int k = 0; k < kAttnWaves; ++k) total += buf.total[k];
+            for (int base = 0;;) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int k = base + slice + i * kSlices;
+                    if (slice < kSlices && k < here) v += ahead[i] * buf.weight[k];
+                }
+                base += kAhead * kSlices;
+                if (base >= here) break;
+                fetch(base);
+            }
+            __syncthreads();
+        }
+        if (slice < kSlices) buf.sums[slice][col] = v;
+        __syncthreads();
+        if (slice == 0) {
+#pragma unroll
+            for (int k = 1; k < kSlices; ++k) v += buf.sums[k][col];
+        }
+    }
+
+    // The row's four elements of a thread of slice 0.
+    __device__ __forceinline__ void store(const AttnArgs &a, const Sequence &s, int kvh, int row) const {
+        const int slice = threadIdx.x / kWide, col = threadIdx.x % kWide;
+        if (slice > 0 || 4 * col >= a.c.head_dim) return;
+        const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
+        const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
+        store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 4 * col,
+               total == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / total) * g, a.bf16 != 0, a.o_wide);
+    }
+};
+
+// One workgroup a query row (`used` of the `rows` that a partial result holds): the
+// results of its pieces joined, or zeros where there are none.
 template <int NB>
 __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int rows, int used) {
-    constexpr int kDp = 16 * NB, kWide = kDp / 4, kSlices = kAttnThreads / kWide;
-    __shared__ f32x4 sums[kSlices][kWide];
-    const int row = blockIdx.x % used, item = blockIdx.x / used;
+    using J = Joiner<NB>;
+    __shared__ typename J::Buffers buf;
+    const int item = blockIdx.x / used, row = blockIdx.x - item * used;
     const int b = item / a.c.kv_heads, kvh = item - b * a.c.kv_heads;
+    const int64_t before = a.prefix[b];
+    const int pieces = static_cast<int>(a.prefix[b + 1] - before);
+    if (pieces == 1) return;                           // finished by its workgroup
     const Sequence s = sequence_of(a, b);
     if (row >= s.computed * a.group) return;
-    const int64_t heads = a.c.kv_heads, before = a.prefix[b], count = a.prefix[b + 1] - before;
-    const int64_t total = a.prefix[a.batch] * heads, n = sharing(a.groups, total);
-    const int slice = threadIdx.x / kWide, col = threadIdx.x % kWide;
-    f32x4 v = {0, 0, 0, 0};
-    float sum = 0.0f;
-    if (count > 0) {
-        const int64_t x = before * heads + kvh * count, y = x + count - 1;
-        const auto owner = [&](int64_t p) {
-            int64_t g = p * n / total;
-            while (g + 1 < n && first_of(g + 1, n, total) <= p) ++g;
-            while (g > 0 && first_of(g, n, total) > p) --g;
-            return g;
-        };
-        const int64_t g0 = owner(x), g1 = owner(y);
-        if (g0 == g1) return;                      // its workgroup had all of it
-        const auto slot = [&](int64_t g) { return 2 * g + (g == g0 && first_of(g0, n, total) < x ? 1 : 0); };
-        float top = -__builtin_inff();
-        for (int64_t g = g0; g <= g1; ++g) top = __builtin_fmaxf(top, a.ml[(slot(g) * rows + row) * 2]);
-        if (slice < kSlices) {
-            for (int64_t g = g0 + slice; g <= g1; g += kSlices) {
-                const int64_t at = slot(g) * rows + row;
-                const float mk = a.ml[at * 2];
-                const float f = mk == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mk - top);
-                v += *reinterpret_cast<const f32x4 *>(a.part + at * kDp + 4 * col) * f;
-            }
-            sums[slice][col] = v;
-        }
-        for (int64_t g = g0; g <= g1; ++g) {
-            const int64_t at = slot(g) * rows + row;
-            const float mk = a.ml[at * 2];
-            sum += a.ml[at * 2 + 1] * (mk == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mk - top));
-        }
-        __syncthreads();
-        if (slice > 0) return;
-        v = sums[0][col];
-#pragma unroll
-        for (int k = 1; k < kSlices; ++k) v += sums[k][col];
-    } else if (slice > 0) {
-        return;
-    }
-    if (4 * col >= a.c.head_dim) return;
-    const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
-    const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
-    store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 4 * col,
-                          sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum) * g, a.bf16 != 0, a.o_wide);
+    const int64_t first = before * a.c.kv_heads + static_cast<int64_t>(kvh) * pieces;
+    J job;
+    job.run(buf, a.part + (first * rows + row) * J::kDp, static_cast<int64_t>(rows) * J::kDp,
+            a.ml + (first * rows + row) * 2, 2 * rows, pieces);
+    job.store(a, s, kvh, row);
 }
 
 // ---------------------------------------------------------------- the tile kernel
@@ -1256,37 +1349,25 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void attn_tiles(const AttnArgs a,
             splits > 1 ? a.part + static_cast<int64_t>(blockIdx.x) * tile_part(T::kRows, T::kDp) : nullptr);
 }
 
-// One workgroup a row of a tile whose steps were shared: its partial results joined.
+// Rows of a tile whose steps were shared, kJoinRows a workgroup one after the other:
+// their partial results joined.
+constexpr int kJoinRows = 8;
 template <int NB>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_tiles(const AttnArgs a, int tiles, int splits, int rows) {
-    constexpr int kDp = 16 * NB, kWide = kDp / 4, kSlices = kAttnThreads / kWide;
-    __shared__ f32x4 sums[kSlices][kWide];
-    const int item = blockIdx.x / rows, row = blockIdx.x - item * rows;
+    using J = Joiner<NB>;
+    __shared__ typename J::Buffers buf;
+    const int chunks = rows / kJoinRows, item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
     const TileJob j = tile_job(a, item, tiles, rows);
     if (j.b >= a.batch) return;
     const Sequence s = sequence_of(a, j.b);
-    if (j.row0 + row >= s.computed * a.group) return;
-    const int slice = threadIdx.x / kWide, col = threadIdx.x % kWide;
-    const float *part = a.part + static_cast<int64_t>(item) * splits * tile_part(rows, kDp);
-    const auto ml = [&](int k) { return part + k * tile_part(rows, kDp) + rows * kDp + 2 * row; };
-    float top = -__builtin_inff();
-    for (int k = 0; k < splits; ++k) top = __builtin_fmaxf(top, ml(k)[0]);
-    f32x4 v = {0, 0, 0, 0};
-    float sum = 0.0f;
-    for (int k = 0; k < splits; ++k) {
-        const float mk = ml(k)[0], f = mk == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mk - top);
-        sum += ml(k)[1] * f;
-        if (k % kSlices == slice) v += *reinterpret_cast<const f32x4 *>(part + k * tile_part(rows, kDp) + row * kDp + 4 * col) * f;
+    const int64_t each = tile_part(rows, J::kDp);
+    const float *part = a.part + static_cast<int64_t>(item) * splits * each;
+    for (int row = chunk * kJoinRows; row < (chunk + 1) * kJoinRows && j.row0 + row < s.computed * a.group; ++row) {
+        J job;
+        job.run(buf, part + row * J::kDp, each, part + rows * J::kDp + 2 * row, each, splits);
+        job.store(a, s, j.kvh, j.row0 + row);
+        __syncthreads();
     }
-    if (slice < kSlices) sums[slice][col] = v;
-    __syncthreads();
-    if (slice > 0 || 4 * col >= a.c.head_dim) return;
-#pragma unroll
-    for (int k = 1; k < kSlices; ++k) v += sums[k][col];
-    const int global_row = j.row0 + row, i = global_row / a.group, head = j.kvh * a.group + (global_row - i * a.group);
-    const float g = a.c.v_global != nullptr ? a.c.v_global[j.kvh] : 1.0f;
-    store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 4 * col,
-           sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum) * g, a.bf16 != 0, a.o_wide);
 }
 
 }  // namespace nvfp4attn

@@ -120,6 +120,7 @@ struct AttnPlan {
     AttnKind kind;
     int64_t rows;         // query rows of a workgroup
     int64_t groups;       // workgroups
+    int64_t pieces;       // kShared: pieces into which the cache's steps are dealt
     int64_t tiles;        // kTiled: bound on the row tiles of all sequences
     int64_t splits;       // kTiled: workgroups that share a tile's steps
     size_t part_bytes, ml_bytes, prefix_bytes;
@@ -138,9 +139,11 @@ inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int
         p.kind = steps <= kWholeSteps ? kWhole : kShared;
         p.groups = batch * kv_heads;
         if (p.kind == kShared) {
-            p.groups = groups_per_unit(dp, p.rows) * kComputeUnits;
-            p.part_bytes = static_cast<size_t>(2 * p.groups * p.rows * dp) * 4;
-            p.ml_bytes = static_cast<size_t>(2 * p.groups * p.rows * 2) * 4;
+            // every sequence and kv head ends with a piece that may be short
+            p.pieces = 2 * groups_per_unit(dp, p.rows) * kComputeUnits;
+            p.groups += p.pieces;
+            p.part_bytes = static_cast<size_t>(p.groups * p.rows * dp) * 4;
+            p.ml_bytes = static_cast<size_t>(p.groups * p.rows * 2) * 4;
             p.prefix_bytes = static_cast<size_t>(batch + 1) * 8;
         }
         return p;

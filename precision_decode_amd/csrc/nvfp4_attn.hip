@@ -160,7 +160,7 @@ AttnPlan plan_of(const AttnCall &c) {
 template <int NB, int R>
 int launch_stream(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
     if (p.kind == kWhole) return run(attn_whole<NB, R>, p.groups, kAttnThreads, stream, a);
-    const int s = run(attn_shared<NB, R>, p.groups, kAttnThreads, stream, a);
+    const int s = run(attn_pieces<NB, R>, p.groups, kAttnThreads, stream, a);
     if (s != NVFP4_GEMV_OK) return s;
     const int rows = 16 * R, most = a.max_query * a.group, used = most < rows ? most : rows;
     return run(attn_join<NB>, static_cast<int64_t>(a.batch) * a.c.kv_heads * used, kAttnThreads, stream, a, rows, used);
@@ -173,7 +173,7 @@ int launch_attn(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
         const int s = p.rows == kTileRows ? run(attn_tiles<NB, 8>, p.groups, 8 * kWave, stream, a, tiles, splits)
                                           : run(attn_tiles<NB, 4>, p.groups, 4 * kWave, stream, a, tiles, splits);
         if (s != NVFP4_GEMV_OK || splits == 1) return s;
-        return run(attn_join_tiles<NB>, p.tiles * a.c.kv_heads * rows, kAttnThreads, stream, a, tiles, splits, rows);
+        return run(attn_join_tiles<NB>, p.tiles * a.c.kv_heads * (rows / kJoinRows), kAttnThreads, stream, a, tiles, splits, rows);
     }
     if (p.rows == 16) return launch_stream<NB, 1>(a, p, stream);
     if constexpr (NB <= 8) return launch_stream<NB, 2>(a, p, stream);
@@ -207,7 +207,7 @@ int attention(const AttnCall &c, const AttnPlan &p, uint8_t *ws, hipStream_t str
     a.q_wide = wide_rows(c.Q, c.q_token, c.q_head);
     a.o_wide = wide_rows(c.out, c.o_token, c.o_head);
     a.scale = c.scale;
-    a.groups = static_cast<int32_t>(p.groups);
+    a.groups = static_cast<int32_t>(p.pieces);
     if (p.part_bytes > 0) {
         a.part = reinterpret_cast<float *>(ws);
         a.ml = reinterpret_cast<float *>(ws + p.part_bytes);
