@@ -46,6 +46,8 @@ struct AttnArgs {
     const int32_t *table, *lengths, *starts;
     int64_t table_stride;
     int32_t pages, table_width, batch, group, tokens, max_query, window, sinks, bf16;
+    int32_t each;          // queries of every sequence where `starts` is NULL
+    uint32_t group_inverse;   // ceil(2^26 / group): row / group of rows below 32
     bool q_wide, o_wide;
     float scale;
     float *part, *ml;      // partial results: [rows][dp] sums, [rows][2] maximum and sum
@@ -75,7 +77,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttnArgs &a, int b) {
         s.first = x;
         s.n = y - x;
     } else {
-        s.n = a.tokens / a.batch;
+        s.n = a.each;
         s.first = b * s.n;
     }
     s.computed = s.n < a.max_query ? s.n : a.max_query;
@@ -90,15 +92,13 @@ struct Steps {
     __device__ __forceinline__ int at(int i) const { return i < sinks ? i : from + (i - sinks); }
 };
 
+// For queries first .. last of sequence s.
 template <int LOG>
-__device__ __forceinline__ Steps steps_for(const AttnArgs &a, const Sequence &s, int row0, int rows) {
+__device__ __forceinline__ Steps steps_between(const AttnArgs &a, const Sequence &s, int first, int last) {
     Steps w = {};
-    const int last_row = s.computed * a.group - 1;
-    if (row0 > last_row) return w;
-    const int end_row = row0 + rows - 1 < last_row ? row0 + rows - 1 : last_row;
-    w.p_first = s.len - s.n + row0 / a.group;
-    w.p_last = s.len - s.n + end_row / a.group;
-    if (w.p_last < 0) return w;
+    w.p_first = s.len - s.n + first;
+    w.p_last = s.len - s.n + last;
+    if (first > last || w.p_last < 0) return w;
     const int hi = w.p_last + 1;
     int lo = 0;
     if (a.window > 0) {
@@ -110,6 +110,17 @@ __device__ __forceinline__ Steps steps_for(const AttnArgs &a, const Sequence &s,
     w.sinks = sinks < w.from ? sinks : w.from;
     w.count = w.sinks + steps_of<LOG>(hi) - w.from;
     return w;
+}
+// For all of its queries.
+template <int LOG>
+__device__ __forceinline__ Steps steps_for(const AttnArgs &a, const Sequence &s) {
+    return steps_between<LOG>(a, s, 0, s.computed - 1);
+}
+// For query rows row0 .. row0 + rows - 1 (query times heads of a kv head).
+template <int LOG>
+__device__ __forceinline__ Steps steps_for(const AttnArgs &a, const Sequence &s, int row0, int rows) {
+    const int last_row = s.computed * a.group - 1, end = row0 + rows - 1 < last_row ? row0 + rows - 1 : last_row;
+    return row0 > last_row ? Steps{} : steps_between<LOG>(a, s, row0 / a.group, end / a.group);
 }
 
 __device__ __forceinline__ float xor16(float v, bool take_max) {
@@ -137,6 +148,28 @@ __device__ __forceinline__ void row_power(uint32_t top, float *up, float *down) 
     e = e < -100 ? -100 : e > 127 ? 127 : e;
     *up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
     *down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+}
+
+// The largest magnitude pattern among 16-bit values, two a word.
+template <int N>
+__device__ __forceinline__ uint32_t top16(const u32x4 (&w)[N]) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j][i] & 0x7FFF7FFFu));
+    return top.x > top.y ? top.x : top.y;
+}
+// 8 bf16 values times a power of two, as fp16.
+__device__ __forceinline__ f16x8 scale_bf16(u32x4 w, float up) {
+    f16x8 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = static_cast<_Float16>(__uint_as_float(w[i] << 16) * up);
+        x[2 * i + 1] = static_cast<_Float16>(__uint_as_float(w[i] & 0xFFFF0000u) * up);
+    }
+    return x;
 }
 
 // Whether a query at position p (-1: none) sees token j.
@@ -193,24 +226,65 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Bytes of 4 x 4 turned: out word t holds byte t of each word.
-__device__ __forceinline__ void turn_bytes(u32x4 w, uint32_t (&t)[4]) {
-    const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
-    const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
-    t[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
-    t[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
-    t[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
-    t[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
-}
-
 // ---------------------------------------------------------------- the stream kernel
 //
 // A workgroup holds 16 R query rows of one sequence and kv head; its four waves
 // take the steps of the cache in turn, each with running maxima, sums and outputs
 // of its own that are joined at the end, so that waves never wait for each other
-// within the loop.  A lane of A operand r = lane % 16 holds token 16 (r / 4) +
-// 4 (r % 4) + t in score tile t: it then ends with the scores of 16 tokens of one
-// run in the order in which the transposed LDS read hands out V's.
+// within the loop.  A whole step is on its way while the one before is worked on:
+// K's codes in registers, read in runs of whole 128-byte lines; V's codes and all
+// scales straight into the other of a wave's two stages in LDS.  A lane of A operand
+// r = lane % 16 holds token 16 (r / 4) + 4 t + r % 4 in score tile t: it then ends
+// with the scores of the 16 tokens of run lane / 16, in the order in which the
+// transposed LDS read hands out V's.
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef const __attribute__((address_space(1))) void global_void_t;
+
+__device__ __forceinline__ uint32_t lds_address(const uint8_t *p) {
+    return static_cast<uint32_t>(reinterpret_cast<size_t>((__attribute__((address_space(3))) const uint8_t *)(p)));
+}
+// Every load to registers and to LDS has arrived.
+__device__ __forceinline__ void wait_loads() {
+    nvfp4dev::phase_fence();
+    __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));   // vmcnt 0, the other counters at their maximum
+    nvfp4dev::phase_fence();
+}
+
+// Reads of what direct-to-LDS loads brought, which the kernel has waited for.  The
+// compiler would put a wait for all loads in flight, the next step's too, before
+// reads that it knows of.  Each waits for its own data; outputs are early-clobber, as
+// a read may return while later ones still use their addresses.
+template <int N>
+__device__ __forceinline__ void lds_read16(uint32_t at, uint32_t apart, u32x4 (&x)[N]) {
+    static_assert(N >= 1 && N <= 4, "one to four blocks");
+    if constexpr (N == 1) {
+        asm volatile("ds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(x[0]) : "v"(at) : "memory");
+    } else if constexpr (N == 2) {
+        asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(x[0]), "=&v"(x[1]) : "v"(at), "v"(at + apart) : "memory");
+    } else if constexpr (N == 3) {
+        asm volatile("ds_read_b128 %0, %3\n\tds_read_b128 %1, %4\n\tds_read_b128 %2, %5\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]) : "v"(at), "v"(at + apart), "v"(at + 2 * apart) : "memory");
+    } else {
+        asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+                     : "v"(at), "v"(at + apart), "v"(at + 2 * apart), "v"(at + 3 * apart) : "memory");
+    }
+}
+// Transposed reads of blocks B .. B + 3: pieces at p0 and p1, two blocks of 8 bytes each.
+__device__ __forceinline__ void lds_read_turned(uint32_t p0, uint32_t p1, i32x2 (&x)[4]) {
+    asm volatile("ds_read_b64_tr_b4 %0, %4\n\tds_read_b64_tr_b4 %1, %4 offset:8\n\t"
+                 "ds_read_b64_tr_b4 %2, %5\n\tds_read_b64_tr_b4 %3, %5 offset:8\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]) : "v"(p0), "v"(p1) : "memory");
+}
+
+// A workgroup's piece: part `part` of the `pieces` of sequence b (-1: none) and kv head.
+struct Piece {
+    int b, kvh, part, pieces;
+    Sequence s;
+};
+
 template <int NB, int R>
 struct Stream {
     static constexpr int kDp = 16 * NB;
@@ -218,28 +292,24 @@ struct Stream {
     static constexpr int kK = kDp / 32;            // 32-element slices of a row: words a lane holds of a token
     static constexpr int kChunks = kDp / 32;       // 16-byte pieces of a token's codes
     static constexpr int kLaneBlocks = NB / 4;     // scale blocks of a lane's slice of K
-    static constexpr int kStage = kStep * kDp / 2; // a wave's V codes in LDS
+    static constexpr int kCodes = kStep * kDp / 2; // bytes of V's codes in a stage
+    static constexpr int kScales = 64 * NB;        // bytes of K's scales, then as many of V's: [block][64 tokens]
+    static constexpr int kStage = kCodes + 2 * kScales;
 
     // 16 rows times up to 8 blocks of outputs are joined at a time
     static constexpr int kJoinBlocks = NB < 8 ? NB : NB % 8 == 0 ? 8 : 6;
     static constexpr int kJoinRow = 16 * kJoinBlocks + 4;
 
-    struct Buffers {
-        union {
-            __attribute__((aligned(16))) uint8_t v[kAttnWaves][kStage];
+    union Buffers {
+        __attribute__((aligned(16))) uint8_t v[kAttnWaves][2][kStage];
+        struct {
             __attribute__((aligned(16))) float o[kAttnWaves][16][kJoinRow];
+            float m[kAttnWaves][kRows], l[kAttnWaves][kRows];
         };
-        float m[kAttnWaves][kRows], l[kAttnWaves][kRows];
+        Piece piece;
     };
 
-    // A step on its way: K's registers are free for the next step once its scores are
-    // there, V's once its codes are in LDS, so that both loads run ahead without a
-    // second set of registers.
-    uint32_t kw[4][kK];
-    uint32_t ks[kLaneBlocks];
-    u32x4 vw[kChunks];
-    u32x4 vsw;
-
+    uint32_t kw[4][kK];                            // K's codes on their way
     int wave;
     f16x8 q[R][kK];
     float c[R];                                    // scores to log2 units
@@ -265,75 +335,96 @@ struct Stream {
     }
     // Lane entry of run i, of all lanes.
     static __device__ __forceinline__ int page_of(int e, int i) { return __builtin_amdgcn_readlane(e, 4 * i); }
+    static __device__ __forceinline__ int page_of_run(int e, uint32_t run) {
+        return run == 0 ? page_of(e, 0) : run == 1 ? page_of(e, 1) : run == 2 ? page_of(e, 2) : page_of(e, 3);
+    }
 
-    __device__ __forceinline__ void load_k(const AttnArgs &a, int kvh, int s, int e) {
+    // Sends for step s: K's codes to kw, the rest to `stage`.  Pages of 64 tokens and
+    // more hold the whole step: addresses are then one base and offsets of the lane.
+    __device__ __forceinline__ void load(const AttnArgs &a, int kvh, int s, int e, uint8_t *stage) {
+        if (a.c.page_log2 >= 6) {
+            load<true>(a, kvh, s, e, stage);
+        } else {
+            load<false>(a, kvh, s, e, stage);
+        }
+    }
+    template <bool ONE_PAGE>
+    __device__ __forceinline__ void load(const AttnArgs &a, int kvh, int s, int e, uint8_t *stage) {
         const auto [lane, r16, h] = this_lane();
-        const int ps = 1 << a.c.page_log2;
-        const uint32_t off = ((s * kStep + kRun * (r16 >> 2)) & (ps - 1)) + 4 * (r16 & 3);
-        const uint64_t at = tokens_before(a, e, kvh);
-        const uint8_t *p = a.c.k_codes + (at + off) * (kDp / 2) + h * (kDp / 8);
+        const int ps = 1 << a.c.page_log2, tok0 = s * kStep;
+        const uint64_t base = tokens_before(a, page_of(e, 0), kvh);     // of ONE_PAGE
+        const uint32_t first = tok0 & (ps - 1);
+        // V's codes: pieces of 16 bytes, each lane's in the place that piece_at gives it
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const uint32_t at = i * kWave + lane, token = at / kChunks, piece = (at % kChunks) ^ turn(token);
+            const uint8_t *p;
+            if constexpr (ONE_PAGE) {
+                p = a.c.v_codes + (base + first) * (kDp / 2) + (token * (kDp / 2) + 16 * piece);
+            } else if constexpr (kWave / kChunks == kRun) {   // the lanes share a run
+                p = a.c.v_codes + (tokens_before(a, page_of(e, i), kvh) + ((tok0 + kRun * i) & (ps - 1))) * (kDp / 2) +
+                    ((token & (kRun - 1)) * (kDp / 2) + 16 * piece);
+            } else {
+                p = a.c.v_codes + (tokens_before(a, page_of_run(e, token >> 4), kvh) + ((tok0 + token) & (ps - 1))) * (kDp / 2) +
+                    16 * piece;
+            }
+            __builtin_amdgcn_global_load_lds((global_void_t *)p, (lds_void_t *)(stage + i * 1024), 16, 0, 0);
+        }
+        // scales: pieces of 16 tokens of a block, K's then V's
+#pragma unroll
+        for (int i = 0; i < (8 * NB + kWave - 1) / kWave; ++i) {
+            uint32_t at = i * kWave + lane;
+            if (8 * NB % kWave == 0 || at < 8 * NB) {
+                const bool is_v = at >= 4 * NB;
+                at = is_v ? at - 4 * NB : at;
+                const uint32_t block = at / 4, run = at % 4;
+                const uint8_t *p = is_v ? a.c.v_scales : a.c.k_scales;
+                if constexpr (ONE_PAGE) {
+                    p += base * NB + first + ((block << a.c.page_log2) + kRun * run);
+                } else {
+                    p += tokens_before(a, page_of_run(e, run), kvh) * NB + (block << a.c.page_log2) +
+                         ((tok0 + kRun * run) & (ps - 1));
+                }
+                __builtin_amdgcn_global_load_lds((global_void_t *)p, (lds_void_t *)(stage + kCodes + i * 1024), 16, 0, 0);
+            }
+        }
+        // K's codes: this lane's four tokens
+        const uint8_t *p;
+        if constexpr (ONE_PAGE) {
+            p = a.c.k_codes + (base + first) * (kDp / 2) + ((kRun * (r16 >> 2) + (r16 & 3)) * (kDp / 2) + h * (kDp / 8));
+        } else {
+            const uint32_t off = ((tok0 + kRun * (r16 >> 2)) & (ps - 1)) + (r16 & 3);
+            p = a.c.k_codes + (tokens_before(a, e, kvh) + off) * (kDp / 2) + h * (kDp / 8);
+        }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if constexpr (kK % 4 == 0) {
 #pragma unroll
                 for (int j = 0; j < kK; j += 4) {
-                    const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + t * (kDp / 2) + 4 * j));
+                    const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + t * (2 * kDp) + 4 * j));
                     kw[t][j] = w[0]; kw[t][j + 1] = w[1]; kw[t][j + 2] = w[2]; kw[t][j + 3] = w[3];
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < kK; j += 2) {
-                    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p + t * (kDp / 2) + 4 * j));
+                    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p + t * (2 * kDp) + 4 * j));
                     kw[t][j] = w[0]; kw[t][j + 1] = w[1];
                 }
             }
         }
-        const uint8_t *sp = a.c.k_scales + at * NB + off;
-#pragma unroll
-        for (int j = 0; j < kLaneBlocks; ++j)
-            ks[j] = *reinterpret_cast<const uint32_t *>(sp + ((h * kLaneBlocks + j) << a.c.page_log2));
     }
 
-    __device__ __forceinline__ void load_v(const AttnArgs &a, int kvh, int s, int e) {
-        const auto [lane, r16, h] = this_lane();
-        const int ps = 1 << a.c.page_log2, tok0 = s * kStep;
-        // pieces of 16 bytes in memory order
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const uint32_t at = i * kWave + lane, token = at / kChunks, piece = at % kChunks;
-            uint64_t base;
-            uint32_t off;
-            if constexpr (kWave / kChunks == kRun) {          // the lanes share a run
-                base = tokens_before(a, page_of(e, i), kvh) + ((tok0 + kRun * i) & (ps - 1));
-                off = (token & (kRun - 1)) * (kDp / 2) + 16 * piece;
-            } else {
-                const uint32_t run = token >> 4;
-                const int p = run == 0 ? page_of(e, 0) : run == 1 ? page_of(e, 1) : run == 2 ? page_of(e, 2) : page_of(e, 3);
-                base = tokens_before(a, p, kvh) + ((tok0 + token) & (ps - 1));
-                off = 16 * piece;
-            }
-            vw[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(a.c.v_codes + base * (kDp / 2) + off));
-        }
-        // scales: lane r16 of run h takes block r16, 16 tokens
-        const int p = h == 0 ? page_of(e, 0) : h == 1 ? page_of(e, 1) : h == 2 ? page_of(e, 2) : page_of(e, 3);
-        const uint32_t b = r16 < NB ? r16 : NB - 1;
-        vsw = *reinterpret_cast<const u32x4 *>(a.c.v_scales + tokens_before(a, p, kvh) * NB + (b << a.c.page_log2) +
-                                               ((tok0 + kRun * h) & (ps - 1)));
+    // Pieces of a token change places by this, so that 16 tokens' reads of one block fall
+    // on all banks.
+    static __device__ __forceinline__ uint32_t turn(uint32_t token) {
+        return kChunks == 2 ? (token >> 3) & 1 : kChunks == 4 ? (token >> 2) & 3 : kChunks == 6 ? (token >> 3) & 1 : (token >> 1) & 7;
     }
-
     static __device__ __forceinline__ uint32_t piece_at(uint32_t token, uint32_t piece) {
-        // pieces change places so that 16 tokens' reads of one block fall on all banks
-        const uint32_t f = kChunks == 2 ? (token >> 3) & 1 : kChunks == 4 ? (token >> 2) & 3
-                      : kChunks == 6 ? (token >> 3) & 1 : (token >> 1) & 7;
-        return token * (kDp / 2) + 16 * (piece ^ f);
+        return token * (kDp / 2) + 16 * (piece ^ turn(token));
     }
 
     template <int B>
-    __device__ __forceinline__ void block(const uint8_t *stage, uint32_t token, const f16x2 (&vs)[8], const f16x8 (&p)[R][2]) {
-        typedef __attribute__((address_space(3))) i32x2 lds2;
-        const uint8_t *at = stage + piece_at(token, B / 2) + 8 * (B % 2);
-        const i32x2 w = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds2 *)at);
-        if constexpr (B % 2 == 0) nvfp4dev::phase_fence();
+    __device__ __forceinline__ void block(i32x2 w, const f16x2 (&vs)[8], const f16x8 (&p)[R][2]) {
         f16x2 s[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = row_bcast<B>(vs[i]);
@@ -344,12 +435,21 @@ struct Stream {
             for (int r = 0; r < R; ++r) acc[r][B] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[r][k], acc[r][B], 0, 0, 0);
         }
     }
-    template <int... B>
-    __device__ __forceinline__ void blocks(std::integer_sequence<int, B...>, const uint8_t *stage, const f16x2 (&vs)[8],
+    // Blocks 4 G .. 4 G + 3 of the outputs.
+    template <int G>
+    __device__ __forceinline__ void four_blocks(uint32_t stage, uint32_t token, const f16x2 (&vs)[8], const f16x8 (&p)[R][2]) {
+        i32x2 w[4];
+        lds_read_turned(stage + piece_at(token, 2 * G), stage + piece_at(token, 2 * G + 1), w);
+        block<4 * G>(w[0], vs, p);
+        block<4 * G + 1>(w[1], vs, p);
+        block<4 * G + 2>(w[2], vs, p);
+        block<4 * G + 3>(w[3], vs, p);
+    }
+    template <int... G>
+    __device__ __forceinline__ void blocks(std::integer_sequence<int, G...>, uint32_t stage, const f16x2 (&vs)[8],
                                            const f16x8 (&p)[R][2]) {
         const Lane n = this_lane();
-        const uint32_t token = kRun * n.h + 4 * (n.r16 & 3) + (n.r16 >> 2);
-        (block<B>(stage, token, vs, p), ...);
+        (four_blocks<G>(stage, kRun * n.h + n.r16, vs, p), ...);
     }
 
     // Rows that see a token whose block of V is NaN: NaN there.  `bad` holds the
@@ -380,7 +480,7 @@ struct Stream {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (!page || !visible(a, pos[r], tok0 + kRun * static_cast<int>(h) + 4 * i + t)) sc[t][i] = -__builtin_inff();
+                if (!page || !visible(a, pos[r], tok0 + kRun * static_cast<int>(h) + 4 * t + i)) sc[t][i] = -__builtin_inff();
     }
 
     // Softmax of row tile r: its running maximum and sum, the step's weights as B
@@ -415,46 +515,28 @@ struct Stream {
         l[r] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
-    // Step s, whose pages e holds, on what is loaded; loads step `next` (pages e_next)
-    // on the way unless it is negative.
-    __device__ __forceinline__ void step(const AttnArgs &a, const Steps &w, int kvh, int s, int e, int next, int e_next,
-                                         uint8_t *stage) {
-        const uint32_t lane = this_lane().id;
+    // Step s, whose pages e holds and whose codes and scales are there: K's in k, the
+    // rest in `stage`.
+    __device__ __forceinline__ void step(const AttnArgs &a, const Steps &w, int s, int e, const uint32_t (&k)[4][kK],
+                                         uint32_t stage) {
+        const auto [lane, r16, h] = this_lane();
         const int tok0 = s * kStep;
         const uint64_t there = __ballot(e >= 0);       // lanes 4 i: run i
         const bool pages = there == ~uint64_t(0);
         const bool whole = pages && tok0 + kStep - 1 <= w.p_first &&
                            (a.window == 0 || tok0 > w.p_last - a.window || tok0 + kStep - 1 < a.sinks);
-        // V's codes to LDS
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const uint32_t at = i * kWave + lane;
-            *reinterpret_cast<u32x4 *>(stage + piece_at(at / kChunks, at % kChunks)) = vw[i];
-        }
-        // V's scales, and which of its blocks are NaN
-        uint32_t bad = 0;
-        if (!whole) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t nan = ((vsw[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                // one bit a byte, to bits 4 i .. 4 i + 3
-                bad |= ((nan >> 7) * 0x10204080u >> 28) << (4 * i);
-                vsw[i] &= ~((nan >> 7) * 0xFFu);
-            }
-        }
-        uint32_t turned[4];
-        turn_bytes(vsw, turned);
-        if (next >= 0) load_v(a, kvh, next, e_next);
-        wave_fence();
 
-        // scores
-        f32x4 sc[R][4];
+        // scores: the lane's tokens' scales are byte r % 4 of each word of their run's
+        u32x4 ks[kLaneBlocks];
+        lds_read16<kLaneBlocks>(stage + kCodes + h * (kLaneBlocks * 64) + (r16 >> 2) * 16, 64, ks);
         f16x2 kf[kLaneBlocks][2];
+        const uint32_t pick = (r16 & 3) * 0x0101u | 0x0400u;
 #pragma unroll
         for (int j = 0; j < kLaneBlocks; ++j) {
-            kf[j][0] = nvfp4dev::e4m3x2_f16(ks[j]);
-            kf[j][1] = e4m3_high_f16(ks[j]);
+            kf[j][0] = nvfp4dev::e4m3x2_f16(__builtin_amdgcn_perm(ks[j][1], ks[j][0], pick));
+            kf[j][1] = nvfp4dev::e4m3x2_f16(__builtin_amdgcn_perm(ks[j][3], ks[j][2], pick));
         }
+        f32x4 sc[R][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
 #pragma unroll
@@ -464,18 +546,31 @@ struct Stream {
             for (int j = 0; j < kK; ++j) {
                 const _Float16 sv = kf[j / 2][t / 2][t % 2];
                 const f16x2 ss = {sv, sv};
-                const f16x8 k = decode8(kw[t][j], ss, ss, ss, ss);
+                const f16x8 x = decode8(k[t][j], ss, ss, ss, ss);
 #pragma unroll
-                for (int r = 0; r < R; ++r) sc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][j], sc[r][t], 0, 0, 0);
+                for (int r = 0; r < R; ++r) sc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, q[r][j], sc[r][t], 0, 0, 0);
             }
         }
-        if (next >= 0) load_k(a, kvh, next, e_next);
 
+        // V's scales: lane r16 of run h takes block r16, 16 tokens; which of them are NaN
+        u32x4 vsw[1];
+        lds_read16<1>(stage + kCodes + kScales + (r16 < NB ? r16 : NB - 1) * 64 + h * 16, 0, vsw);
+        uint32_t bad = 0;
+        if (!whole) {
+            __asm__ volatile("" : "+v"(bad));           // keeps this a branch: most steps skip it
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t nan = ((vsw[0][i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                // one bit a byte, to bits 4 i .. 4 i + 3
+                bad |= ((nan >> 7) * 0x10204080u >> 28) << (4 * i);
+                vsw[0][i] &= ~((nan >> 7) * 0xFFu);
+            }
+        }
         f16x2 vs[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            vs[2 * t] = nvfp4dev::e4m3x2_f16(turned[t]);
-            vs[2 * t + 1] = e4m3_high_f16(turned[t]);
+            vs[2 * t] = nvfp4dev::e4m3x2_f16(vsw[0][t]);
+            vs[2 * t + 1] = e4m3_high_f16(vsw[0][t]);
         }
 
         f16x8 p[R][2];
@@ -486,19 +581,19 @@ struct Stream {
 #pragma unroll
         for (int r = 0; r < R; ++r) weigh(r, sc[r], p[r]);
 
-        blocks(std::make_integer_sequence<int, NB>{}, stage, vs, p);
+        blocks(std::make_integer_sequence<int, NB / 4>{}, stage, vs, p);
         if (!whole && __any(bad != 0)) poison(std::make_integer_sequence<int, NB>{}, a, tok0, bad);
-        wave_fence();
     }
 
-    // Query rows row0 .. of sequence s, and their positions.
-    __device__ __forceinline__ void fetch_queries(const AttnArgs &a, const Sequence &s, int kvh, int row0, u32x4 (&raw)[R][kK]) {
+    // The query rows of sequence s, and their positions.
+    __device__ __forceinline__ void fetch_queries(const AttnArgs &a, const Sequence &s, int kvh, u32x4 (&raw)[R][kK]) {
         const auto [lane, r16, h] = this_lane();
         const int rows = s.computed * a.group;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int row = row0 + 16 * r + static_cast<int>(r16);
-            const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
+            const int row = 16 * r + static_cast<int>(r16);
+            const int i = static_cast<int>((static_cast<uint32_t>(row) * a.group_inverse) >> 26);
+            const int head = kvh * a.group + (row - i * a.group);
             pos[r] = -1;
 #pragma unroll
             for (int j = 0; j < kK; ++j) raw[r][j] = u32x4{0, 0, 0, 0};
@@ -518,54 +613,41 @@ struct Stream {
     // As B operands.
     __device__ __forceinline__ void take_queries(const AttnArgs &a, int kvh, const u32x4 (&raw)[R][kK]) {
         const float g = a.scale * (a.c.k_global != nullptr ? a.c.k_global[kvh] : 1.0f);
-        const bool bf16 = a.bf16 != 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            float x[kK][8];
-            uint32_t top = 0;
+            float down = 1.0f;
+            if (a.bf16 != 0) {
+                // a power of two that brings the row's largest element to [2^14, 2^15)
+                uint32_t top = top16(raw[r]), t = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, kWave));
+                top = t > top ? t : top;
+                t = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave));
+                float up;
+                row_power((t > top ? t : top) << 16, &up, &down);
+                up = g < 0.0f ? -up : up;
 #pragma unroll
-            for (int j = 0; j < kK; ++j) {
-                widen(raw[r][j], bf16, x[j]);
+                for (int j = 0; j < kK; ++j) q[r][j] = scale_bf16(raw[r][j], up);
+            } else {
+                const uint32_t sign = g < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t b = __float_as_uint(x[j][k]) & 0x7FFFFFFFu;
-                    top = b > top ? b : top;
-                }
+                for (int j = 0; j < kK; ++j) q[r][j] = __builtin_bit_cast(f16x8, raw[r][j] ^ sign);
             }
-            // a power of two that brings the row's largest element to [2^14, 2^15), bf16 only
-            float up = 1.0f, down = 1.0f;
-            if (bf16) {
-                const uint32_t t16 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, kWave));
-                top = t16 > top ? t16 : top;
-                const uint32_t t32 = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave));
-                row_power(t32 > top ? t32 : top, &up, &down);
-            }
-            const float sign = g < 0.0f ? -up : up;
             c[r] = __builtin_fabsf(g) * kLog2e * down;
             c[r] = c[r] == 0.0f ? 0x1p-126f : c[r];      // hidden scores stay minus infinity, others about 0
-#pragma unroll
-            for (int j = 0; j < kK; ++j)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) q[r][j][k] = static_cast<_Float16>(x[j][k] * sign);
         }
     }
 
-    // Steps i0 .. i1 of the sequence's list for query rows row0 .., joined over the
-    // waves and written: to `out`, or where `slot` >= 0 as a partial result.
+    // Steps i0 .. i1 of the sequence's list, joined over the waves and written: to `out`,
+    // or where `slot` >= 0 as a partial result.
     __device__ __forceinline__ void run(const AttnArgs &a, Buffers &buf, const Sequence &s, const Steps &w, int b, int kvh,
-                                        int row0, int i0, int i1, int64_t slot) {
+                                        int i0, int i1, int64_t slot) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         const int32_t *row = a.table + static_cast<int64_t>(b) * a.table_stride;
-        uint8_t *stage = buf.v[wave];
         int i = i0 + wave;
         const int at0 = i < i1 ? w.at(i) : -1;
         const int e0 = at0 >= 0 ? entry(a, row, s.len, at0) : -1;
         u32x4 raw[R][kK];
-        fetch_queries(a, s, kvh, row0, raw);
-        if (at0 >= 0) {
-            load_v(a, kvh, at0, e0);
-            load_k(a, kvh, at0, e0);
-        }
+        fetch_queries(a, s, kvh, raw);
+        if (at0 >= 0) load(a, kvh, at0, e0, buf.v[wave][0]);
         take_queries(a, kvh, raw);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -578,10 +660,17 @@ struct Stream {
             int at = at0, e = e0;
             int next = i + kAttnWaves < i1 ? w.at(i + kAttnWaves) : -1;
             int e_next = next >= 0 ? entry(a, row, s.len, next) : -1;
-            for (;;) {
+            for (uint32_t turn = 0;; turn ^= 1) {
+                wait_loads();
+                uint32_t k[4][kK];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < kK; ++j) k[t][j] = kw[t][j];
+                if (next >= 0) load(a, kvh, next, e_next, buf.v[wave][turn ^ 1]);
                 const int after = i + 2 * kAttnWaves < i1 ? w.at(i + 2 * kAttnWaves) : -1;
                 const int e_after = after >= 0 ? entry(a, row, s.len, after) : -1;
-                step(a, w, kvh, at, e, next, e_next, stage);
+                step(a, w, at, e, k, lds_address(buf.v[wave][turn]));
                 if (next < 0) break;
                 i += kAttnWaves;
                 at = next;
@@ -590,13 +679,13 @@ struct Stream {
                 e_next = e_after;
             }
         }
-        join(a, buf, s, kvh, row0, slot);
+        join(a, buf, s, kvh, slot);
     }
 
-    __device__ __forceinline__ void join(const AttnArgs &a, Buffers &buf, const Sequence &s, int kvh, int row0,
-                                         int64_t slot) {
+    __device__ __forceinline__ void join(const AttnArgs &a, Buffers &buf, const Sequence &s, int kvh, int64_t slot) {
         const auto [lane, r16, h] = this_lane();
-        const int left = s.computed * a.group - row0, rows = left < kRows ? left : kRows;
+        const int rows = s.computed * a.group;         // at most kRows, as the plan has it
+        __syncthreads();                               // the waves are done with their stages
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float sum = rows_sum(l[r]);
@@ -605,7 +694,7 @@ struct Stream {
                 buf.l[wave][16 * r + r16] = sum;
             }
         }
-        __syncthreads();                               // the waves are done with V's codes, too
+        __syncthreads();
         const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
         const bool bf16 = a.bf16 != 0;
 #pragma unroll
@@ -644,7 +733,8 @@ struct Stream {
                             a.ml[(slot * kRows + row) * 2 + 1] = total;
                         }
                     } else if (16 * b0 + col < a.c.head_dim) {
-                        const int i = (row0 + row) / a.group, head = kvh * a.group + (row0 + row - i * a.group);
+                        const int i = static_cast<int>((static_cast<uint32_t>(row) * a.group_inverse) >> 26);
+                        const int head = kvh * a.group + (row - i * a.group);
                         store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 16 * b0 + col,
                                total == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / total) * g, bf16, a.o_wide);
                     }
@@ -722,9 +812,9 @@ __global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * N
     __shared__ typename S::Buffers buf;
     const int b = blockIdx.x / a.c.kv_heads, kvh = blockIdx.x - b * a.c.kv_heads;
     const Sequence s = sequence_of(a, b);
-    const Steps w = steps_for<6>(a, s, 0, S::kRows);
+    const Steps w = steps_for<6>(a, s);
     S job;
-    job.run(a, buf, s, w, b, kvh, 0, 0, w.count, -1);
+    job.run(a, buf, s, w, b, kvh, 0, w.count, -1);
 }
 
 // Steps of a piece: the steps of all sequences and kv heads over the pieces wanted, a
@@ -736,6 +826,55 @@ __device__ __forceinline__ int piece_steps(int64_t total, int pieces) {
     return each < kAttnWaves ? kAttnWaves : each < (1 << 26) ? static_cast<int>(each) : 1 << 26;
 }
 
+// By one wave.  The first workgroup's also leaves the pieces before each sequence for
+// attn_join.
+__device__ __forceinline__ Piece find_piece(const AttnArgs &a) {
+    const int lane = threadIdx.x & (kWave - 1);
+    // the first 64 sequences stay in registers, one a lane
+    Sequence own = {};
+    int steps = 0;
+    if (lane < a.batch) {
+        own = sequence_of(a, lane);
+        steps = steps_for<6>(a, own).count;
+    }
+    const auto count = [&](int b) { return steps_for<6>(a, sequence_of(a, b)).count; };
+    int64_t total = wave_total(steps);
+    for (int b = kWave + lane; b - lane < a.batch; b += kWave) total += wave_total(b < a.batch ? count(b) : 0);
+    const int each = piece_steps(total * a.c.kv_heads, a.groups);
+
+    Piece p = {-1, 0, 0, 0, {}};
+    int64_t before = 0;                                // pieces of one kv head of the sequences before
+    for (int b0 = 0; b0 < a.batch; b0 += kWave) {
+        const int n = b0 == 0 ? steps : b0 + lane < a.batch ? count(b0 + lane) : 0;
+        const uint32_t mine = static_cast<uint32_t>(n + each - 1) / static_cast<uint32_t>(each);   // n < 2^25
+        const uint32_t upto = wave_upto(mine);
+        const int64_t end = (before + upto) * a.c.kv_heads;
+        if (blockIdx.x == 0 && b0 + lane < a.batch) a.prefix[b0 + lane] = before + upto - mine;
+        const uint64_t past = __ballot(end > static_cast<int64_t>(blockIdx.x));
+        if (past != 0 && p.b < 0) {
+            const int k = __builtin_ctzll(past);
+            p.b = b0 + k;
+            p.pieces = __builtin_amdgcn_readlane(static_cast<int>(mine), k);
+            const int64_t start = (before + static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto - mine), k))) * a.c.kv_heads;
+            const uint32_t at = static_cast<uint32_t>(static_cast<int64_t>(blockIdx.x) - start);
+            p.kvh = static_cast<int>(at / static_cast<uint32_t>(p.pieces));
+            p.part = static_cast<int>(at) - p.kvh * p.pieces;
+            if (blockIdx.x != 0) break;                // the first workgroup goes on with the prefix
+        }
+        before += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto), kWave - 1));
+    }
+    if (blockIdx.x == 0 && lane == 0) a.prefix[a.batch] = before;
+    if (p.b >= kWave) {
+        p.s = sequence_of(a, p.b);
+    } else if (p.b >= 0) {
+        p.s.len = __builtin_amdgcn_readlane(own.len, p.b);
+        p.s.first = __builtin_amdgcn_readlane(own.first, p.b);
+        p.s.n = __builtin_amdgcn_readlane(own.n, p.b);
+        p.s.computed = __builtin_amdgcn_readlane(own.computed, p.b);
+    }
+    return p;
+}
+
 // Every sequence and kv head in pieces of nearly equal length, one a workgroup: more
 // pieces than fit the chip at once, so that one's beginning and end run beside
 // others' loads.  A sequence in one piece is finished by it, those in several leave
@@ -744,148 +883,126 @@ template <int NB, int R>
 __global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * NB, 16 * R)) void attn_pieces(const AttnArgs a) {
     using S = Stream<NB, R>;
     __shared__ typename S::Buffers buf;
-    const int lane = threadIdx.x & (kWave - 1);
-    // the first 64 sequences stay in registers, one a lane
-    Sequence own = {};
-    int steps = 0;
-    if (lane < a.batch) {
-        own = sequence_of(a, lane);
-        steps = steps_for<6>(a, own, 0, S::kRows).count;
+    if (threadIdx.x < kWave) {                         // one wave finds it for all
+        const Piece p = find_piece(a);
+        if (threadIdx.x == 0) buf.piece = p;
     }
-    const auto count = [&](int b) { return steps_for<6>(a, sequence_of(a, b), 0, S::kRows).count; };
-    int64_t total = wave_total(steps);
-    for (int b = kWave + lane; b - lane < a.batch; b += kWave) total += wave_total(b < a.batch ? count(b) : 0);
-    const int each = piece_steps(total * a.c.kv_heads, a.groups);
-
-    int64_t before = 0;                                // pieces of one kv head of the sequences before
-    int found = -1, part = 0, kvh = 0, pieces = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kWave) {
-        const int n = b0 == 0 ? steps : b0 + lane < a.batch ? count(b0 + lane) : 0;
-        const uint32_t mine = static_cast<uint32_t>(n + each - 1) / static_cast<uint32_t>(each);   // n < 2^25
-        const uint32_t upto = wave_upto(mine);
-        const int64_t end = (before + upto) * a.c.kv_heads;
-        if (blockIdx.x == 0 && threadIdx.x < kWave && b0 + lane < a.batch) a.prefix[b0 + lane] = before + upto - mine;
-        const uint64_t past = __ballot(end > static_cast<int64_t>(blockIdx.x));
-        if (past != 0 && found < 0) {
-            const int k = __builtin_ctzll(past);
-            found = b0 + k;
-            pieces = __builtin_amdgcn_readlane(static_cast<int>(mine), k);
-            const int64_t start = (before + static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto - mine), k))) * a.c.kv_heads;
-            const uint32_t at = static_cast<uint32_t>(static_cast<int64_t>(blockIdx.x) - start);
-            kvh = static_cast<int>(at / static_cast<uint32_t>(pieces));
-            part = static_cast<int>(at) - kvh * pieces;
-            if (blockIdx.x != 0) break;                // the first workgroup goes on with the prefix
-        }
-        before += static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(upto), kWave - 1));
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.batch] = before;
-    if (found < 0) return;
-    Sequence s;
-    if (found < kWave) {
-        s.len = __builtin_amdgcn_readlane(own.len, found);
-        s.first = __builtin_amdgcn_readlane(own.first, found);
-        s.n = __builtin_amdgcn_readlane(own.n, found);
-        s.computed = __builtin_amdgcn_readlane(own.computed, found);
-    } else {
-        s = sequence_of(a, found);
-    }
-    const Steps w = steps_for<6>(a, s, 0, S::kRows);
+    __syncthreads();
+    const Piece piece = buf.piece;
+    __syncthreads();                                   // before the stages take its place
+    const int b = __builtin_amdgcn_readfirstlane(piece.b);
+    if (b < 0) return;
+    const Sequence s = {__builtin_amdgcn_readfirstlane(piece.s.len), __builtin_amdgcn_readfirstlane(piece.s.first),
+                        __builtin_amdgcn_readfirstlane(piece.s.n), __builtin_amdgcn_readfirstlane(piece.s.computed)};
+    const int kvh = __builtin_amdgcn_readfirstlane(piece.kvh), part = __builtin_amdgcn_readfirstlane(piece.part),
+              pieces = __builtin_amdgcn_readfirstlane(piece.pieces);
+    const Steps w = steps_for<6>(a, s);
     // pieces of a sequence differ by a step at most
     const int base = w.count / pieces, longer = w.count - base * pieces;
     const int i0 = part * base + (part < longer ? part : longer), i1 = i0 + base + (part < longer ? 1 : 0);
     S job;
-    job.run(a, buf, s, w, found, kvh, 0, i0, i1, pieces == 1 ? -1 : static_cast<int64_t>(blockIdx.x));
+    job.run(a, buf, s, w, b, kvh, i0, i1, pieces == 1 ? -1 : static_cast<int64_t>(blockIdx.x));
 }
 
 // Weighted sum of `n` partial results (sums from `part` on, `stride` floats apart, and
-// maximum and sum at `ml`, `ml_stride` apart) of one row, by a workgroup: four
-// elements a thread, slices of the partial results.  Every thread of slice 0 gets the
-// sums and the weights' total.  All loads of a round are on their way together.
-template <int NB>
+// maximum and sum at `ml`, `ml_stride` apart) of one row: WAVES waves take the results in
+// turn, a lane NB / 4 outputs.  The loads of up to 8 results a wave, and of the maxima,
+// are on their way together (past the last result they read it again, with no weight).
+template <int NB, int WAVES>
 struct Joiner {
-    static constexpr int kDp = 16 * NB, kWide = kDp / 4, kSlices = kAttnThreads / kWide;
-    static constexpr int kAhead = 8;
+    static constexpr int kDp = 16 * NB, kEach = NB / 4;
+    typedef float Vec __attribute__((ext_vector_type(kEach)));
     struct Buffers {
-        f32x4 sums[kSlices][kWide];
-        float weight[kAttnThreads];
-        float best[kAttnWaves], total[kAttnWaves];
+        Vec sums[WAVES][kWave];
+        float total[WAVES];
     };
-    f32x4 v;
-    float total;
 
-    __device__ __forceinline__ void run(Buffers &buf, const float *part, int64_t stride, const float *ml, int64_t ml_stride,
-                                        int n) {
-        const int slice = threadIdx.x / kWide, col = threadIdx.x % kWide;
-        const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-        v = f32x4{0, 0, 0, 0};
-        total = 0.0f;
-        float best = -__builtin_inff();                // of the rounds before
-        for (int k0 = 0; k0 < n; k0 += kAttnThreads) {
-            const int here = n - k0 < kAttnThreads ? n - k0 : kAttnThreads;
-            f32x4 ahead[kAhead];
-            const auto fetch = [&](int base) {
+    template <int AHEAD>
+    static __device__ __forceinline__ void sum(const float *part, int64_t stride, const float *ml, int64_t ml_stride, int n,
+                                               int wave, Vec &v, float &total) {
+        const int lane = threadIdx.x & (kWave - 1);
+        Vec ahead[AHEAD];
+        f32x2 ahead_ml[AHEAD];
+        const auto fetch = [&](int base) {
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const int k = base + slice + i * kSlices;
-                    ahead[i] = f32x4{0, 0, 0, 0};
-                    if (slice < kSlices && k < here)
-                        ahead[i] = *reinterpret_cast<const f32x4 *>(part + (k0 + k) * stride + 4 * col);
+            for (int i = 0; i < AHEAD; ++i) {
+                const int k = base + wave + i * WAVES, at = k < n ? k : n - 1;
+                const float *p = part + at * stride + kEach * lane;
+                if constexpr (kEach == 3) {
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) ahead[i][j] = p[j];
+                } else {
+                    ahead[i] = *reinterpret_cast<const Vec *>(p);
                 }
-            };
-            fetch(0);
-            const int mine = threadIdx.x;
-            float m = -__builtin_inff(), l = 0.0f;
-            if (mine < here) {
-                m = ml[(k0 + mine) * ml_stride];
-                l = ml[(k0 + mine) * ml_stride + 1];
+                ahead_ml[i] = *reinterpret_cast<const f32x2 *>(ml + at * ml_stride);
             }
-            float top = m;
+        };
+        fetch(0);
+        float top = -__builtin_inff();
+        for (int k = lane; k < n; k += kWave) top = __builtin_fmaxf(top, ml[k * ml_stride]);
 #pragma unroll
-            for (int o = 1; o < kWave; o <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, kWave));
-            if (lane == 0) buf.best[wave] = top;
-            __syncthreads();
-            top = best;
+        for (int o = 1; o < kWave; o <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, kWave));
+        for (int base = 0;;) {
 #pragma unroll
-            for (int k = 0; k < kAttnWaves; ++k) top = __builtin_fmaxf(top, buf.best[k]);
-            const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-            buf.weight[mine] = f;
-            const float sum = nvfp4dev::wave_sum(mine < here ? l * f : 0.0f);
-            if (lane == 0) buf.total[wave] = sum;
-            const float old = best == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(best - top);
-            best = top;
-            __syncthreads();
-            v *= old;
-            total *= old;
-#pragma unroll
-            for (int k = 0; k < kAttnWaves; ++k) total += buf.total[k];
-            for (int base = 0;;) {
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const int k = base + slice + i * kSlices;
-                    if (slice < kSlices && k < here) v += ahead[i] * buf.weight[k];
-                }
-                base += kAhead * kSlices;
-                if (base >= here) break;
-                fetch(base);
+            for (int i = 0; i < AHEAD; ++i) {
+                const float m = ahead_ml[i][0];
+                const bool none = base + wave + i * WAVES >= n;
+                const float f = none || m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+                v += none ? Vec{} : ahead[i] * f;
+                total += none ? 0.0f : ahead_ml[i][1] * f;
             }
-            __syncthreads();
-        }
-        if (slice < kSlices) buf.sums[slice][col] = v;
-        __syncthreads();
-        if (slice == 0) {
-#pragma unroll
-            for (int k = 1; k < kSlices; ++k) v += buf.sums[k][col];
+            base += AHEAD * WAVES;
+            if (base >= n) break;
+            fetch(base);
         }
     }
 
-    // The row's four elements of a thread of slice 0.
-    __device__ __forceinline__ void store(const AttnArgs &a, const Sequence &s, int kvh, int row) const {
-        const int slice = threadIdx.x / kWide, col = threadIdx.x % kWide;
-        if (slice > 0 || 4 * col >= a.c.head_dim) return;
+    // The row's outputs of this lane; true in the first of the waves, `wave` 0, only.
+    static __device__ __forceinline__ bool run(Buffers &buf, const float *part, int64_t stride, const float *ml,
+                                               int64_t ml_stride, int n, int wave, Vec *out, float *total) {
+        const int lane = threadIdx.x & (kWave - 1);
+        Vec v = {};
+        float sum = 0.0f;
+        if (n > 2 * WAVES) {
+            Joiner::template sum<8>(part, stride, ml, ml_stride, n, wave, v, sum);
+        } else if (n > WAVES) {
+            Joiner::template sum<2>(part, stride, ml, ml_stride, n, wave, v, sum);
+        } else if (n > 0) {
+            Joiner::template sum<1>(part, stride, ml, ml_stride, n, wave, v, sum);
+        }
+        if constexpr (WAVES > 1) {
+            if (wave > 0) {
+                buf.sums[wave][lane] = v;
+                if (lane == 0) buf.total[wave] = sum;
+            }
+            __syncthreads();
+            if (wave > 0) return false;
+#pragma unroll
+            for (int k = 1; k < WAVES; ++k) {
+                v += buf.sums[k][lane];
+                sum += buf.total[k];
+            }
+        }
+        *out = v;
+        *total = sum;
+        return true;
+    }
+
+    static __device__ __forceinline__ void store(const AttnArgs &a, const Sequence &s, int kvh, int row, Vec v, float total) {
+        const int lane = threadIdx.x & (kWave - 1), e = kEach * lane;
         const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
         const float g = a.c.v_global != nullptr ? a.c.v_global[kvh] : 1.0f;
-        store4(a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + 4 * col,
-               total == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / total) * g, a.bf16 != 0, a.o_wide);
+        uint16_t *out = a.out + static_cast<int64_t>(s.first + i) * a.o_token + head * a.o_head + e;
+        v = total == 0.0f ? Vec{} : v * (1.0f / total) * g;
+        // rows that may be written 16 bytes at a time may be written 4
+        if (kEach == 2 && a.o_wide) {
+            if (e < a.c.head_dim)
+                *reinterpret_cast<uint32_t *>(out) = to16(v[0], a.bf16 != 0) | to16(v[kEach - 1], a.bf16 != 0) << 16;
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            if (e + j < a.c.head_dim) out[j] = static_cast<uint16_t>(to16(v[j], a.bf16 != 0));
     }
 };
 
@@ -893,8 +1010,9 @@ struct Joiner {
 // results of its pieces joined, or zeros where there are none.
 template <int NB>
 __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int rows, int used) {
-    using J = Joiner<NB>;
+    using J = Joiner<NB, kAttnWaves>;
     __shared__ typename J::Buffers buf;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int item = blockIdx.x / used, row = blockIdx.x - item * used;
     const int b = item / a.c.kv_heads, kvh = item - b * a.c.kv_heads;
     const int64_t before = a.prefix[b];
@@ -903,10 +1021,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int 
     const Sequence s = sequence_of(a, b);
     if (row >= s.computed * a.group) return;
     const int64_t first = before * a.c.kv_heads + static_cast<int64_t>(kvh) * pieces;
-    J job;
-    job.run(buf, a.part + (first * rows + row) * J::kDp, static_cast<int64_t>(rows) * J::kDp,
-            a.ml + (first * rows + row) * 2, 2 * rows, pieces);
-    job.store(a, s, kvh, row);
+    typename J::Vec v;
+    float total;
+    if (J::run(buf, a.part + (first * rows + row) * J::kDp, static_cast<int64_t>(rows) * J::kDp,
+               a.ml + (first * rows + row) * 2, 2 * rows, pieces, wave, &v, &total))
+        J::store(a, s, kvh, row, v, total);
 }
 
 // ---------------------------------------------------------------- the tile kernel
@@ -1091,7 +1210,6 @@ struct Tile {
         const Lane n = this_lane();
         const uint32_t h = n.id >> 5;
         const float g = a.scale * (a.c.k_global != nullptr ? a.c.k_global[kvh] : 1.0f);
-        const bool bf16 = a.bf16 != 0;
         const int i = row / a.group, head = kvh * a.group + (row - i * a.group);
         pos = -1;
         u32x4 raw[kSlices];
@@ -1105,30 +1223,21 @@ struct Tile {
             for (int j = 0; j < kSlices; ++j)
                 if (16 * j < a.c.head_dim) raw[j] = load8(p + 16 * j + 8 * h, a.q_wide);
         }
-        uint32_t top = 0;
-        float x[8];
-        float up = 1.0f, down = 1.0f;
-        if (bf16) {
+        float down = 1.0f;
+        if (a.bf16 != 0) {
+            const uint32_t top = top16(raw), other = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave));
+            float up;
+            row_power((other > top ? other : top) << 16, &up, &down);
+            up = g < 0.0f ? -up : up;
 #pragma unroll
-            for (int j = 0; j < kSlices; ++j)
+            for (int j = 0; j < kSlices; ++j) q[j] = scale_bf16(raw[j], up);
+        } else {
+            const uint32_t sign = g < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t lo = raw[j][k] << 16 & 0x7FFFFFFFu, hi = raw[j][k] & 0x7FFF0000u;
-                    top = lo > top ? lo : top;
-                    top = hi > top ? hi : top;
-                }
-            const uint32_t other = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave));
-            row_power(other > top ? other : top, &up, &down);
+            for (int j = 0; j < kSlices; ++j) q[j] = __builtin_bit_cast(f16x8, raw[j] ^ sign);
         }
-        const float sign = g < 0.0f ? -up : up;
         c = __builtin_fabsf(g) * kLog2e * down;
         c = c == 0.0f ? 0x1p-126f : c;                 // as in the stream kernel
-#pragma unroll
-        for (int j = 0; j < kSlices; ++j) {
-            widen(raw[j], bf16, x);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) q[j][k] = static_cast<_Float16>(x[k] * sign);
-        }
     }
 
     // Step s from buffer `from`; `there`: bit r where run r's page is.
@@ -1349,24 +1458,25 @@ __global__ __launch_bounds__(WAVES * kWave, 2) void attn_tiles(const AttnArgs a,
             splits > 1 ? a.part + static_cast<int64_t>(blockIdx.x) * tile_part(T::kRows, T::kDp) : nullptr);
 }
 
-// Rows of a tile whose steps were shared, kJoinRows a workgroup one after the other:
-// their partial results joined.
+// Rows of a tile whose steps were shared, kJoinRows a workgroup, each by a wave: their
+// partial results joined.
 constexpr int kJoinRows = 8;
 template <int NB>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_tiles(const AttnArgs a, int tiles, int splits, int rows) {
-    using J = Joiner<NB>;
-    __shared__ typename J::Buffers buf;
+    using J = Joiner<NB, 1>;
+    typename J::Buffers *none = nullptr;               // one wave a row exchanges nothing
     const int chunks = rows / kJoinRows, item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
     const TileJob j = tile_job(a, item, tiles, rows);
     if (j.b >= a.batch) return;
     const Sequence s = sequence_of(a, j.b);
     const int64_t each = tile_part(rows, J::kDp);
     const float *part = a.part + static_cast<int64_t>(item) * splits * each;
-    for (int row = chunk * kJoinRows; row < (chunk + 1) * kJoinRows && j.row0 + row < s.computed * a.group; ++row) {
-        J job;
-        job.run(buf, part + row * J::kDp, each, part + rows * J::kDp + 2 * row, each, splits);
-        job.store(a, s, j.kvh, j.row0 + row);
-        __syncthreads();
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), end = s.computed * a.group - j.row0;
+    for (int row = chunk * kJoinRows + wave; row < (chunk + 1) * kJoinRows && row < end; row += kAttnWaves) {
+        typename J::Vec v;
+        float total;
+        J::run(*none, part + row * J::kDp, each, part + rows * J::kDp + 2 * row, each, splits, 0, &v, &total);
+        J::store(a, s, j.kvh, j.row0 + row, v, total);
     }
 }
 

@@ -106,7 +106,7 @@ constexpr int64_t kWholeSteps = 8;
 // registers are kept to (512 a lane of a SIMD; no variant needs accumulation
 // registers, which the loads in flight must not end up in).
 constexpr int groups_per_unit(int64_t dp, int64_t rows) {
-    return rows <= 16 ? (dp <= 64 ? 4 : dp <= 128 ? 3 : 2) : 2;
+    return rows <= 16 ? (dp <= 64 ? 5 : dp <= 128 ? 4 : 2) : dp <= 64 ? 3 : 2;
 }
 
 // Rows of a workgroup of the tile kernel, 32 a wave: 8 waves decode a step of the cache
@@ -140,7 +140,7 @@ inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int
         p.groups = batch * kv_heads;
         if (p.kind == kShared) {
             // every sequence and kv head ends with a piece that may be short
-            p.pieces = 2 * groups_per_unit(dp, p.rows) * kComputeUnits;
+            p.pieces = groups_per_unit(dp, p.rows) * kComputeUnits;
             p.groups += p.pieces;
             p.part_bytes = static_cast<size_t>(p.groups * p.rows * dp) * 4;
             p.ml_bytes = static_cast<size_t>(p.groups * p.rows * 2) * 4;

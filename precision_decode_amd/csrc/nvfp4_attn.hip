@@ -201,6 +201,8 @@ int attention(const AttnCall &c, const AttnPlan &p, uint8_t *ws, hipStream_t str
     a.group = static_cast<int32_t>(c.heads / c.cache->kv_heads);
     a.tokens = static_cast<int32_t>(c.tokens);
     a.max_query = static_cast<int32_t>(c.max_query);
+    a.each = static_cast<int32_t>(c.tokens / c.batch);
+    a.group_inverse = static_cast<uint32_t>(ceil_div(int64_t(1) << 26, a.group));
     a.window = c.window < context ? static_cast<int32_t>(c.window) : 0;   // a window over everything is none
     a.sinks = static_cast<int32_t>(c.sinks < context ? c.sinks : context);
     a.bf16 = c.x_type == NVFP4_OUT_BF16;
