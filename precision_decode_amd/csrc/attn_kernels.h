@@ -36,6 +36,7 @@ constexpr int kStep = 64;                  // cache tokens of a step: four runs 
 constexpr int kRun = 16;
 constexpr float kWeightShift = 8.0f;       // P is scaled by 2^8
 constexpr float kRescaleAt = 6.0f;         // growth of the maximum (log2) that rescales the sums: P stays below 2^14
+constexpr int kAluCrosses = 0x2 | 0x4 | 0x400;   // a scheduling barrier for all but VALU, SALU and transcendentals
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
@@ -1086,6 +1087,12 @@ struct Tile {
         return token * (kDp / 2) + 16 * (piece ^ f);
     }
 
+    // Bytes of an element's offset that a row's turn by up to TURN chunks of 16 changes.
+    template <int TURN>
+    static __device__ __forceinline__ uint32_t turned_low(uint32_t elements) {
+        return 2 * elements & (16 * TURN);
+    }
+
     // The page of step s that run lane % kRuns lies in, -1 without one.
     __device__ __forceinline__ int entry(const AttnArgs &a, const int32_t *row, int len, int s) const {
         const int token = s * kT + kRun * static_cast<int>(this_lane().id % kRuns);
@@ -1246,17 +1253,39 @@ struct Tile {
         const int tok0 = s * kT;
         const Lane n = this_lane();
         const uint32_t r32 = n.id & 31, h = n.id >> 5;
+        // Operands are read kAhead products before they are needed.  A read's address is
+        // the lane's row, its place turned by the chunk's low bits, and a constant.
+        constexpr int kAhead = NB <= 8 ? 8 : 4, kTurnK = NB == 8 || NB == 16 ? 15 : 7, kTurnV = kT == 64 ? 7 : 3;
+        const uint8_t *k_row = reinterpret_cast<const uint8_t *>(&buf.k[from][k_at(r32, h)]);
+        const uint8_t *v_row = reinterpret_cast<const uint8_t *>(&buf.v[from][v_at(r32, h)]);
+        const uint32_t k_low = turned_low<kTurnK>(k_at(r32, h)), v_low = turned_low<kTurnV>(v_at(r32, h));
+        const auto read_k = [&](int i) {
+            const int u = i / kSlices, chunk = 2 * (i % kSlices);
+            return *reinterpret_cast<const f16x8 *>(k_row + ((k_low ^ (16 * (chunk & kTurnK))) - k_low) +
+                                                    (16 * (chunk & ~kTurnK) + 64 * u * kDp));
+        };
+        const auto read_v = [&](int i) {
+            const int o = i % kOuts, chunk = 2 * (i / kOuts);
+            return *reinterpret_cast<const f16x8 *>(v_row + ((v_low ^ (16 * (chunk & kTurnV))) - v_low) +
+                                                    (16 * (chunk & ~kTurnV) + 64 * o * kT));
+        };
+        f16x8 ahead[kAhead];
         f32x16 sc[kT / 32];
+        constexpr int kProducts = kT / 32 * kSlices;
 #pragma unroll
-        for (int u = 0; u < kT / 32; ++u) {
+        for (int i = 0; i < kAhead; ++i) ahead[i] = read_k(i);
+#pragma unroll
+        for (int u = 0; u < kT / 32; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kSlices; ++j) {
-                const f16x8 k = *reinterpret_cast<const f16x8 *>(&buf.k[from][k_at(32 * u + r32, 2 * j + h)]);
-                sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[j], sc[u], 0, 0, 0);
-            }
+        for (int i = 0; i < kProducts; ++i) {
+            nvfp4dev::phase_fence();
+            sc[i / kSlices] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[i % kAhead], q[i % kSlices], sc[i / kSlices], 0, 0, 0);
+            // the last ones make room for the second product's first operands
+            ahead[i % kAhead] = i + kAhead < kProducts ? read_k(i + kAhead) : read_v(i + kAhead - kProducts);
         }
+        nvfp4dev::phase_fence();
         const uint64_t all = (uint64_t(1) << kRuns) - 1;
         const bool whole = (there & all) == all && tok0 + kT - 1 <= p_first &&
                            (a.window == 0 || tok0 > p_last - a.window || tok0 + kT - 1 < a.sinks);
@@ -1299,13 +1328,13 @@ struct Tile {
                 p[2 * u + i / 8][i % 8] = static_cast<_Float16>(e);
             }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        constexpr int kSums = kT / 16 * kOuts;
 #pragma unroll
-        for (int k = 0; k < kT / 16; ++k)
-#pragma unroll
-            for (int o = 0; o < kOuts; ++o) {
-                const f16x8 v = *reinterpret_cast<const f16x8 *>(&buf.v[from][v_at(32 * o + r32, 2 * k + h)]);
-                acc[o] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[k], acc[o], 0, 0, 0);
-            }
+        for (int i = 0; i < kSums; ++i) {
+            acc[i % kOuts] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[i % kAhead], p[i / kOuts], acc[i % kOuts], 0, 0, 0);
+            if (i + kAhead < kSums) ahead[i % kAhead] = read_v(i + kAhead);
+            __builtin_amdgcn_sched_barrier(kAluCrosses);
+        }
         uint32_t bad = 0;
 #pragma unroll
         for (int r = 0; r < kRuns; ++r) bad |= buf.bad[from][r];

@@ -157,7 +157,7 @@ inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int
     p.rows = rows > kTileRowsFew && bound(kTileRows) * kv_heads >= kComputeUnits ? kTileRows : kTileRowsFew;
     p.tiles = bound(p.rows);
     const int64_t items = p.tiles * kv_heads, fill = 2 * kComputeUnits * kTileRowsFew / p.rows;
-    if (items < fill && steps > kWholeSteps) {
+    if (items < 64 && steps > kWholeSteps) {
         p.splits = ceil_div(fill, items);
         if (p.splits > ceil_div(steps, kWholeSteps)) p.splits = ceil_div(steps, kWholeSteps);
         if (p.splits > kMaxSplits) p.splits = kMaxSplits;
