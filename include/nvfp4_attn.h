@@ -39,7 +39,7 @@
  * Shape rules: head_dim a multiple of 16 from 16 to 256; page_size a power of two
  * from 16 to 1024; pages >= 1, pages * page_size < 2^31; kv_heads from 1 to 1024;
  * heads a multiple of kv_heads, at most 16384; tokens < 2^24 and
- * tokens * (heads + 2 kv_heads) < 2^31 (tokens = 0 does nothing); strides from 0
+ * tokens * (heads + 2 kv_heads) < 2^27 (tokens = 0 does nothing); strides from 0
  * to 2^40 elements, those of outputs such that rows do not overlap.
  * Alignment: rows to their element, codes and scales to 16 bytes, float arrays to
  * 16 (globals to 4), positions and slots to 8, other integers to 4.  Rows that are
@@ -147,8 +147,8 @@ int nvfp4_qk_norm_rope_launch(const void *Q, int64_t q_token_stride, int64_t q_h
  * power of two of its row to fit fp16, where e2m1 * e4m3 is exact), softmax
  * statistics and sums are fp32, and the weights meet v rounded to fp16 after
  * scaling, 2^-11 relative; results do not depend on other sequences' values.
- * table_width * page_size < 2^31, batch from 1 to 65535, batch * kv_heads < 2^22,
- * batch and strides of block_table non-negative, scale finite.
+ * table_width * page_size < 2^31, batch from 1 to 65535, batch * kv_heads <= 2^18,
+ * tokens * heads < 2^30, strides of block_table not negative, scale finite.
  */
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache_t *cache, int64_t heads, int64_t batch,
                                          int64_t tokens, int64_t max_query, int64_t table_width);

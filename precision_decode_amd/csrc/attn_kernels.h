@@ -179,7 +179,7 @@ __device__ __forceinline__ bool visible(const AttnArgs &a, int p, int j) {
 }
 
 __device__ __forceinline__ void store4(uint16_t *p, f32x4 v, bool bf16, bool wide) {
-    const uint32_t lo = to16(v[0], bf16) | to16(v[1], bf16) << 16, hi = to16(v[2], bf16) | to16(v[3], bf16) << 16;
+    const uint32_t lo = pair16(v[0], v[1], bf16), hi = pair16(v[2], v[3], bf16);
     if (wide) {
         *reinterpret_cast<u32x2 *>(p) = u32x2{lo, hi};
     } else {
@@ -998,7 +998,7 @@ struct Joiner {
         // rows that may be written 16 bytes at a time may be written 4
         if (kEach == 2 && a.o_wide) {
             if (e < a.c.head_dim)
-                *reinterpret_cast<uint32_t *>(out) = to16(v[0], a.bf16 != 0) | to16(v[kEach - 1], a.bf16 != 0) << 16;
+                *reinterpret_cast<uint32_t *>(out) = pair16(v[0], v[kEach - 1], a.bf16 != 0);
             return;
         }
 #pragma unroll
@@ -1029,6 +1029,14 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int 
         J::store(a, s, kvh, row, v, total);
 }
 
+// A barrier that orders the workgroup's LDS accesses and waits for them alone:
+// __syncthreads also waits for the codes on their way from memory.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // ---------------------------------------------------------------- the tile kernel
 //
 // Many query rows: a workgroup holds 32 of them a wave and walks the cache in steps
@@ -1036,9 +1044,13 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int 
 // [token][element], V turned, as [element][token].  Products run on the 32 x 32
 // matrix instructions.  Codes are loaded two steps ahead into registers and decoded
 // one step ahead into the other of two buffers, so that one barrier a step is
-// enough; half of the waves decode before their products and half after them, so
-// that the two waves of a SIMD need the VALU and the matrix cores at different
-// times.
+// enough; one half of the waves decodes before its products and the other after them,
+// so that the two waves of a SIMD need the VALU and the matrix cores at different
+// times (a prompt of 4096 tokens, 32 heads of 128: 210 us in step, 195 us so; waves
+// that took turns at whole phases, with V three deep, took 201 to 220 us).  8 waves of
+// 256 rows decode a step half as often as 4 of 128 (225 us), which are taken where 256
+// would leave compute units idle.  The VALU is busy for 0.54 of the time, the matrix
+// cores for 0.31.
 template <int NB, int WAVES>
 struct Tile {
     static constexpr int kDp = 16 * NB;
@@ -1057,7 +1069,7 @@ struct Tile {
         __attribute__((aligned(16))) _Float16 k[2][kT * kDp];
         __attribute__((aligned(16))) _Float16 v[2][kT * kDp];
         __attribute__((aligned(16))) uint8_t raw[kRuns][kRun * kDp / 2];
-        uint32_t bad[2][kRuns];                    // whether a run of V holds NaN, and which tokens of which block
+        uint32_t bad[2][kRuns];            // whether a run of V holds NaN, and which tokens of which block
         uint16_t nan[2][kRuns][NB];
     };
 
@@ -1069,6 +1081,8 @@ struct Tile {
     f16x8 q[kSlices];
     float c;
     int pos;
+    f32x16 sc[kT / 32];                            // a step's scores, then its weights
+    f16x8 p[kT / 16];
     f32x16 acc[kOuts];
     float m, l;
 
@@ -1077,7 +1091,7 @@ struct Tile {
         return token * kDp + 8 * (chunk ^ f);
     }
     static __device__ __forceinline__ uint32_t v_at(uint32_t element, uint32_t chunk) {   // chunks of 8 tokens
-        const uint32_t f = kT == 64 ? element & 7 : (element >> 2) & 3;
+        const uint32_t f = kT == 64 ? (element >> 1) & 7 : (element >> 2) & 3;
         return element * kT + 8 * (chunk ^ f);
     }
     static __device__ __forceinline__ uint32_t raw_at(uint32_t token, uint32_t piece) {
@@ -1247,54 +1261,52 @@ struct Tile {
         c = c == 0.0f ? 0x1p-126f : c;                 // as in the stream kernel
     }
 
-    // Step s from buffer `from`; `there`: bit r where run r's page is.
-    __device__ __forceinline__ void step(const AttnArgs &a, const Buffers &buf, int from, int s, uint64_t there, int p_first,
-                                         int p_last) {
-        const int tok0 = s * kT;
+    // Operands are read kAhead products before they are needed.  A read's address is the
+    // lane's row, its place turned by the chunk's low bits, and a constant.
+    static constexpr int kAhead = NB <= 8 ? 8 : 4;
+    static constexpr int kTurnK = NB == 8 || NB == 16 ? 15 : 7, kTurnV = kT == 64 ? 7 : 3;
+
+    // Scores of K in buffer `from`.
+    __device__ __forceinline__ void scores(const Buffers &buf, int from) {
         const Lane n = this_lane();
-        const uint32_t r32 = n.id & 31, h = n.id >> 5;
-        // Operands are read kAhead products before they are needed.  A read's address is
-        // the lane's row, its place turned by the chunk's low bits, and a constant.
-        constexpr int kAhead = NB <= 8 ? 8 : 4, kTurnK = NB == 8 || NB == 16 ? 15 : 7, kTurnV = kT == 64 ? 7 : 3;
-        const uint8_t *k_row = reinterpret_cast<const uint8_t *>(&buf.k[from][k_at(r32, h)]);
-        const uint8_t *v_row = reinterpret_cast<const uint8_t *>(&buf.v[from][v_at(r32, h)]);
-        const uint32_t k_low = turned_low<kTurnK>(k_at(r32, h)), v_low = turned_low<kTurnV>(v_at(r32, h));
-        const auto read_k = [&](int i) {
-            const int u = i / kSlices, chunk = 2 * (i % kSlices);
-            return *reinterpret_cast<const f16x8 *>(k_row + ((k_low ^ (16 * (chunk & kTurnK))) - k_low) +
+        const uint32_t at = k_at(n.id & 31, n.id >> 5), low = turned_low<kTurnK>(at);
+        const uint8_t *row = reinterpret_cast<const uint8_t *>(&buf.k[from][at]);
+        constexpr int kU = kT / 32;
+        const auto read = [&](int i) {             // product i: tokens 32 (i mod kU) .., elements 16 (i / kU) ..
+            const int u = i % kU, chunk = 2 * (i / kU);
+            return *reinterpret_cast<const f16x8 *>(row + ((low ^ (16 * (chunk & kTurnK))) - low) +
                                                     (16 * (chunk & ~kTurnK) + 64 * u * kDp));
         };
-        const auto read_v = [&](int i) {
-            const int o = i % kOuts, chunk = 2 * (i / kOuts);
-            return *reinterpret_cast<const f16x8 *>(v_row + ((v_low ^ (16 * (chunk & kTurnV))) - v_low) +
-                                                    (16 * (chunk & ~kTurnV) + 64 * o * kT));
-        };
-        f16x8 ahead[kAhead];
-        f32x16 sc[kT / 32];
         constexpr int kProducts = kT / 32 * kSlices;
+        f16x8 ahead[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) ahead[i] = read_k(i);
+        for (int i = 0; i < kAhead; ++i) ahead[i] = read(i);
 #pragma unroll
         for (int u = 0; u < kT / 32; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kProducts; ++i) {
-            nvfp4dev::phase_fence();
-            sc[i / kSlices] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[i % kAhead], q[i % kSlices], sc[i / kSlices], 0, 0, 0);
-            // the last ones make room for the second product's first operands
-            ahead[i % kAhead] = i + kAhead < kProducts ? read_k(i + kAhead) : read_v(i + kAhead - kProducts);
+            __builtin_amdgcn_sched_barrier(kAluCrosses);
+            sc[i % kU] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[i % kAhead], q[i / kU], sc[i % kU], 0, 0, 0);
+            if (i + kAhead < kProducts) ahead[i % kAhead] = read(i + kAhead);
         }
-        nvfp4dev::phase_fence();
+    }
+
+    // Softmax of the scores of step s: the running maximum and sum, the weights.
+    // `there`: bit r where run r's page is.
+    __device__ __forceinline__ void weigh(const AttnArgs &a, int s, uint64_t there, int p_first, int p_last) {
+        const int tok0 = s * kT;
         const uint64_t all = (uint64_t(1) << kRuns) - 1;
         const bool whole = (there & all) == all && tok0 + kT - 1 <= p_first &&
                            (a.window == 0 || tok0 > p_last - a.window || tok0 + kT - 1 < a.sinks);
         if (!whole) {
+            const int h = static_cast<int>(this_lane().id >> 5);
 #pragma unroll
             for (int u = 0; u < kT / 32; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int token = 32 * u + 8 * (i / 4) + 4 * static_cast<int>(h) + i % 4;
+                    const int token = 32 * u + 8 * (i / 4) + 4 * h + i % 4;
                     if (!((there >> (token / kRun)) & 1u) || !visible(a, pos, tok0 + token)) sc[u][i] = -__builtin_inff();
                 }
         }
@@ -1317,7 +1329,6 @@ struct Tile {
                 for (int i = 0; i < 16; ++i) acc[o][i] *= f;
         }
         const float shift = kWeightShift - (m == -__builtin_inff() ? 0.0f : m);
-        f16x8 p[kT / 16];
         float sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int u = 0; u < kT / 32; ++u)
@@ -1328,17 +1339,33 @@ struct Tile {
                 p[2 * u + i / 8][i % 8] = static_cast<_Float16>(e);
             }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
+
+    // The weights of step s times V in buffer `from`.
+    __device__ __forceinline__ void sums(const AttnArgs &a, const Buffers &buf, int from, int s, uint64_t there) {
+        const Lane n = this_lane();
+        const uint32_t at = v_at(n.id & 31, n.id >> 5), low = turned_low<kTurnV>(at);
+        const uint8_t *row = reinterpret_cast<const uint8_t *>(&buf.v[from][at]);
+        const auto read = [&](int i) {
+            const int o = i % kOuts, chunk = 2 * (i / kOuts);
+            return *reinterpret_cast<const f16x8 *>(row + ((low ^ (16 * (chunk & kTurnV))) - low) +
+                                                    (16 * (chunk & ~kTurnV) + 64 * o * kT));
+        };
         constexpr int kSums = kT / 16 * kOuts;
+        f16x8 ahead[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < kSums) ahead[i] = read(i);
 #pragma unroll
         for (int i = 0; i < kSums; ++i) {
             acc[i % kOuts] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ahead[i % kAhead], p[i / kOuts], acc[i % kOuts], 0, 0, 0);
-            if (i + kAhead < kSums) ahead[i % kAhead] = read_v(i + kAhead);
+            if (i + kAhead < kSums) ahead[i % kAhead] = read(i + kAhead);
             __builtin_amdgcn_sched_barrier(kAluCrosses);
         }
         uint32_t bad = 0;
 #pragma unroll
         for (int r = 0; r < kRuns; ++r) bad |= buf.bad[from][r];
-        if (__builtin_amdgcn_readfirstlane(static_cast<int>(bad)) != 0) poison(a, buf, from, tok0, there);
+        if (__builtin_amdgcn_readfirstlane(static_cast<int>(bad)) != 0) poison(a, buf, from, s * kT, there);
     }
 
     // Rows that see a token whose block of V is NaN: NaN there.
@@ -1393,22 +1420,25 @@ struct Tile {
                 load(a, kvh, w.at(i0 + 1), e);
             }
             int e_after = i0 + 2 < i1 ? entry(a, table, s.len, w.at(i0 + 2)) : -1;
-            __syncthreads();
+            lds_barrier();
             for (int i = i0; i < i1; ++i) {
                 const int from = (i - i0) & 1;
-                const bool early = wave >= WAVES / 2;
                 const auto ahead = [&]() {
                     if (i + 1 < i1) decode(buf, from ^ 1);
                     if (i + 2 < i1) load(a, kvh, w.at(i + 2), e_after);
                 };
+                const bool early = wave >= WAVES / 2;
                 if (early) ahead();
-                const int tok0 = w.at(i) * kT;
-                if (tok0 <= p_last) step(a, buf, from, w.at(i), there, p_first, p_last);
+                if (w.at(i) * kT <= p_last) {
+                    scores(buf, from);
+                    weigh(a, w.at(i), there, p_first, p_last);
+                    sums(a, buf, from, w.at(i), there);
+                }
                 if (!early) ahead();
                 there = there_next;
                 there_next = __ballot(e_after >= 0);
                 if (i + 3 < i1) e_after = entry(a, table, s.len, w.at(i + 3));
-                __syncthreads();
+                lds_barrier();
             }
         }
         // this lane's row: elements 32 o + 8 j + 4 h ..

@@ -44,6 +44,11 @@ inline int check_cache_shape(const nvfp4_kv_cache_t &c) {
     return NVFP4_GEMV_OK;
 }
 
+// Rows of a call that moves them, 32 threads each at most: below 2^32 threads.
+inline bool rows_ok(int64_t tokens, int64_t per_token) {
+    return tokens >= 0 && tokens <= kMaxTokens && tokens * per_token < (int64_t(1) << 27);
+}
+
 // Bytes of each code and scale buffer of a cache whose shape has been checked
 // (below 2^31 * 2^10 * 2^7).
 inline int64_t code_bytes(const nvfp4_kv_cache_t &c) {
@@ -112,7 +117,7 @@ constexpr int groups_per_unit(int64_t dp, int64_t rows) {
 // Rows of a workgroup of the tile kernel, 32 a wave: 8 waves decode a step of the cache
 // half as often as 4, which fill the chip with half as many rows.
 constexpr int64_t kTileRows = 256, kTileRowsFew = 128;
-constexpr int64_t kMaxSplits = 64;
+constexpr int64_t kMaxSplits = 64, kFewTiles = 64, kManySteps = 64;
 
 enum AttnKind { kWhole, kShared, kTiled };
 
@@ -157,7 +162,9 @@ inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int
     p.rows = rows > kTileRowsFew && bound(kTileRows) * kv_heads >= kComputeUnits ? kTileRows : kTileRowsFew;
     p.tiles = bound(p.rows);
     const int64_t items = p.tiles * kv_heads, fill = 2 * kComputeUnits * kTileRowsFew / p.rows;
-    if (items < 64 && steps > kWholeSteps) {
+    // joining costs the more the more tiles there are (273 tiles of up to 1501 tokens: 70 us
+    // in two parts each, 45 in one)
+    if (steps > kWholeSteps && (items < kFewTiles || (items < kComputeUnits && steps > kManySteps))) {
         p.splits = ceil_div(fill, items);
         if (p.splits > ceil_div(steps, kWholeSteps)) p.splits = ceil_div(steps, kWholeSteps);
         if (p.splits > kMaxSplits) p.splits = kMaxSplits;
@@ -170,8 +177,8 @@ inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int
 inline int check_attn_shape(const nvfp4_kv_cache_t &c, int64_t heads, int64_t batch, int64_t tokens,
                             int64_t max_query, int64_t table_width) {
     if (check_cache_shape(c) != NVFP4_GEMV_OK || heads < c.kv_heads || heads > kMaxHeads ||
-        heads % c.kv_heads != 0 || tokens < 0 || tokens > kMaxTokens || tokens * heads >= (int64_t(1) << 31) ||
-        batch < 1 || batch > kMaxBatch || batch * c.kv_heads >= (int64_t(1) << 22) || max_query < 1 ||
+        heads % c.kv_heads != 0 || tokens < 0 || tokens > kMaxTokens || tokens * heads >= (int64_t(1) << 30) ||
+        batch < 1 || batch > kMaxBatch || batch * c.kv_heads > (int64_t(1) << 18) || max_query < 1 ||
         (tokens > 0 && max_query > tokens) || table_width < 1 ||
         table_width > ((int64_t(1) << 31) - 1) / c.page_size)
         return NVFP4_GEMV_ERR_BAD_SHAPE;

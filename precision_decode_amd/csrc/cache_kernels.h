@@ -72,9 +72,13 @@ __device__ __forceinline__ float from16(uint32_t h, bool bf16) {
     return bf16 ? __uint_as_float(h << 16)
                 : static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(h)));
 }
-__device__ __forceinline__ uint32_t to16(float f, bool bf16) {
-    return bf16 ? nvfp4dev::bf16_rne(f) : __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+// Two floats rounded to nearest even, a in the low half.
+__device__ __forceinline__ uint32_t pair16(float a, float b, bool bf16) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return bf16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2))
+                : nvfp4dev::bits(__builtin_convertvector(f32x2{a, b}, f16x2));
 }
+__device__ __forceinline__ uint32_t to16(float f, bool bf16) { return pair16(f, 0.0f, bf16) & 0xFFFFu; }
 
 // 8 elements, two per word.
 __device__ __forceinline__ u32x4 load8(const uint16_t *p, bool wide) {
@@ -105,7 +109,7 @@ __device__ __forceinline__ void widen(u32x4 w, bool bf16, float (&x)[8]) {
 __device__ __forceinline__ u32x4 narrow(const float (&x)[8], bool bf16) {
     u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = to16(x[2 * i], bf16) | to16(x[2 * i + 1], bf16) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = pair16(x[2 * i], x[2 * i + 1], bf16);
     return w;
 }
 
@@ -139,29 +143,47 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], int rule) {
     return w;
 }
 
-// This lane's 8 of a block's 16 values (the neighbour lane has the others): codes
-// and the block's scale code, the arithmetic of nvfp4_quantize.h.
-__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], float g, int rule, uint32_t *scale) {
-    // the largest magnitude by its bit pattern, where NaN comes above infinity
-    uint32_t top = 0;
+// This lane's 8 of a block's 16 values (`w` as they are stored, x as floats; the
+// neighbour lane has the others): codes and the block's scale code, the arithmetic of
+// nvfp4_quantize.h.  For ordinary values and scales the two divisions of an element are
+// products that round as the divisions do (quot_f64, quot_short); `inverse` is 1 / g in
+// 64 bits.
+__device__ __forceinline__ uint32_t quantize8(u32x4 w, const float (&x)[8], float g, double inverse, bool bf16, int rule,
+                                              uint32_t *scale) {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    // the largest magnitude by its bit pattern, where NaN comes above infinity, and the
+    // smallest that is not zero (less one: zero wraps to the top)
+    u16x2 high = {0, 0}, low = {0xFFFF, 0xFFFF};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-        top = b > top ? b : top;
+    for (int i = 0; i < 4; ++i) {
+        const u16x2 m = __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu);
+        high = __builtin_elementwise_max(high, m);
+        low = __builtin_elementwise_min(low, static_cast<u16x2>(m - u16x2{1, 1}));
     }
+    uint32_t top = high.x > high.y ? high.x : high.y;
+    const uint32_t tiny = low.x < low.y ? low.x : low.y;
     const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(top), 0xB1, 0xF, 0xF, false));
     top = other > top ? other : top;
+    // every nonzero bf16 magnitude at least 2^-100 (fp16 ones all are)
+    const bool fast = g >= 0x1p-40f && g <= 0x1p30f && (!bf16 || tiny >= (27u << 7) - 1u);
     // rounding is monotonic: max |x / g| is max |x| / |g|
-    float am = __uint_as_float(top) / __builtin_fabsf(g);
+    const float largest = from16(top, bf16);
+    float am = fast ? nvfp4quant::quot_f64(largest, inverse) : largest / __builtin_fabsf(g);
     am = am < 1e-8f ? 1e-8f : am;                     // NaN stays NaN
-    const uint32_t s = nvfp4quant::e4m3_code_pos(am / 6.0f);
+    const uint32_t s = nvfp4quant::e4m3_code_pos(nvfp4quant::quot_f64(am, 1.0 / 6.0));
     *scale = s;
     if (s == 0x7Fu) return 0u;                        // a NaN scale: every code is 0
     const float sv = nvfp4quant::e4m3_value_pos(s);
     const float den = sv < 1e-8f ? 1e-8f : sv;
     float v[8];
+    if (fast && s != 0u) {                            // s = 0: den is no 4-bit number
+        const float y = __builtin_amdgcn_rcpf(den);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[i] / g / den + 0.0f;   // -0 -> +0: its code is 0
+        for (int i = 0; i < 8; ++i) v[i] = nvfp4quant::quot_short(nvfp4quant::quot_f64(x[i], inverse), den, y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x[i] / g / den + 0.0f;   // -0 -> +0: its code is 0
+    }
     return codes8(v, rule);
 }
 
@@ -288,8 +310,10 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope_rows(const RowArgs a) {
             for (int j = 0; j < 8; ++j) x[j] = 0.0f;
         }
         const float *global = is_v ? a.cache.v_global : a.cache.k_global;
+        const float g = global != nullptr ? global[h] : 1.0f;
         uint32_t scale;
-        uint32_t codes = quantize8(x, global != nullptr ? global[h] : 1.0f, a.rule, &scale);
+        uint32_t codes = quantize8(inside ? out : u32x4{0, 0, 0, 0}, x, g, nvfp4quant::recip_f64(static_cast<double>(g)), bf16,
+                                   a.rule, &scale);
         if (!inside) codes = scale = 0u;              // the padding up to dp
         if (slot < 0 || e0 >= a.cache.dp) continue;
         const int64_t page = slot >> a.cache.page_log2;

@@ -270,8 +270,8 @@ int nvfp4_qk_norm_rope_launch(const void *Q, int64_t q_token_stride, int64_t q_h
     if (!type16(x_type) || interleaved < 0 || interleaved > 1 || !rule_known(rule) || (cached && K_out) ||
         !(eps >= 0.0f) || std::isinf(eps))
         return NVFP4_GEMV_ERR_BAD_ARGUMENT;
-    if (check_dims(kv_heads, head_dim) != NVFP4_GEMV_OK || heads < 0 || heads > kMaxHeads || tokens < 0 ||
-        tokens > kMaxTokens || tokens * (heads + 2 * kv_heads) >= (int64_t(1) << 31) || rot_dim < 0 ||
+    if (check_dims(kv_heads, head_dim) != NVFP4_GEMV_OK || heads < 0 || heads > kMaxHeads ||
+        !rows_ok(tokens, heads + 2 * kv_heads) || rot_dim < 0 ||
         rot_dim > head_dim || rot_dim % 16 != 0 || (rot_dim > 0 && (table_rows < 1 || table_rows > kMaxStride)) ||
         (cached && (cache->kv_heads != kv_heads || cache->head_dim != head_dim)))
         return NVFP4_GEMV_ERR_BAD_SHAPE;
@@ -349,8 +349,7 @@ int nvfp4_kv_read_launch(const nvfp4_kv_cache_t *cache, const int64_t *slots, in
     if (s != NVFP4_GEMV_OK) return s;
     if (!slots || !K || !V) return NVFP4_GEMV_ERR_NULL_POINTER;
     if (!type16(y_type) && y_type != NVFP4_OUT_F32) return NVFP4_GEMV_ERR_BAD_ARGUMENT;
-    if (tokens < 0 || tokens > kMaxTokens || tokens * 2 * cache->kv_heads >= (int64_t(1) << 31))
-        return NVFP4_GEMV_ERR_BAD_SHAPE;
+    if (!rows_ok(tokens, 2 * cache->kv_heads)) return NVFP4_GEMV_ERR_BAD_SHAPE;
     const int bytes = y_type == NVFP4_OUT_F32 ? 4 : 2;
     if (misaligned(K, bytes) || misaligned(V, bytes) || misaligned(slots, 8)) return NVFP4_GEMV_ERR_ALIGNMENT;
     s = check_cache_alignment(*cache);
