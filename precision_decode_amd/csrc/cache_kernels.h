@@ -52,9 +52,9 @@ struct RowArgs {
     const float *cos_sin;
     int64_t table_rows, tokens;
     int32_t heads, kv_heads, head_dim, rot_dim;
-    int32_t rows, chunks;  // rows of a token (queries, keys, values); chunks of kRowsInFlight of them
+    int32_t q_chunks, k_chunks, chunks;   // chunks of kRowsInFlight rows of a token: queries', keys', all with values'
     int32_t interleaved, bf16, rule;
-    float eps;
+    float eps, inverse_dim;
     CacheArgs cache;
     const int64_t *slots;  // NULL: no cache
 };
@@ -187,6 +187,14 @@ __device__ __forceinline__ uint32_t quantize8(u32x4 w, const float (&x)[8], floa
     return codes8(v, rule);
 }
 
+// 1 / sqrt(v) to about one unit in the last place, also where v is subnormal (which
+// the instruction takes as zero).
+__device__ __forceinline__ float inverse_root(float v) {
+    const bool small = v < 0x1p-100f;
+    const float y = __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v);
+    return small ? y * 0x1p32f : y;
+}
+
 // Sum over the L lanes of a group, the same in each.
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
@@ -197,38 +205,65 @@ __device__ __forceinline__ float group_sum(float v) {
 
 // One group of L lanes takes up to kRowsInFlight rows of one token: queries, then
 // keys, then values.  L * 8 elements hold a row.
-template <int L>
+template <int L, bool kBf16>
 __global__ __launch_bounds__(kRowThreads) void norm_rope_rows(const RowArgs a) {
     const int l = threadIdx.x % L;
-    const int64_t group = static_cast<int64_t>(blockIdx.x) * (kRowThreads / L) + threadIdx.x / L;
-    const int64_t t = group / a.chunks;
-    if (t >= a.tokens) return;                        // whole groups
-    const int first = static_cast<int>(group - t * a.chunks) * kRowsInFlight;
+    const uint32_t group = blockIdx.x * (kRowThreads / L) + threadIdx.x / L;   // below 2^28
+    const uint32_t token = group / static_cast<uint32_t>(a.chunks);
+    if (token >= static_cast<uint32_t>(a.tokens)) return;   // whole groups
+    const int64_t t = token;
+    // a chunk holds rows of one kind, queries first, then keys, then values
+    const int chunk = static_cast<int>(group - token * static_cast<uint32_t>(a.chunks));
+    const bool is_q = chunk < a.q_chunks, is_v = chunk >= a.q_chunks + a.k_chunks;
+    const int first = (is_q ? chunk : is_v ? chunk - a.q_chunks - a.k_chunks : chunk - a.q_chunks) * kRowsInFlight;
+    const int left = (is_q ? a.heads : a.kv_heads) - first;   // rows of this chunk and the ones behind it
     const int e0 = 8 * l;                             // this lane's first element
     const bool inside = e0 < a.head_dim;
-    const bool bf16 = a.bf16 != 0;
+    const bool cached = a.slots != nullptr && !is_q;
 
+    const Rows r = is_q ? a.q : is_v ? a.v : a.k;
+    const uint16_t *from = r.p + t * r.token + first * r.head + e0;
+    const float *global = is_v ? a.cache.v_global : a.cache.k_global;
     u32x4 raw[kRowsInFlight];
+    float g[kRowsInFlight];
 #pragma unroll
     for (int i = 0; i < kRowsInFlight; ++i) {
-        const int row = first + i;
         raw[i] = u32x4{0, 0, 0, 0};
-        if (row >= a.rows || !inside) continue;
-        const Rows &r = row < a.heads ? a.q : row < a.heads + a.kv_heads ? a.k : a.v;
-        const int h = row < a.heads ? row : row < a.heads + a.kv_heads ? row - a.heads : row - a.heads - a.kv_heads;
-        raw[i] = load8(r.p + t * r.token + h * r.head + e0, r.wide);
+        g[i] = 1.0f;
+        if (i < left && inside) raw[i] = load8(from + i * r.head, r.wide);
+        if (i < left && cached && global != nullptr) g[i] = global[first + i];
+    }
+    float weight[8];
+    const float *w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
+    if (w != nullptr && inside) {
+        const f32x4 w0 = *reinterpret_cast<const f32x4 *>(w + e0), w1 = *reinterpret_cast<const f32x4 *>(w + e0 + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) weight[j] = j < 4 ? w0[j % 4] : w1[j % 4];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) weight[j] = 1.0f;
     }
     int64_t slot = -1;
-    if (a.slots != nullptr) {
+    if (cached) {
         slot = a.slots[t];
         if (slot >= a.cache.slots) slot = -1;
     }
+    const int64_t page = slot >> a.cache.page_log2;
+    const int64_t off = slot & ((int64_t(1) << a.cache.page_log2) - 1);
+    const int64_t head = page * a.cache.kv_heads + first;
+    uint8_t *codes_at = (is_v ? a.cache.v_codes : a.cache.k_codes) + ((head << a.cache.page_log2) + off) * (a.cache.dp / 2) + 4 * l;
+    uint8_t *scales_at = (is_v ? a.cache.v_scales : a.cache.k_scales) +
+                         ((head * (a.cache.dp / 16) + l / 2) << a.cache.page_log2) + off;
+    const int codes_step = (a.cache.dp / 2) << a.cache.page_log2, scales_step = (a.cache.dp / 16) << a.cache.page_log2;
+    const int64_t to_head = is_q ? a.qo_head : a.ko_head;
+    uint16_t *to = is_q ? a.q_out + t * a.qo_token + first * to_head + e0 : a.k_out + t * a.ko_token + first * to_head + e0;
+    const bool to_wide = is_q ? a.qo_wide : a.ko_wide;
     // cosines and sines of this lane's elements
     const int half = a.rot_dim / 2;
     const bool turned = e0 < a.rot_dim;
     float cs[8], sn[8];
     bool known = true;
-    if (a.rot_dim > 0) {
+    if (a.rot_dim > 0 && !is_v) {
         const int64_t p = a.positions[t];
         known = p >= 0 && p < a.table_rows;
         if (turned && known) {
@@ -259,25 +294,18 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope_rows(const RowArgs a) {
 
 #pragma unroll
     for (int i = 0; i < kRowsInFlight; ++i) {
-        const int row = first + i;
-        if (row >= a.rows) return;                    // whole groups
-        const bool is_q = row < a.heads, is_v = row >= a.heads + a.kv_heads;
+        if (i >= left) return;                        // whole groups
         float x[8];
-        widen(raw[i], bf16, x);
+        widen(raw[i], kBf16, x);
+        u32x4 out = raw[i];                           // values go on as they are
         if (!is_v) {
-            const float *w = is_q ? a.q_weight : a.k_weight;
             if (w != nullptr) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum += x[j] * x[j];
-                sum = group_sum<L>(sum);
-                const float r = 1.0f / __builtin_sqrtf(sum / static_cast<float>(a.head_dim) + a.eps);
-                if (inside) {
-                    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(w + e0);
-                    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(w + e0 + 4);
+                const float rr = inverse_root(group_sum<L>(sum) * a.inverse_dim + a.eps);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = x[j] * r * (j < 4 ? w0[j % 4] : w1[j % 4]);
-                }
+                for (int j = 0; j < 8; ++j) x[j] = x[j] * rr * weight[j];
             }
             if (a.rot_dim > 0) {
                 float y[8];
@@ -291,38 +319,22 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope_rows(const RowArgs a) {
                     for (int j = 0; j < 8; ++j) x[j] = x[j] * cs[j] + y[j] * sn[j];
                 }
             }
+            out = narrow(x, kBf16);
         }
-        const int h = is_q ? row : is_v ? row - a.heads - a.kv_heads : row - a.heads;
-        const u32x4 out = narrow(x, bf16);            // values are widened and narrowed unchanged
-        if (is_q) {
-            if (inside) store8(a.q_out + t * a.qo_token + h * a.qo_head + e0, out, a.qo_wide);
-            continue;
-        }
-        if (a.slots == nullptr) {
-            if (inside) store8(a.k_out + t * a.ko_token + h * a.ko_head + e0, out, a.ko_wide);
+        if (!cached) {
+            if (inside) store8(to + i * to_head, out, to_wide);
             continue;
         }
         // the cache holds the rows as rounded to x_type, so that this call and a
         // plain write of its outputs leave the same codes
-        widen(out, bf16, x);
-        if (!inside) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-        }
-        const float *global = is_v ? a.cache.v_global : a.cache.k_global;
-        const float g = global != nullptr ? global[h] : 1.0f;
+        if (!inside) out = u32x4{0, 0, 0, 0};
+        widen(out, kBf16, x);
         uint32_t scale;
-        uint32_t codes = quantize8(inside ? out : u32x4{0, 0, 0, 0}, x, g, nvfp4quant::recip_f64(static_cast<double>(g)), bf16,
-                                   a.rule, &scale);
+        uint32_t codes = quantize8(out, x, g[i], nvfp4quant::recip_f64(static_cast<double>(g[i])), kBf16, a.rule, &scale);
         if (!inside) codes = scale = 0u;              // the padding up to dp
         if (slot < 0 || e0 >= a.cache.dp) continue;
-        const int64_t page = slot >> a.cache.page_log2;
-        const int64_t off = slot & ((int64_t(1) << a.cache.page_log2) - 1);
-        const int64_t head = page * a.cache.kv_heads + h;
-        uint8_t *c = is_v ? a.cache.v_codes : a.cache.k_codes;
-        uint8_t *s = is_v ? a.cache.v_scales : a.cache.k_scales;
-        *reinterpret_cast<uint32_t *>(c + ((head << a.cache.page_log2) + off) * (a.cache.dp / 2) + 4 * l) = codes;
-        if (l % 2 == 0) s[((head * (a.cache.dp / 16) + l / 2) << a.cache.page_log2) + off] = static_cast<uint8_t>(scale);
+        *reinterpret_cast<uint32_t *>(codes_at + static_cast<int64_t>(i) * codes_step) = codes;
+        if (l % 2 == 0) scales_at[static_cast<int64_t>(i) * scales_step] = static_cast<uint8_t>(scale);
     }
 }
 
@@ -330,12 +342,13 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope_rows(const RowArgs a) {
 template <int L>
 __global__ __launch_bounds__(kRowThreads) void read_rows(const ReadArgs a) {
     const int l = threadIdx.x % L;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / L) + threadIdx.x / L;
+    const uint32_t row = blockIdx.x * (kRowThreads / L) + threadIdx.x / L;   // below 2^28
     const CacheArgs &c = a.cache;
-    const int64_t t = row / (2 * c.kv_heads);
+    const uint32_t token = row / (2u * static_cast<uint32_t>(c.kv_heads));
     const int e0 = 8 * l;
-    if (t >= a.tokens || e0 >= c.head_dim) return;
-    const int j = static_cast<int>(row - t * (2 * c.kv_heads));
+    if (token >= static_cast<uint32_t>(a.tokens) || e0 >= c.head_dim) return;
+    const int64_t t = token;
+    const int j = static_cast<int>(row - token * (2u * static_cast<uint32_t>(c.kv_heads)));
     const bool is_v = j >= c.kv_heads;
     const int h = is_v ? j - c.kv_heads : j;
     const int64_t slot = a.slots[t];

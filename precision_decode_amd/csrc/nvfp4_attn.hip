@@ -104,9 +104,13 @@ Rows rows_of(const void *p, int64_t token, int64_t head) {
 int launch_rows(RowArgs a, int64_t dp, hipStream_t stream) {
     const int lanes = dp == 64 ? 8 : dp == 128 ? 16 : 32;
     const int64_t groups = ceil_div(a.tokens * a.chunks, kRowThreads / lanes);
-    return lanes == 8    ? run(norm_rope_rows<8>, groups, kRowThreads, stream, a)
-           : lanes == 16 ? run(norm_rope_rows<16>, groups, kRowThreads, stream, a)
-                         : run(norm_rope_rows<32>, groups, kRowThreads, stream, a);
+    if (a.bf16)
+        return lanes == 8    ? run(norm_rope_rows<8, true>, groups, kRowThreads, stream, a)
+               : lanes == 16 ? run(norm_rope_rows<16, true>, groups, kRowThreads, stream, a)
+                             : run(norm_rope_rows<32, true>, groups, kRowThreads, stream, a);
+    return lanes == 8    ? run(norm_rope_rows<8, false>, groups, kRowThreads, stream, a)
+           : lanes == 16 ? run(norm_rope_rows<16, false>, groups, kRowThreads, stream, a)
+                         : run(norm_rope_rows<32, false>, groups, kRowThreads, stream, a);
 }
 
 // ---------------------------------------------------------------- attention
@@ -332,8 +336,10 @@ int nvfp4_qk_norm_rope_launch(const void *Q, int64_t q_token_stride, int64_t q_h
     a.kv_heads = static_cast<int32_t>(kv_heads);
     a.head_dim = static_cast<int32_t>(head_dim);
     a.rot_dim = static_cast<int32_t>(rot_dim);
-    a.rows = static_cast<int32_t>(heads + (cached ? 2 : 1) * kv_heads);
-    a.chunks = static_cast<int32_t>(ceil_div(a.rows, kRowsInFlight));
+    a.q_chunks = static_cast<int32_t>(ceil_div(heads, kRowsInFlight));
+    a.k_chunks = static_cast<int32_t>(ceil_div(kv_heads, kRowsInFlight));
+    a.chunks = a.q_chunks + (cached ? 2 : 1) * a.k_chunks;
+    a.inverse_dim = 1.0f / static_cast<float>(head_dim);
     a.interleaved = interleaved;
     a.bf16 = x_type == NVFP4_OUT_BF16;
     a.rule = rule;
