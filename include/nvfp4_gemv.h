@@ -121,10 +121,11 @@ int nvfp4_gemv_launch_ws(const uint8_t *A_packed, const uint8_t *sfA,
  * `bytes` bytes, so that later calls on `stream` needing no more than that
  * allocate nothing (for instance under graph capture).  The workspace serves
  * nvfp4_gemv_launch, nvfp4_gemm_smalln_launch(_packed), nvfp4_quantize_weight,
- * nvfp4_gemv_bf16x_launch, nvfp4_linear_launch and nvfp4_moe_layer_launch on that
- * stream; take `bytes` from nvfp4_gemv_workspace_size, the plan calls,
- * nvfp4_linear_workspace_size or nvfp4_moe_layer_workspace_size.  Not capture-safe
- * itself.
+ * nvfp4_gemv_bf16x_launch, nvfp4_linear_launch, nvfp4_moe_layer_launch and
+ * nvfp4_kv_attention_launch on that stream; take `bytes` from
+ * nvfp4_gemv_workspace_size, the plan calls, nvfp4_linear_workspace_size,
+ * nvfp4_moe_layer_workspace_size or nvfp4_kv_attention_workspace_size.  Not
+ * capture-safe itself.
  * Returns NVFP4_GEMV_OK, NVFP4_GEMV_ERR_DEVICE (no current device) or
  * NVFP4_GEMV_ERR_WORKSPACE (allocation failed, or `stream` is capturing).
  */

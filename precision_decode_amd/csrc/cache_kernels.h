@@ -4,7 +4,11 @@
 // the C ABI.
 //
 // All three move bytes: a row of head_dim elements is read once and written once,
-// 16 bytes a lane, with a few dozen operations per 8 elements.
+// 16 bytes a lane.  Queries and keys of 4096 tokens normalised and rotated (64 rows of
+// 128, 136 MB): 34 us, 4.0 TB/s, against 27 at the rate of a copy; beside it 228 vector
+// instructions per 8 elements (the sum of squares, the rotation, the roundings,
+// addresses).  Keys and values of 8192 tokens, 8 heads of 128, into the cache: 20 us,
+// 204 instructions per 8 elements, and back 12.7 us.
 #ifndef NVFP4_CACHE_KERNELS_H
 #define NVFP4_CACHE_KERNELS_H
 
@@ -52,7 +56,8 @@ struct RowArgs {
     const float *cos_sin;
     int64_t table_rows, tokens;
     int32_t heads, kv_heads, head_dim, rot_dim;
-    int32_t q_chunks, k_chunks, chunks;   // chunks of kRowsInFlight rows of a token: queries', keys', all with values'
+    int32_t each;          // rows of a chunk, at most kRowsInFlight
+    int32_t q_chunks, k_chunks, chunks;   // chunks of a token: queries', keys', all with values'
     int32_t interleaved, bf16, rule;
     float eps, inverse_dim;
     CacheArgs cache;
@@ -215,8 +220,8 @@ __global__ __launch_bounds__(kRowThreads) void norm_rope_rows(const RowArgs a) {
     // a chunk holds rows of one kind, queries first, then keys, then values
     const int chunk = static_cast<int>(group - token * static_cast<uint32_t>(a.chunks));
     const bool is_q = chunk < a.q_chunks, is_v = chunk >= a.q_chunks + a.k_chunks;
-    const int first = (is_q ? chunk : is_v ? chunk - a.q_chunks - a.k_chunks : chunk - a.q_chunks) * kRowsInFlight;
-    const int left = (is_q ? a.heads : a.kv_heads) - first;   // rows of this chunk and the ones behind it
+    const int first = (is_q ? chunk : is_v ? chunk - a.q_chunks - a.k_chunks : chunk - a.q_chunks) * a.each;
+    const int rest = (is_q ? a.heads : a.kv_heads) - first, left = rest < a.each ? rest : a.each;
     const int e0 = 8 * l;                             // this lane's first element
     const bool inside = e0 < a.head_dim;
     const bool cached = a.slots != nullptr && !is_q;
