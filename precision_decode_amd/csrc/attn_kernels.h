@@ -454,7 +454,7 @@ struct Stream {
     }
 
     // Rows that see a token whose block of V is NaN: NaN there.  `bad` holds the
-    // tokens (bits) of this lane's run and block.
+    // tokens (bits) of this lane's run and block, none of a run whose page is not there.
     template <int B>
     __device__ __forceinline__ void poison_block(const AttnArgs &a, int tok0, uint32_t bad) {
         for (int run = 0; run < 4; ++run) {
@@ -566,6 +566,8 @@ struct Stream {
                 bad |= ((nan >> 7) * 0x10204080u >> 28) << (4 * i);
                 vsw[0][i] &= ~((nan >> 7) * 0xFFu);
             }
+            // page 0 stands in for a page that is not there: what it holds is of another's
+            if (!((there >> (4 * h)) & 1u)) bad = 0;
         }
         f16x2 vs[8];
 #pragma unroll
