@@ -36,6 +36,7 @@ constexpr int kStep = 64;                  // cache tokens of a step: four runs 
 constexpr int kRun = 16;
 constexpr float kWeightShift = 8.0f;       // P is scaled by 2^8
 constexpr float kRescaleAt = 6.0f;         // growth of the maximum (log2) that rescales the sums: P stays below 2^14
+constexpr float kFarMaximum = 0x1p16f;     // a maximum (log2) from which scores are rounded before it is subtracted
 constexpr int kAluCrosses = 0x2 | 0x4 | 0x400;   // a scheduling barrier for all but VALU, SALU and transcendentals
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -177,6 +178,13 @@ __device__ __forceinline__ f16x8 scale_bf16(u32x4 w, float up) {
 __device__ __forceinline__ bool visible(const AttnArgs &a, int p, int j) {
     return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
 }
+
+// A weight is exp2(score c - maximum + 8), which takes one fused operation while the
+// maximum's own rounding is small beside 1.  A maximum of 2^24 and more is off by its
+// rounding from the product that it was rounded from, which fp16 weights do not hold:
+// there the scores are rounded as the maximum was, before it is subtracted, and the
+// difference of near ones is exact.
+__device__ __forceinline__ bool far_maximum(float m) { return __builtin_fabsf(m) >= kFarMaximum; }
 
 __device__ __forceinline__ void store4(uint16_t *p, f32x4 v, bool bf16, bool wide) {
     const uint32_t lo = pair16(v[0], v[1], bf16), hi = pair16(v[2], v[3], bf16);
@@ -486,7 +494,7 @@ struct Stream {
 
     // Softmax of row tile r: its running maximum and sum, the step's weights as B
     // operands.
-    __device__ __forceinline__ void weigh(int r, const f32x4 (&sc)[4], f16x8 (&p)[2]) {
+    __device__ __forceinline__ void weigh(int r, f32x4 (&sc)[4], f16x8 (&p)[2]) {
         float top = sc[0][0];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -494,7 +502,7 @@ struct Stream {
             for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, sc[t][i]);
         top = rows_max(top);
         top = top == -__builtin_inff() ? top : top * c[r];
-        const bool grown = top > m[r] + kRescaleAt || (m[r] == -__builtin_inff() && top > m[r]);
+        const bool grown = top - m[r] > kRescaleAt;    // also of a first score; not of NaN, nor of none
         if (__any(grown)) {
             const float to = grown ? top : m[r];
             const float f = grown ? __builtin_amdgcn_exp2f(m[r] - to) : 1.0f;
@@ -503,13 +511,22 @@ struct Stream {
 #pragma unroll
             for (int b = 0; b < NB; ++b) acc[r][b] *= f;
         }
-        const float shift = kWeightShift - (m[r] == -__builtin_inff() ? 0.0f : m[r]);
+        const float base = m[r] == -__builtin_inff() ? 0.0f : m[r];
+        float factor = c[r], shift = kWeightShift - base;
+        if (__any(far_maximum(base))) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[t][i] = far_maximum(base) ? sc[t][i] * c[r] - base : sc[t][i];
+            factor = far_maximum(base) ? 1.0f : factor;
+            shift = far_maximum(base) ? kWeightShift : shift;
+        }
         float sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], c[r], shift));
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], factor, shift));
                 sum[i] += e;
                 p[t / 2][4 * (t % 2) + i] = static_cast<_Float16>(e);
             }
@@ -1274,8 +1291,11 @@ struct Tile {
     }
 
     // Operands are read kAhead products before they are needed.  A read's address is the
-    // lane's row, its place turned by the chunk's low bits, and a constant.
-    static constexpr int kAhead = NB <= 8 ? 8 : 4;
+    // lane's row, its place turned by the chunk's low bits, and a constant.  Heads of more
+    // than 192 have registers for three (4096 tokens, 16 heads on 4 of 256: 336 us with 27
+    // of them spilled, 370 with four and 39, 342 with two; five ragged prompts of up to 701
+    // tokens, 12 heads on 3: 112, 120 and 117).
+    static constexpr int kAhead = NB <= 8 ? 8 : NB <= 12 ? 4 : 3;
     static constexpr int kTurnK = NB == 8 || NB == 16 ? 15 : 7, kTurnV = kT == 64 ? 7 : 3;
 
     // Scores of K in buffer `from`.
@@ -1329,7 +1349,7 @@ struct Tile {
             for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, sc[u][i]);
         top = xor32(top, true);
         top = top == -__builtin_inff() ? top : top * c;
-        const bool grown = top > m + kRescaleAt || (m == -__builtin_inff() && top > m);
+        const bool grown = top - m > kRescaleAt;       // also of a first score; not of NaN, nor of none
         if (__any(grown)) {
             const float to = grown ? top : m;
             const float f = grown ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
@@ -1340,13 +1360,22 @@ struct Tile {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[o][i] *= f;
         }
-        const float shift = kWeightShift - (m == -__builtin_inff() ? 0.0f : m);
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+        float factor = c, shift = kWeightShift - base;
+        if (__any(far_maximum(base))) {
+#pragma unroll
+            for (int u = 0; u < kT / 32; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sc[u][i] = far_maximum(base) ? sc[u][i] * c - base : sc[u][i];
+            factor = far_maximum(base) ? 1.0f : factor;
+            shift = far_maximum(base) ? kWeightShift : shift;
+        }
         float sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int u = 0; u < kT / 32; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][i], c, shift));
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][i], factor, shift));
                 sum[i % 4] += e;
                 p[2 * u + i / 8][i % 8] = static_cast<_Float16>(e);
             }
