@@ -129,6 +129,7 @@ int nvfp4_qk_norm_rope_launch(const void *Q, int64_t q_token_stride, int64_t q_h
  *
  * A query that sees no token, or whose scores are all minus infinity, gives zeros;
  * what stands in the places of other tokens (infinities, NaN) does not matter.
+ * Where scale * k_global[head] is not finite in fp32, queries that see a token give NaN.
  *   Q, out        x_type (fp16 or bf16), tokens x heads rows; out is not Q
  *   block_table   int32, row b at block_table + b * table_stride, table_width pages
  *                 each.  A page outside [0, pages) is not read and its tokens are not

@@ -174,6 +174,10 @@ __device__ __forceinline__ f16x8 scale_bf16(u32x4 w, float up) {
     return x;
 }
 
+__device__ __forceinline__ f16x8 nan8() {
+    return __builtin_bit_cast(f16x8, u32x4{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u});
+}
+
 // Whether a query at position p (-1: none) sees token j.
 __device__ __forceinline__ bool visible(const AttnArgs &a, int p, int j) {
     return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
@@ -653,6 +657,11 @@ struct Stream {
             }
             c[r] = __builtin_fabsf(g) * kLog2e * down;
             c[r] = c[r] == 0.0f ? 0x1p-126f : c[r];      // hidden scores stay minus infinity, others about 0
+            if (!(__builtin_fabsf(g) < __builtin_inff())) {   // no factor of scores: those of tokens that are seen are NaN
+                c[r] = 1.0f;
+#pragma unroll
+                for (int j = 0; j < kK; ++j) q[r][j] = nan8();
+            }
         }
     }
 
@@ -1288,6 +1297,11 @@ struct Tile {
         }
         c = __builtin_fabsf(g) * kLog2e * down;
         c = c == 0.0f ? 0x1p-126f : c;                 // as in the stream kernel
+        if (!(__builtin_fabsf(g) < __builtin_inff())) {
+            c = 1.0f;
+#pragma unroll
+            for (int j = 0; j < kSlices; ++j) q[j] = nan8();
+        }
     }
 
     // Operands are read kAhead products before they are needed.  A read's address is the

@@ -1,5 +1,5 @@
 """Attention where scores are far from ordinary: finite ones of 2^20 to 2^90, whose
-softmax is one or a few tokens."""
+softmax is one or a few tokens, and globals that are not finite."""
 import numpy as np
 import pytest
 import torch
@@ -76,3 +76,22 @@ def test_large_scores_of_either_sign(n, tokens):
         want, _ = oa.attention(q, cache, table, [tokens], [0, n], scale)
         got = pd.kv_attention(heads_on_device(q, "f16"), on_device(cache, dim), i32(table), i32([tokens]), scale=scale)
         assert_close(got, want, np.abs(want) * (2.0 ** -11 + 2.0 ** -20), "f16")
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("n,tokens,width", [(6, 3, 16), (6, 3, 64), (16, 9, 64), (80, 40, 64)])
+def test_globals_that_are_not_finite_leave_rows_without_tokens_zero(n, tokens, width, value):
+    """The first n - tokens queries see no token: they are zero whatever the globals are; the
+    others are NaN where k_global is not finite."""
+    rng = np.random.default_rng(2)
+    cache = filled(rng, 8, 2, 16, 64)
+    cache["kg"][0] = value
+    table, _ = tables(rng, [tokens], 16, 8, width)
+    q = heads_on_device(rng.standard_normal((n, 4, 64)), "bf16")
+    got = pd.kv_attention(q, on_device(cache, 64), i32(table), i32([tokens]))
+    assert bool((got[:n - tokens] == 0).all())
+    assert bool(got[n - tokens:, :2].isnan().all()) and bool(got[n - tokens:, 2:].isfinite().all())
+    cache["kg"][0], cache["vg"][1] = 1.0, np.nan
+    got = pd.kv_attention(q, on_device(cache, 64), i32(table), i32([tokens]))
+    assert bool((got[:n - tokens] == 0).all())
+    assert bool(got[n - tokens:, 2:].isnan().all()) and bool(got[n - tokens:, :2].isfinite().all())
