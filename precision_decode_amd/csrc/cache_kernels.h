@@ -16,6 +16,7 @@
 
 #include <cstdint>
 
+#include "attn_plan.h"
 #include "device_common.h"
 #include "nvfp4_attn.h"
 #include "quant_arith.h"
@@ -28,10 +29,10 @@ using nvfp4dev::f32x4;
 using nvfp4dev::kWave;
 using nvfp4dev::u32x4;
 
-constexpr int kRowThreads = 256;
+using nvfp4attnplan::kRowThreads;
 // Rows of one token that a group of lanes takes one after the other, all loads
 // first: its cosines and sines are read once for them.
-constexpr int kRowsInFlight = 4;
+using nvfp4attnplan::kRowsInFlight;
 
 struct Rows {
     const uint16_t *p;

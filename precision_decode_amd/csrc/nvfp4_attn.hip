@@ -100,19 +100,14 @@ Rows rows_of(const void *p, int64_t token, int64_t head) {
     return {static_cast<const uint16_t *>(p), token, head, wide_rows(p, token, head)};
 }
 
-constexpr int64_t kWavesPerUnit = 16;
-
-// Lanes of a row's group: 8 elements each, a power of two.
 int launch_rows(RowArgs a, int64_t dp, hipStream_t stream) {
-    const int lanes = dp == 64 ? 8 : dp == 128 ? 16 : 32;
-    const int parts = a.slots != nullptr ? 2 : 1;
-    // One row a group of lanes until that gives each SIMD its waves: the rows of a group
-    // come one after the other (64 tokens of 48 rows of 128: 4.9 us with one, 9.2 with four).
-    a.each = a.tokens * (a.heads + parts * a.kv_heads) * lanes / kWave < kComputeUnits * kWavesPerUnit ? 1 : kRowsInFlight;
-    a.q_chunks = static_cast<int32_t>(ceil_div(a.heads, a.each));
-    a.k_chunks = static_cast<int32_t>(ceil_div(a.kv_heads, a.each));
-    a.chunks = a.q_chunks + parts * a.k_chunks;
-    const int64_t groups = ceil_div(a.tokens * a.chunks, kRowThreads / lanes);
+    const RowPlan p = plan_rows(a.tokens, a.heads, a.kv_heads, a.slots != nullptr, dp);
+    const int lanes = p.lanes;
+    const int64_t groups = p.groups;
+    a.each = p.each;
+    a.q_chunks = p.q_chunks;
+    a.k_chunks = p.k_chunks;
+    a.chunks = p.chunks;
     if (a.bf16)
         return lanes == 8    ? run(norm_rope_rows<8, true>, groups, kRowThreads, stream, a)
                : lanes == 16 ? run(norm_rope_rows<16, true>, groups, kRowThreads, stream, a)
@@ -373,18 +368,22 @@ int nvfp4_kv_read_launch(const nvfp4_kv_cache_t *cache, const int64_t *slots, in
     if (tokens == 0) return NVFP4_GEMV_OK;
     ReadArgs a = {};
     a.cache = cache_args(*cache);
-    a.slots = slots;
-    a.k = K;
-    a.v = V;
-    a.tokens = tokens;
     a.y_type = y_type;
     a.wide = !misaligned(K, 16) && !misaligned(V, 16);
-    const int lanes = a.cache.dp == 64 ? 8 : a.cache.dp == 128 ? 16 : 32;
-    const int64_t groups = ceil_div(tokens * 2 * cache->kv_heads, kRowThreads / lanes);
+    const int lanes = row_lanes(a.cache.dp);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    return lanes == 8    ? run(read_rows<8>, groups, kRowThreads, st, a)
-           : lanes == 16 ? run(read_rows<16>, groups, kRowThreads, st, a)
-                         : run(read_rows<32>, groups, kRowThreads, st, a);
+    const int64_t most = read_tokens(cache->kv_heads, a.cache.dp), token = cache->kv_heads * cache->head_dim * bytes;
+    for (int64_t first = 0; first < tokens && s == NVFP4_GEMV_OK; first += most) {   // one launch but next to 2^27 rows
+        a.slots = slots + first;
+        a.k = static_cast<uint8_t *>(K) + first * token;
+        a.v = static_cast<uint8_t *>(V) + first * token;
+        a.tokens = tokens - first < most ? tokens - first : most;
+        const int64_t groups = read_groups(a.tokens, cache->kv_heads, a.cache.dp);
+        s = lanes == 8    ? run(read_rows<8>, groups, kRowThreads, st, a)
+            : lanes == 16 ? run(read_rows<16>, groups, kRowThreads, st, a)
+                          : run(read_rows<32>, groups, kRowThreads, st, a);
+    }
+    return s;
 }
 
 size_t nvfp4_kv_attention_workspace_size(const nvfp4_kv_cache_t *cache, int64_t heads, int64_t batch,
