@@ -996,7 +996,8 @@ struct Joiner {
     }
 
     // The row's outputs of this lane; true in the first of the waves, `wave` 0, only.
-    static __device__ __forceinline__ bool run(Buffers &buf, const float *part, int64_t stride, const float *ml,
+    // One wave exchanges nothing: `buf` may be NULL.
+    static __device__ __forceinline__ bool run(Buffers *buf, const float *part, int64_t stride, const float *ml,
                                                int64_t ml_stride, int n, int wave, Vec *out, float *total) {
         const int lane = threadIdx.x & (kWave - 1);
         Vec v = {};
@@ -1010,15 +1011,15 @@ struct Joiner {
         }
         if constexpr (WAVES > 1) {
             if (wave > 0) {
-                buf.sums[wave][lane] = v;
-                if (lane == 0) buf.total[wave] = sum;
+                buf->sums[wave][lane] = v;
+                if (lane == 0) buf->total[wave] = sum;
             }
             __syncthreads();
             if (wave > 0) return false;
 #pragma unroll
             for (int k = 1; k < WAVES; ++k) {
-                v += buf.sums[k][lane];
-                sum += buf.total[k];
+                v += buf->sums[k][lane];
+                sum += buf->total[k];
             }
         }
         *out = v;
@@ -1062,7 +1063,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(const AttnArgs a, int 
     const int64_t first = before * a.c.kv_heads + static_cast<int64_t>(kvh) * pieces;
     typename J::Vec v;
     float total;
-    if (J::run(buf, a.part + (first * rows + row) * J::kDp, static_cast<int64_t>(rows) * J::kDp,
+    if (J::run(&buf, a.part + (first * rows + row) * J::kDp, static_cast<int64_t>(rows) * J::kDp,
                a.ml + (first * rows + row) * 2, 2 * rows, pieces, wave, &v, &total))
         J::store(a, s, kvh, row, v, total);
 }
@@ -1583,7 +1584,6 @@ constexpr int kJoinRows = 8;
 template <int NB>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_tiles(const AttnArgs a, int tiles, int splits, int rows) {
     using J = Joiner<NB, 1>;
-    typename J::Buffers *none = nullptr;               // one wave a row exchanges nothing
     const int chunks = rows / kJoinRows, item = blockIdx.x / chunks, chunk = blockIdx.x - item * chunks;
     const TileJob j = tile_job(a, item, tiles, rows);
     if (j.b >= a.batch) return;
@@ -1594,7 +1594,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_tiles(const AttnArgs a
     for (int row = chunk * kJoinRows + wave; row < (chunk + 1) * kJoinRows && row < end; row += kAttnWaves) {
         typename J::Vec v;
         float total;
-        J::run(*none, part + row * J::kDp, each, part + rows * J::kDp + 2 * row, each, splits, 0, &v, &total);
+        J::run(nullptr, part + row * J::kDp, each, part + rows * J::kDp + 2 * row, each, splits, 0, &v, &total);
         J::store(a, s, j.kvh, j.row0 + row, v, total);
     }
 }
