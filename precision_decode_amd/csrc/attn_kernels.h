@@ -815,21 +815,20 @@ __device__ __forceinline__ Counts counts_from(int b0, int batch, Count count) {
     c.upto = wave_upto(c.own);
     return c;
 }
-// The sequence that holds `at` where each counts count(b) * times, and where its
-// counts begin; batch if none does.  Every wave finds it by itself.
+// The sequence that holds `at` where each counts count(b), and where its counts begin;
+// batch if none does.  Every wave finds it by itself.
 template <typename Count>
-__device__ __forceinline__ int sequence_with(int64_t at, int64_t times, int batch, Count count, int64_t *before) {
+__device__ __forceinline__ int sequence_with(int64_t at, int batch, Count count, int64_t *before) {
     int64_t base = 0;
     for (int b0 = 0; b0 < batch; b0 += kWave) {
         const Counts c = counts_from(b0, batch, count);
-        const int64_t end = base + static_cast<int64_t>(c.upto) * times;
-        const uint64_t past = __ballot(end > at);
+        const uint64_t past = __ballot(base + static_cast<int64_t>(c.upto) > at);
         if (past != 0) {
             const int n = __builtin_ctzll(past);
-            *before = uniform64(base + static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<int>(c.upto - c.own), n)) * times);
+            *before = uniform64(base + static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(c.upto - c.own), n)));
             return b0 + n;
         }
-        base += static_cast<int64_t>(c.all()) * times;
+        base += c.all();
     }
     return batch;
 }
@@ -1551,7 +1550,7 @@ __device__ __forceinline__ TileJob tile_job(const AttnArgs &a, int item, int til
         return static_cast<int>((static_cast<int64_t>(sequence_of(a, b).computed) * a.group + rows - 1) / rows);
     };
     int64_t before = 0;
-    j.b = __builtin_amdgcn_readfirstlane(sequence_with(tile, 1, a.batch, count, &before));
+    j.b = __builtin_amdgcn_readfirstlane(sequence_with(tile, a.batch, count, &before));
     j.row0 = (tile - static_cast<int>(before)) * rows;
     return j;
 }
