@@ -149,8 +149,7 @@ inline int64_t stream_rows(int64_t dp) { return dp <= 128 ? 32 : 16; }
 constexpr int64_t kWholeSteps = 8;
 
 // Workgroups of four waves that a compute unit holds: what the stream kernel's
-// registers are kept to (512 a lane of a SIMD; no variant needs accumulation
-// registers, which the loads in flight must not end up in).
+// registers are kept to (512 a lane of a SIMD, without spills).
 constexpr int groups_per_unit(int64_t dp, int64_t rows) {
     return rows <= 16 ? (dp <= 64 ? 5 : dp <= 128 ? 4 : 2) : dp <= 64 ? 3 : 2;
 }
