@@ -144,10 +144,12 @@ int nvfp4_qk_norm_rope_launch(const void *Q, int64_t q_token_stride, int64_t q_h
  *   window        0 (all tokens) or the tokens that a query sees, itself included
  *   sinks         first tokens that stay visible outside the window
  *
- * Products of q and k are exact sums in fp32 up to its rounding (q is scaled by a
- * power of two of its row to fit fp16, where e2m1 * e4m3 is exact), softmax
- * statistics and sums are fp32, and the weights meet v rounded to fp16 after
- * scaling, 2^-11 relative; results do not depend on other sequences' values.
+ * Products of q and k are exact and summed in fp32 (a bf16 row of q is scaled by a
+ * power of two to fit fp16, where e2m1 * e4m3 is exact: elements below 2^-31 of the
+ * row's largest are rounded to multiples of at most 2^-38 of it); softmax statistics
+ * and sums are fp32, and the weights meet v rounded to fp16 after scaling, 2^-11
+ * relative.  Results do not depend on other sequences' values; their last bits may
+ * depend on the batch's lengths, by which histories are cut into pieces.
  * table_width * page_size < 2^31, batch from 1 to 65535, batch * kv_heads <= 2^18,
  * tokens * heads < 2^30, strides of block_table not negative, scale finite.
  */

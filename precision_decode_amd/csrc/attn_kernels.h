@@ -7,8 +7,8 @@
 // sums are rescaled by one number a lane.  e2m1 * e4m3 has at most 6 significant
 // bits within 2^-10 .. 2688 and is exact in fp16, so K and V meet the fp16 matrix
 // instructions as they are.  Q keeps its bits: a bf16 row is scaled by a power of
-// two that brings its largest element to 2^14, where elements down to 2^-28 of it
-// stay exact and what smaller ones lose lies below fp32's rounding of the sum.  P
+// two that brings its largest element to [2^14, 2^15), where elements down to 2^-31
+// of it stay exact (subnormal ones too) and smaller ones are rounded to 2^-24.  P
 // is exp2 of the scores minus the row's running maximum, times 2^8, rounded to
 // fp16: 11 significant bits for every weight down to 2^-22 of the largest.
 #ifndef NVFP4_ATTN_KERNELS_H

@@ -1,5 +1,6 @@
 """Attention where scores are far from ordinary: finite ones of 2^20 to 2^90, whose
-softmax is one or a few tokens, and globals that are not finite."""
+softmax is one or a few tokens, globals that are not finite, and rows of queries whose
+elements are very different in size."""
 import numpy as np
 import pytest
 import torch
@@ -95,3 +96,21 @@ def test_globals_that_are_not_finite_leave_rows_without_tokens_zero(n, tokens, w
     got = pd.kv_attention(q, on_device(cache, 64), i32(table), i32([tokens]))
     assert bool((got[:n - tokens] == 0).all())
     assert bool(got[n - tokens:, 2:].isnan().all()) and bool(got[n - tokens:, :2].isfinite().all())
+
+
+@pytest.mark.parametrize("power", [20, 27, 31])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("n,tokens", SHAPES)
+def test_small_elements_beside_a_large_one_that_meets_zeros(n, tokens, dim, power):
+    """Elements of a bf16 row down to 2^-31 of its largest keep their bits: the largest meets
+    zeros of K here, so that the scores are those of the others alone."""
+    rng = np.random.default_rng(n + dim)
+    page, pages = 16, -(-tokens // 16) + 1
+    cache = filled(rng, pages, 2, page, dim)
+    cache["kc"][..., 0] &= 0xF0
+    table, _ = tables(rng, [tokens], page, pages)
+    q = rounded(rng.uniform(1.0, 2.0, (n, 4, dim)) * rng.choice([-1.0, 1.0], (n, 4, dim)), "bf16")
+    q[..., 0] = 2.0 ** power
+    want, err = oa.attention(q, cache, table, [tokens], [0, n], 0.05)
+    got = pd.kv_attention(heads_on_device(q, "bf16"), on_device(cache, dim), i32(table), i32([tokens]), scale=0.05)
+    assert_close(got, want, err, "bf16")
