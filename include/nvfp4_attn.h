@@ -138,9 +138,10 @@ int nvfp4_qk_norm_rope_launch(const void *Q, int64_t q_token_stride, int64_t q_h
  *   query_starts  int32 [batch + 1], not decreasing, or NULL: tokens / batch queries
  *                 each.  Taken to lie in [0, tokens]; rows of out that belong to no
  *                 sequence are left as they were
- *   max_query     at least the queries of any sequence, 1 .. tokens (the kernels are
- *                 chosen by it; only that many of a sequence are computed, and only
- *                 max(1, ...) matters where query_starts is NULL)
+ *   max_query     at least the queries of any sequence, 1 .. tokens, and at least
+ *                 tokens / batch where query_starts is NULL.  The kernels are chosen by it
+ *                 for the whole batch: single tokens that share a call with a prompt take the
+ *                 prompt's.  Only that many queries of a sequence are computed
  *   window        0 (all tokens) or the tokens that a query sees, itself included
  *   sinks         first tokens that stay visible outside the window
  *

@@ -912,10 +912,11 @@ __device__ __forceinline__ Piece find_piece(const AttnArgs &a) {
 //
 // A step of 64 tokens and 128 elements takes some 600 vector instructions a wave, most of
 // them the decode of two 4-bit codes at a time and the products with their scales, and 32
-// matrix ones.  64 histories of up to 4096 tokens, 32 heads on 8 of 128 (192 MB): 52 us,
-// 3.7 TB/s, against 49 with the arithmetic left out and 43 with the loads left out: loads
-// and decode overlap, and the beginnings (the search for the piece, the page table, the
-// first step's loads: some 8 us) do not.
+// matrix ones.  64 histories of up to 4096 tokens, 32 heads on 8 of 128 (192 MB): 51 us,
+// 3.8 TB/s, and 5 for attn_join; together 55, 44 with the arithmetic of the steps left out
+// and 45 with their loads left out but the first (one query on 131072 tokens: 41, 33 and
+// 37).  Either alone takes most of the time, and they overlap only in part: vector
+// instructions are issued for 0.53 of the time, and a wave waits for 0.44 of its own.
 template <int NB, int R>
 __global__ __launch_bounds__(kAttnThreads, nvfp4attnplan::groups_per_unit(16 * NB, 16 * R)) void attn_pieces(const AttnArgs a) {
     using S = Stream<NB, R>;
@@ -1084,11 +1085,9 @@ __device__ __forceinline__ void lds_barrier() {
 // one step ahead into the other of two buffers, so that one barrier a step is
 // enough; one half of the waves decodes before its products and the other after them,
 // so that the two waves of a SIMD need the VALU and the matrix cores at different
-// times (a prompt of 4096 tokens, 32 heads of 128: 210 us in step, 195 us so; waves
-// that took turns at whole phases, with V three deep, took 201 to 220 us).  8 waves of
-// 256 rows decode a step half as often as 4 of 128 (225 us), which are taken where 256
-// would leave compute units idle.  The VALU is busy for 0.54 of the time, the matrix
-// cores for 0.31.
+// times (a prompt of 4096 tokens, 32 heads on 8 of 128: 208 us in step, 190 so).  8 waves
+// of 256 rows decode a step half as often as 4 of 128 (221 us), which are taken where 256
+// would leave compute units idle.
 template <int NB, int WAVES>
 struct Tile {
     static constexpr int kDp = 16 * NB;
@@ -1306,9 +1305,9 @@ struct Tile {
 
     // Operands are read kAhead products before they are needed.  A read's address is the
     // lane's row, its place turned by the chunk's low bits, and a constant.  Heads of more
-    // than 192 have registers for three (4096 tokens, 16 heads on 4 of 256: 336 us with 27
-    // of them spilled, 370 with four and 39, 342 with two; five ragged prompts of up to 701
-    // tokens, 12 heads on 3: 112, 120 and 117).
+    // than 192 have registers for three (4096 tokens, 16 heads on 4 of 256: 329 us with 27
+    // of them spilled, 378 with four, 342 with two; five ragged prompts of up to 701 tokens,
+    // 12 heads on 3: 112, 120 and 117).
     static constexpr int kAhead = NB <= 8 ? 8 : NB <= 12 ? 4 : 3;
     static constexpr int kTurnK = NB == 8 || NB == 16 ? 15 : 7, kTurnV = kT == 64 ? 7 : 3;
 
@@ -1558,8 +1557,8 @@ __device__ __forceinline__ TileJob tile_job(const AttnArgs &a, int item, int til
 // `tiles` bounds the tiles of all sequences; `splits` workgroups share a tile's steps.
 // Many queries of a sequence: 32 rows a wave on the 32x32x16 instructions, and each step
 // of the cache decoded once into LDS for all waves.  A prompt of 4096 tokens, 32 heads on
-// 8 of 128: 186 us, 740 TFLOP/s; vector instructions (softmax, decode) are issued for
-// half of the time and the matrix cores run for a third of it, and the two hardly overlap
+// 8 of 128: 180 - 190 us, 730 TFLOP/s; vector instructions (softmax, decode) are issued for
+// 0.55 of the time and the matrix cores run for 0.33 of it, and the two hardly overlap
 // within a wave, since a step's scores, weights and sums follow from each other.
 template <int NB, int WAVES>
 __global__ __launch_bounds__(WAVES * kWave, 2) void attn_tiles(const AttnArgs a, int tiles, int splits) {

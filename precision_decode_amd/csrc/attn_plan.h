@@ -122,8 +122,12 @@ inline RowPlan plan_rows(int64_t tokens, int64_t heads, int64_t kv_heads, bool c
     RowPlan p = {};
     const int parts = cached ? 2 : 1;
     p.lanes = row_lanes(dp);
-    // One row a group of lanes until that gives each SIMD its waves: the rows of a group
-    // come one after the other (64 tokens of 48 rows of 128: 4.9 us with one, 9.2 with four).
+    // One row a group of lanes until that gives each SIMD its waves, four from there on: the
+    // rows of a group come one after the other, but read the cosines once.  Us with one and
+    // with four, 32 + 8 heads of 128 rotated: 64 tokens 3.8 and 6.1, 512 tokens 6.2 and 7.3,
+    // 1024 tokens 11.5 and 9.8, 2048 tokens 20 and 14.6; with the cache written and read back
+    // 7.3 and 11.3, 11.0 and 13.8, 17.6 and 17.8, 29 and 25.  The rule changes at some 400 and
+    // 340 tokens, sooner than these figures ask for (up to 2.8 us at 512 tokens).
     p.each = tokens * (heads + parts * kv_heads) * p.lanes / 64 < kComputeUnits * kWavesPerUnit ? 1 : kRowsInFlight;
     p.q_chunks = static_cast<int32_t>(ceil_div(heads, p.each));
     p.k_chunks = static_cast<int32_t>(ceil_div(kv_heads, p.each));
@@ -143,9 +147,14 @@ inline int64_t read_groups(int64_t tokens, int64_t kv_heads, int64_t dp) {
 
 // ---------------------------------------------------------------- attention
 // Query rows (tokens times heads of one kv head) that a workgroup of the stream
-// kernel holds: 16, or 32 where their sums fit the registers of two waves a SIMD.
+// kernel holds: 16, or 32 where their sums fit the registers of two waves a SIMD; more
+// rows take the tile kernel (16 sequences of 32 rows of 128 on 600, 2048 and 8192 tokens:
+// 19, 26 and 39 us here, 29, 77 and 61 in tiles).
 inline int64_t stream_rows(int64_t dp) { return dp <= 128 ? 32 : 16; }
-// Steps of the cache up to which one workgroup takes a sequence and kv head alone.
+// Steps of the cache up to which one workgroup takes a sequence and kv head alone: the
+// pieces' second launch costs some 2.5 us (32 heads on 8 of 128, one sequence of 512 tokens
+// 7.4 us alone, 9.8 in pieces; 64 of them 13.4 and 19.7; one of 1024 tokens 11.2 and 9.8,
+// one of 2048 20.8 and 10; 64 of 1024 tokens 20.7 and 27, which the rule does not take).
 constexpr int64_t kWholeSteps = 8;
 
 // Workgroups of four waves that a compute unit holds: what the stream kernel's
@@ -155,7 +164,9 @@ constexpr int groups_per_unit(int64_t dp, int64_t rows) {
 }
 
 // Rows of a workgroup of the tile kernel, 32 a wave: 8 waves decode a step of the cache
-// half as often as 4, which fill the chip with half as many rows.
+// half as often as 4, which fill the chip with half as many rows (prompts of 32 heads on 8
+// of 128: 1024 tokens 46 us with 128 rows and 49 with 256, 2048 tokens 82 and 86, 3000
+// tokens 122 and 119, 4096 tokens 217 and 180; 256 from 2048 tokens on).
 constexpr int64_t kTileRows = 256, kTileRowsFew = 128;
 constexpr int64_t kMaxSplits = 64, kFewTiles = 64, kManySteps = 64;
 
@@ -202,8 +213,14 @@ inline AttnPlan plan_attn(int64_t heads, int64_t kv_heads, int64_t head_dim, int
     p.rows = rows > kTileRowsFew && bound(kTileRows) * kv_heads >= kComputeUnits ? kTileRows : kTileRowsFew;
     p.tiles = bound(p.rows);
     const int64_t items = p.tiles * kv_heads, fill = 2 * kComputeUnits * kTileRowsFew / p.rows;
-    // joining costs the more the more tiles there are (273 tiles of up to 1501 tokens: 70 us
-    // in two parts each, 45 in one)
+    // A tile's steps are shared out where tiles are few; a second launch joins the parts, which
+    // costs the more the more tiles there are.  Us in parts that fill the chip and in one, a
+    // chunk of a prompt, 32 heads on 8 of 128: 32 items 30 and 44 on 1024 tokens, 39 and 144 on
+    // 4096; 128 items 53 and 78 on 2048, 117 and 282 on 8192; 232 items 87 and 81 on 2048, 222
+    // and 283 on 8192; 384 items 95 and 82 on 2048, 578 and 685 on 16384; 291 items of ragged
+    // prompts (1501 tokens, window 500) 53 and 45 in two parts each.  The thresholds keep one
+    // part in some cases where parts would pay: 64 to 255 items of up to 64 steps (128 items on
+    // 4096 tokens 73 and 146), and from 256 items on long tables (256 on 8192: 199 and 281).
     if (steps > kWholeSteps && (items < kFewTiles || (items < kComputeUnits && steps > kManySteps))) {
         p.splits = ceil_div(fill, items);
         if (p.splits > ceil_div(steps, kWholeSteps)) p.splits = ceil_div(steps, kWholeSteps);

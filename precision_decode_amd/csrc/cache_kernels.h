@@ -5,10 +5,13 @@
 //
 // All three move bytes: a row of head_dim elements is read once and written once,
 // 16 bytes a lane.  Queries and keys of 4096 tokens normalised and rotated (64 rows of
-// 128, 136 MB): 34 us, 4.0 TB/s, against 27 at the rate of a copy; beside it 228 vector
-// instructions per 8 elements (the sum of squares, the rotation, the roundings,
-// addresses).  Keys and values of 8192 tokens, 8 heads of 128, into the cache: 20 us,
-// 204 instructions per 8 elements, and back 12.7 us.
+// 128, 136 MB): 34 - 36 us, 3.9 TB/s, against 27 at the rate of a copy; vector
+// instructions, 229 per 8 elements (the sum of squares, the rotation, the roundings,
+// addresses), are issued for 0.92 of the time.  Keys and values of 8192 tokens, 8 heads of
+// 128, into the cache: 20 us, 204 instructions per 8 elements (0.69 of the time), and back
+// 12.9 us, 140 instructions (0.78).  Scales lie [block][token], a byte each, so that a
+// token's writer stores and its reader loads single bytes of lines that other tokens'
+// workgroups use too: 16.8 MB written for 9.4, 25.8 MB read for 9.4.
 #ifndef NVFP4_CACHE_KERNELS_H
 #define NVFP4_CACHE_KERNELS_H
 
